@@ -102,7 +102,8 @@ def kernel_source_digest() -> str:
     import hashlib
     from optimizer_state_gb300 import build as libbuild
     h = hashlib.sha256()
-    for name in ("z3_kernels.cu", "z3_launch.h", "z3_internal.h", "z3_layout.cpp"):
+    for name in ("z3_kernels.cu", "z3_device.cuh", "z3_launch.h", "z3_internal.h",
+                 "z3_layout.cpp"):
         with open(os.path.join(ROOT, "optimizer_state_gb300", "csrc", name), "rb") as f:
             h.update(f.read())
     # include paths name where the repository sits, not what is compiled

@@ -27,7 +27,7 @@ CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{INCLUDE}"]
 
 SOURCES = [("z3_layout.cpp", "cxx"), ("z3_api.cpp", "cxx"), ("z3_kernels.cu", "nvcc"),
            ("z3_noalloc.cu", "nvcc")]
-HEADERS = ["z3_internal.h", "z3_launch.h"]
+HEADERS = ["z3_internal.h", "z3_launch.h", "z3_device.cuh"]
 
 
 def _nvcc() -> str:
