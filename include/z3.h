@@ -267,6 +267,110 @@ z3_status z3_model_step(const z3_unit *units, int32_t n_units, uint16_t *const *
                         int32_t n_full, const z3_adam_hp *hp, int64_t step,
                         z3_stream stream, z3_stream gather_stream);
 
+/* ---- gradient clipping by the global norm ------------------------------ */
+
+/* The global norm joins the gradients of every unit before any unit is
+ * updated, so a clipped step takes its parts in another order than
+ * z3_step_layer: first every unit's ReduceScatter, then one norm over all
+ * of them, then every unit's update.  With g all the elements of all the
+ * tensors given,
+ *   norm = sqrt(sum of g^2), rounded once to binary32;
+ *   coef = max_norm / norm where norm > max_norm, else 1 (binary32), and NaN
+ *          where norm is not finite: +Inf or NaN among the gradients, or a
+ *          norm beyond binary32.
+ * Both are left in device memory, clip[0] = norm and clip[1] = coef, and the
+ * calls that clip read coef there: no host synchronisation.  A NaN coef
+ * means that there is no step to take: those calls then write nothing, and
+ * the caller sees it in clip.  Sums of squares are held in binary64 and
+ * added in an order that the sizes, and the addresses modulo 16, fix: the
+ * same call gives the same bits.  Values whose squares leave binary32's range are
+ * summed without loss: the norm is right over the whole range of bf16 and
+ * fp32, subnormals included. */
+
+typedef enum z3_dtype {
+    Z3_BF16 = 0,  /* gradients */
+    Z3_F32 = 1,   /* gradients */
+    Z3_SUMSQ = 2  /* double: sums of squares that z3_reduce_scatter_norm left */
+} z3_dtype;
+
+/* One tensor of a list: numel contiguous elements in device memory.  data
+ * needs the alignment of its elements only (a parameter's view into a flat
+ * buffer may start anywhere); it may be NULL where numel is 0. */
+typedef struct z3_tensor {
+    void *data;
+    int64_t numel;
+    int32_t dtype; /* z3_dtype */
+    int32_t reserved;
+} z3_tensor;
+
+/* Bytes of z3_grad_norm's workspace (device memory, 16-byte aligned).  The
+ * caller fills it with zeros once; every call leaves it ready for the next.
+ * Calls that may overlap on the GPU need a workspace each. */
+z3_status z3_grad_norm_workspace_bytes(int64_t *bytes);
+
+/* The global norm of n tensors and its factor, written to clip (float [2],
+ * device).  The tensors are read; they may be of different types, may
+ * overlap and may be empty (n = 0: norm 0).  A Z3_SUMSQ tensor adds its
+ * elements as they are.  max_norm > 0; +Inf measures without clipping.
+ * Errors: n < 0, tensors NULL (n > 0), a negative numel, an unknown dtype,
+ * max_norm not > 0, clip or workspace overlapping a tensor or each other
+ * (INVALID_ARG); data not aligned to its element (ALIGNMENT); a size beyond
+ * int64 (OVERFLOW). */
+z3_status z3_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm, float *clip,
+                       void *workspace, z3_stream stream);
+
+/* Clips n tensors in place: g = coef * g in binary32, rounded once to the
+ * tensor's type.  Nothing is written where coef is 1 or NaN.  clip is read.
+ * Errors: those of z3_grad_norm, a Z3_SUMSQ tensor, and tensors that overlap
+ * one another or clip (INVALID_ARG). */
+z3_status z3_clip(const z3_tensor *tensors, int32_t n, const float *clip, z3_stream stream);
+
+/* Length (doubles) of the sumsq buffer of z3_reduce_scatter_norm. */
+z3_status z3_sumsq_len(const z3_layout *layout, int64_t *len);
+
+/* z3_reduce_scatter that also writes the sums of squares of what it stores
+ * (with accumulate: of the accumulated gradient) to sumsq (double
+ * [z3_sumsq_len], device): one per CTA, to be given to z3_grad_norm as a
+ * Z3_SUMSQ tensor.  The norm then costs no second pass over the gradient.
+ * With micro-batches, the last one's call takes this form. */
+z3_status z3_reduce_scatter_norm(const z3_layout *layout, const uint16_t *grads,
+                                 int64_t grad_stride, float *grad_shards, float scale,
+                                 int32_t accumulate, double *sumsq, z3_stream stream);
+
+/* z3_adam_shard_step with coef * g (binary32, one rounding) as its gradient;
+ * grad_shards itself stays as it is.  Where coef is 1 the results are those
+ * of z3_adam_shard_step bit for bit; where it is NaN nothing is written.
+ * clip is read. */
+z3_status z3_adam_shard_step_clipped(const z3_layout *layout, float *master, float *m, float *v,
+                                     const float *grad_shards, uint16_t *shards,
+                                     const z3_adam_hp *hp, int64_t step, const float *clip,
+                                     z3_stream stream);
+
+/* What a unit of a clipped step has beside its z3_unit: the fp32 [N][S]
+ * reduced gradient (written; with accumulate != 0 the running sums of
+ * earlier micro-batches, which this step's gradients are added to) and its
+ * sums of squares (double [z3_sumsq_len], written). */
+typedef struct z3_clip_unit {
+    float *grad_shards;
+    double *sumsq;
+    int32_t accumulate;
+    int32_t reserved;
+} z3_clip_unit;
+
+/* z3_model_step with the gradients of all units clipped by their global
+ * norm.  The gathers and their buffers are z3_model_step's; the backward
+ * pass reduces each unit's gradients into its grad_shards, and once the
+ * last unit is reduced, the norm of all of them gives coef, every unit is
+ * updated with coef times its gradient, and resident units are gathered.
+ * Where norm <= max_norm the state after the step is z3_model_step's bit for
+ * bit.  Where the norm is not finite no unit's state changes.  clips: one
+ * for each unit; clip and workspace: as for z3_grad_norm.  The buffers of clips,
+ * clip and workspace must be disjoint from every other buffer of the call. */
+z3_status z3_model_step_clipped(const z3_unit *units, const z3_clip_unit *clips, int32_t n_units,
+                                uint16_t *const *full, int32_t n_full, const z3_adam_hp *hp,
+                                int64_t step, float max_norm, float *clip, void *workspace,
+                                z3_stream stream, z3_stream gather_stream);
+
 /* ---- the layer step fed from host memory ------------------------------- */
 
 /* A pipeline that runs z3_step_layer on gradients held in host memory and

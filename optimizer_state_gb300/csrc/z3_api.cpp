@@ -1,7 +1,8 @@
 // z3_api.cpp -- the C-ABI entry points of include/z3.h: argument validation
 // on the host, NVTX ranges, and the calls into the kernel launchers
 // (z3_launch.h, z3_kernels.cu).  No device code here; the whole-model step
-// (z3_model_step) orders its launches on two streams with CUDA events.
+// (z3_model_step, z3_model_step_clipped) orders its launches on two streams
+// with CUDA events.
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -12,6 +13,7 @@
 #include <string>
 #include <vector>
 
+#include "z3_clip.h"
 #include "z3_launch.h"
 
 namespace z3 {
@@ -342,6 +344,189 @@ extern "C" z3_status z3_reshard(const z3_layout *Ls, const z3_layout *Ld, int32_
     return launched(fn, launch_reshard(Ls, Ld, elem_bytes, src, dst, (cudaStream_t)stream));
 }
 
+// --------------------------------------------------------------------------
+// gradient clipping by the global norm
+// --------------------------------------------------------------------------
+
+namespace {
+// max_norm and the two device outputs of a norm.
+z3_status check_clip_out(const char *fn, float max_norm, const float *clip,
+                         const void *workspace) {
+    if (!(max_norm > 0.0f))
+        return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": max_norm must be > 0");
+    const Buf bufs[2] = {{clip, 8, "clip"}, {workspace, sizeof(NormWorkspace), "workspace"}};
+    return check_bufs(fn, bufs, 2);
+}
+
+// Checks one unit's clipping buffers and appends its sums to the norm's list.
+z3_status check_clip_unit(const char *fn, const z3_layout *L, const z3_clip_unit &u,
+                          std::vector<z3_tensor> *sums) {
+    const int64_t len = sumsq_len(L);
+    const Buf bufs[2] = {{u.grad_shards, 4 * L->psi_padded, "grad_shards"},
+                         {u.sumsq, 8 * len, "sumsq"}};
+    const z3_status st = check_bufs(fn, bufs, 2);
+    if (st == Z3_OK && len > 0) sums->push_back({u.sumsq, len, Z3_SUMSQ, 0});
+    return st;
+}
+
+// Checks a list of tensors; with `written`, also that it holds no sums and
+// that its tensors are disjoint.  `others` are buffers that must not overlap
+// a tensor.
+z3_status check_list(const char *fn, const z3_tensor *tensors, int32_t n, const Buf *others,
+                     int n_others, bool written) {
+    const std::string name = fn;
+    auto at = [&](int32_t i) { return name + ": tensors[" + std::to_string(i) + "]"; };
+    if (n < 0) return fail(Z3_ERR_INVALID_ARG, name + ": n < 0");
+    if (n > 0 && tensors == nullptr) return fail(Z3_ERR_INVALID_ARG, name + ": tensors is NULL");
+    uintptr_t past = 0;         // the end of the tensors so far, while they ascend
+    bool ascending = true;
+    for (int32_t i = 0; i < n; ++i) {
+        const z3_tensor &t = tensors[i];
+        if (t.dtype != Z3_BF16 && t.dtype != Z3_F32 && t.dtype != Z3_SUMSQ)
+            return fail(Z3_ERR_INVALID_ARG, at(i) + ": unknown dtype");
+        if (written && t.dtype == Z3_SUMSQ)
+            return fail(Z3_ERR_INVALID_ARG, at(i) + " holds sums of squares: nothing to clip");
+        if (t.numel < 0) return fail(Z3_ERR_INVALID_ARG, at(i) + ": numel < 0");
+        if (t.numel == 0) continue;
+        if (t.data == nullptr) return fail(Z3_ERR_INVALID_ARG, at(i) + ": data is NULL");
+        const int64_t size = list_dtype_bytes(t.dtype);
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(t.data);
+        int64_t bytes;
+        uintptr_t hi;
+        if (__builtin_mul_overflow(t.numel, size, &bytes) ||
+            __builtin_add_overflow(lo, (uintptr_t)bytes, &hi) || hi > (uintptr_t)INT64_MAX >> 8)
+            return fail(Z3_ERR_OVERFLOW, at(i) + ": size overflows");
+        if (lo % (uintptr_t)size != 0)
+            return fail(Z3_ERR_ALIGNMENT, at(i) + " is not aligned to its elements");
+        for (int k = 0; k < n_others; ++k) {
+            const uintptr_t o = reinterpret_cast<uintptr_t>(others[k].ptr);
+            if (lo < o + (uintptr_t)others[k].bytes && o < hi)
+                return fail(Z3_ERR_INVALID_ARG, at(i) + " overlaps " + others[k].name);
+        }
+        ascending = ascending && lo >= past;
+        past = hi;
+    }
+    if (!written || ascending) return Z3_OK;
+    struct Extent {
+        uintptr_t lo, hi;
+        int32_t i;
+    };
+    std::vector<Extent> ext;
+    ext.reserve((size_t)n);
+    for (int32_t i = 0; i < n; ++i) {
+        if (tensors[i].numel == 0) continue;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(tensors[i].data);
+        ext.push_back({lo, lo + (uintptr_t)(tensors[i].numel * list_dtype_bytes(tensors[i].dtype)),
+                       i});
+    }
+    std::sort(ext.begin(), ext.end(), [](const Extent &a, const Extent &b) { return a.lo < b.lo; });
+    for (size_t k = 1; k < ext.size(); ++k)
+        if (ext[k].lo < ext[k - 1].hi)
+            return fail(Z3_ERR_INVALID_ARG, at(ext[k].i) + " overlaps tensors[" +
+                                                std::to_string(ext[k - 1].i) + "]");
+    return Z3_OK;
+}
+}  // namespace
+
+extern "C" z3_status z3_grad_norm_workspace_bytes(int64_t *bytes) {
+    if (bytes == nullptr)
+        return fail(Z3_ERR_INVALID_ARG, "z3_grad_norm_workspace_bytes: bytes is NULL");
+    *bytes = (int64_t)sizeof(NormWorkspace);
+    return Z3_OK;
+}
+
+extern "C" z3_status z3_sumsq_len(const z3_layout *L, int64_t *len) {
+    if (L == nullptr) return fail(Z3_ERR_INVALID_ARG, "z3_sumsq_len: layout is NULL");
+    if (len == nullptr) return fail(Z3_ERR_INVALID_ARG, "z3_sumsq_len: len is NULL");
+    *len = sumsq_len(L);
+    return Z3_OK;
+}
+
+extern "C" z3_status z3_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm,
+                                  float *clip, void *workspace, z3_stream stream) {
+    const char *fn = "z3_grad_norm";
+    try {
+        z3_status st = check_clip_out(fn, max_norm, clip, workspace);
+        if (st != Z3_OK) return st;
+        const Buf others[2] = {{clip, 8, "clip"},
+                               {workspace, sizeof(NormWorkspace), "workspace"}};
+        st = check_list(fn, tensors, n, others, 2, false);
+        if (st != Z3_OK) return st;
+        Range range("z3/grad_norm");
+        return launched(fn, launch_grad_norm(tensors, n, max_norm, clip,
+                                             (NormWorkspace *)workspace, (cudaStream_t)stream));
+    } catch (const std::bad_alloc &) {
+        return fail_host_memory(fn);
+    }
+}
+
+extern "C" z3_status z3_clip(const z3_tensor *tensors, int32_t n, const float *clip,
+                             z3_stream stream) {
+    const char *fn = "z3_clip";
+    try {
+        const Buf others[1] = {{clip, 8, "clip"}};
+        z3_status st = check_bufs(fn, others, 1);
+        if (st != Z3_OK) return st;
+        st = check_list(fn, tensors, n, others, 1, true);
+        if (st != Z3_OK) return st;
+        Range range("z3/clip");
+        return launched(fn, launch_clip(tensors, n, clip, (cudaStream_t)stream));
+    } catch (const std::bad_alloc &) {
+        return fail_host_memory(fn);
+    }
+}
+
+extern "C" z3_status z3_reduce_scatter_norm(const z3_layout *L, const uint16_t *grads,
+                                            int64_t grad_stride, float *grad_shards, float scale,
+                                            int32_t accumulate, double *sumsq, z3_stream stream) {
+    const char *fn = "z3_reduce_scatter_norm";
+    if (L == nullptr) return fail(Z3_ERR_INVALID_ARG, "z3_reduce_scatter_norm: layout is NULL");
+    if (!std::isfinite(scale)) return fail(Z3_ERR_INVALID_ARG, "z3_reduce_scatter_norm: scale");
+    int64_t gbytes;
+    z3_status st = check_grads(fn, L, grad_stride, &gbytes);
+    if (st != Z3_OK) return st;
+    const Buf bufs[3] = {{grads, L->psi ? gbytes : 0, "grads"},
+                         {grad_shards, 4 * L->psi_padded, "grad_shards"},
+                         {sumsq, 8 * sumsq_len(L), "sumsq"}};
+    st = check_bufs(fn, bufs, 3);
+    if (st != Z3_OK) return st;
+    if (L->psi_padded == 0) return Z3_OK;
+    const ReduceNormArgs a{grads, grad_stride, scale, grad_shards, sumsq};
+    Range range(accumulate ? "z3/ReduceScatter+acc+norm" : "z3/ReduceScatter+norm");
+    return launched(fn, launch_reduce_norm(L, a, accumulate != 0, (cudaStream_t)stream, false));
+}
+
+extern "C" z3_status z3_adam_shard_step_clipped(const z3_layout *L, float *master, float *m,
+                                                float *v, const float *grad_shards,
+                                                uint16_t *shards, const z3_adam_hp *hp,
+                                                int64_t step, const float *clip,
+                                                z3_stream stream) {
+    const char *fn = "z3_adam_shard_step_clipped";
+    if (L == nullptr) return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": layout is NULL");
+    AdamClipArgs c{};
+    AdamArgs &a = c.a;
+    z3_status st = adam_constants(fn, hp, step, &a.k);
+    if (st != Z3_OK) return st;
+    const int64_t T = L->psi_padded;
+    const Buf bufs[6] = {{master, 4 * T, "master"}, {m, 4 * T, "m"}, {v, 4 * T, "v"},
+                         {grad_shards, 4 * T, "grad_shards"}, {shards, 2 * T, "shards"},
+                         {clip, 8, "clip"}};
+    st = check_bufs(fn, bufs, 6);
+    if (st != Z3_OK) return st;
+    if (T == 0) return Z3_OK;
+    a.master = master;
+    a.m = m;
+    a.v = v;
+    a.grad = grad_shards;
+    a.shards = shards;
+    a.total = T;
+    c.clip = clip;
+    if (flat_blocks(T, kAdamThreads) > 0x7fffffff)
+        return fail(Z3_ERR_OVERFLOW, std::string(fn) + ": grid too large");
+    Range range("z3/Adam(clipped)");
+    return launched(fn, launch_adam_clipped(c, (cudaStream_t)stream, false));
+}
+
 namespace {
 // Events used by one prefetching model step; destroyed when the step has
 // been enqueued (the runtime releases them once their work completes).
@@ -363,39 +548,58 @@ struct Events {
 }  // namespace
 
 namespace {
-// The body of z3_model_step.  Every host allocation happens before the
-// first launch, so a std::bad_alloc (thrown out of here) leaves nothing
-// enqueued.
-z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *full,
-                     int32_t n_full, const z3_adam_hp *hp, int64_t step, z3_stream stream,
-                     z3_stream gather_stream) {
-    const char *fn = "z3_model_step";
-    if (units == nullptr || n_units < 1)
-        return fail(Z3_ERR_INVALID_ARG, "z3_model_step: no units");
+// What a clipped step has beside the plain one's arguments.
+struct ClipStep {
+    const z3_clip_unit *units;
+    float max_norm;
+    float *clip;
+    void *workspace;
+};
+
+// The body of z3_model_step (c NULL) and z3_model_step_clipped.  Every host
+// allocation happens before the first launch, so a std::bad_alloc (thrown out
+// of here) leaves nothing enqueued.
+z3_status model_step(const char *fn, const z3_unit *units, int32_t n_units,
+                     uint16_t *const *full, int32_t n_full, const z3_adam_hp *hp, int64_t step,
+                     z3_stream stream, z3_stream gather_stream, const ClipStep *c) {
+    const std::string name = fn;
+    if (units == nullptr || n_units < 1) return fail(Z3_ERR_INVALID_ARG, name + ": no units");
     if (full == nullptr || n_full < 1 || n_full > 8)
-        return fail(Z3_ERR_INVALID_ARG, "z3_model_step: n_full must be 1..8");
+        return fail(Z3_ERR_INVALID_ARG, name + ": n_full must be 1..8");
     if (n_full >= 2 && (gather_stream == nullptr || gather_stream == stream))
         return fail(Z3_ERR_INVALID_ARG,
-                    "z3_model_step: prefetch needs a gather stream distinct from stream");
+                    name + ": prefetch needs a gather stream distinct from stream");
+    if (c != nullptr) {
+        if (c->units == nullptr) return fail(Z3_ERR_INVALID_ARG, name + ": clips is NULL");
+        z3_status st = check_clip_out(fn, c->max_norm, c->clip, c->workspace);
+        if (st != Z3_OK) return st;
+    }
     // the transient buffers hold the largest unit that is gathered through them
     int64_t full_bytes = 0;
     for (int32_t i = 0; i < n_units; ++i) {
-        if (units[i].layout == nullptr) return fail(Z3_ERR_INVALID_ARG, "z3_model_step: layout is NULL");
+        if (units[i].layout == nullptr) return fail(Z3_ERR_INVALID_ARG, name + ": layout is NULL");
         if (units[i].resident == nullptr) full_bytes = std::max(full_bytes, 2 * units[i].layout->psi);
     }
     std::vector<ReduceArgs> args((size_t)n_units);
     std::vector<int64_t> grad_bytes((size_t)n_units, 0);
+    std::vector<z3_tensor> sums;   // every unit's sums of squares: the norm's list
+    if (c != nullptr) sums.reserve((size_t)n_units);
     for (int32_t i = 0; i < n_units; ++i) {
         const z3_unit &u = units[i];
         z3_status st = prepare_rs_adam(fn, u.layout, u.grads, u.grad_stride, u.scale, nullptr,
                                        u.master, u.m, u.v, u.shards, u.resident,
-                                       u.hp != nullptr ? u.hp : hp, step, &args[i], "resident");
+                                       u.hp != nullptr ? u.hp : hp, step, &args[i], "resident",
+                                       c != nullptr ? c->units[i].grad_shards : nullptr);
         if (st != Z3_OK) return st;
         const int64_t T = u.layout->psi_padded;
         int64_t gbytes = 0;
         st = check_grads(fn, u.layout, u.grad_stride, &gbytes);
         if (st != Z3_OK) return st;
         grad_bytes[(size_t)i] = u.layout->psi ? gbytes : 0;
+        if (c != nullptr) {
+            st = check_clip_unit(fn, u.layout, c->units[i], &sums);
+            if (st != Z3_OK) return st;
+        }
         for (int32_t k = 0; k < n_full; ++k) {
             const Buf bufs[7] = {{full[k], full_bytes, "full[k]"},
                                  {u.resident, u.resident ? 2 * u.layout->psi : 0, "resident"},
@@ -424,13 +628,13 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
     {
         struct Span {
             uintptr_t lo, hi;
-            int32_t unit;
+            int64_t unit;
             bool written;
             const char *name;
         };
         std::vector<Span> spans;
-        spans.reserve((size_t)n_units * 6);
-        auto add = [&](const void *p, int64_t bytes, int32_t unit, bool written,
+        spans.reserve((size_t)n_units * 8 + 2 + (size_t)n_full);
+        auto add = [&](const void *p, int64_t bytes, int64_t unit, bool written,
                        const char *name) {
             if (bytes <= 0) return;
             const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
@@ -445,7 +649,23 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
             add(u.v, 4 * T, i, true, "v");
             add(u.resident, u.resident ? 2 * u.layout->psi : 0, i, true, "resident copy");
             add(u.grads, grad_bytes[(size_t)i], i, false, "grads");
+            if (c == nullptr) continue;
+            // owners of their own: disjoint from the unit's other buffers too
+            const z3_clip_unit &cu = c->units[i];
+            add(cu.grad_shards, 4 * T, n_units + i, true, "grad_shards");
+            add(cu.sumsq, 8 * sumsq_len(u.layout), 2 * n_units + i, true, "sumsq");
         }
+        if (c != nullptr) {
+            add(c->clip, 8, 3 * n_units, true, "clip");
+            add(c->workspace, sizeof(NormWorkspace), 3 * n_units + 1, true, "workspace");
+            for (int32_t k = 0; k < n_full; ++k)
+                add(full[k], full_bytes, 3 * n_units + 2 + k, true, "full[k]");
+        }
+        auto span_name = [&](const Span &a) {
+            return a.unit < 3 * (int64_t)n_units
+                       ? "unit " + std::to_string(a.unit % n_units) + "'s " + a.name
+                       : std::string(a.name);
+        };
         std::sort(spans.begin(), spans.end(),
                   [](const Span &a, const Span &b) { return a.lo < b.lo; });
         std::vector<const Span *> open;   // spans that may still overlap the next one
@@ -454,11 +674,15 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
             for (const Span *y : open) {
                 if (y->hi <= x.lo) continue;  // ended before x starts
                 open[keep++] = y;
-                if (y->unit != x.unit && (y->written || x.written))
+                if (y->unit != x.unit && (y->written || x.written)) {
+                    if (y->unit >= n_units || x.unit >= n_units)
+                        return fail(Z3_ERR_INVALID_ARG, name + ": " + span_name(*y) +
+                                                            " overlaps " + span_name(x));
                     return fail(Z3_ERR_INVALID_ARG,
                                 std::string(fn) + ": unit " + std::to_string(y->unit) + "'s " +
                                     y->name + " overlaps another unit's (" +
                                     std::to_string(x.unit) + ") " + x.name);
+                }
             }
             open.resize(keep);
             open.push_back(&x);
@@ -469,7 +693,7 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
     std::vector<bool> buffer_used((size_t)nb, false);
     Events E;
     E.ev.reserve((size_t)(2 + 2 * nb));
-    Range range("z3/model_step");
+    Range range(c != nullptr ? "z3/model_step(clipped)" : "z3/model_step");
     z3_status st = Z3_OK;
     // whether this call has enqueued a kernel on s (on g) yet: a launch may
     // read early only after one of its own
@@ -480,6 +704,15 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
     auto update = [&](int32_t i) -> z3_status {
         const z3_layout *L = units[i].layout;
         if (L->psi_padded == 0) return Z3_OK;
+        if (c != nullptr) {   // no update before the norm of every unit
+            Range r("z3/ReduceScatter+norm");
+            const z3_clip_unit &cu = c->units[i];
+            const ReduceNormArgs a{units[i].grads, units[i].grad_stride, units[i].scale,
+                                   cu.grad_shards, cu.sumsq};
+            const bool early = ours_s;
+            ours_s = true;
+            return launched(fn, launch_reduce_norm(L, a, cu.accumulate != 0, s, early));
+        }
         z3_status us;
         {
             Range r("z3/ReduceScatter+Adam");
@@ -489,6 +722,40 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
         if (us != Z3_OK || units[i].resident == nullptr || L->psi == 0) return us;
         Range r("z3/AllGather(resident)");
         return run_allgather(L, units[i].shards, units[i].resident, s, false);
+    };
+    // The rest of a clipped step, once every unit is reduced: the norm, every
+    // unit's update, and the resident units' gathers.  Units go in forward
+    // order, the reverse of the backward pass: the gradients reduced last are
+    // still in L2.  The first update reads what the norm kernel before it
+    // writes; a later one follows an update of another unit (or its resident
+    // gather), which writes nothing that it reads.
+    auto finish = [&]() -> z3_status {
+        if (c == nullptr) return Z3_OK;
+        {
+            Range r("z3/grad_norm");
+            z3_status fs = launched(fn, launch_grad_norm(sums.data(), (int32_t)sums.size(),
+                                                         c->max_norm, c->clip,
+                                                         (NormWorkspace *)c->workspace, s));
+            if (fs != Z3_OK) return fs;
+        }
+        bool early = false;
+        for (int32_t i = 0; i < n_units; ++i) {
+            const z3_unit &u = units[i];
+            const int64_t T = u.layout->psi_padded;
+            if (T == 0) continue;
+            Range r("z3/Adam(clipped)");
+            const AdamClipArgs a{{u.master, u.m, u.v, c->units[i].grad_shards, u.shards, T,
+                                  args[(size_t)i].k},
+                                 c->clip};
+            z3_status fs = launched(fn, launch_adam_clipped(a, s, early));
+            if (fs != Z3_OK) return fs;
+            early = true;
+            if (u.resident == nullptr) continue;
+            Range r2("z3/AllGather(resident)");
+            fs = run_allgather(u.layout, u.shards, u.resident, s, false);
+            if (fs != Z3_OK) return fs;
+        }
+        return Z3_OK;
     };
     if (n_full == 1) {
         for (int32_t i = 0; i < n_units && st == Z3_OK; ++i) {
@@ -507,7 +774,7 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
             }
             if (st == Z3_OK) st = update(i);
         }
-        return st;
+        return st == Z3_OK ? finish() : st;
     }
     // Prefetch depth D = n_full - 1: the gathers run on gather_stream up to
     // D units ahead of the updates, unit i in buffer i mod n_full.  A gather
@@ -563,7 +830,7 @@ z3_status model_step(const z3_unit *units, int32_t n_units, uint16_t *const *ful
     if (st != Z3_OK) return st;
     if ((err = cudaEventRecord(E.ev[1], g)) != cudaSuccess) return cuda_fail(err);
     if ((err = cudaStreamWaitEvent(s, E.ev[1], 0)) != cudaSuccess) return cuda_fail(err);
-    return Z3_OK;
+    return finish();
 }
 }  // namespace
 
@@ -571,9 +838,24 @@ extern "C" z3_status z3_model_step(const z3_unit *units, int32_t n_units, uint16
                                    int32_t n_full, const z3_adam_hp *hp, int64_t step,
                                    z3_stream stream, z3_stream gather_stream) {
     try {
-        return model_step(units, n_units, full, n_full, hp, step, stream, gather_stream);
+        return model_step("z3_model_step", units, n_units, full, n_full, hp, step, stream,
+                          gather_stream, nullptr);
     } catch (const std::bad_alloc &) {
         return fail_host_memory("z3_model_step");
+    }
+}
+
+extern "C" z3_status z3_model_step_clipped(const z3_unit *units, const z3_clip_unit *clips,
+                                           int32_t n_units, uint16_t *const *full, int32_t n_full,
+                                           const z3_adam_hp *hp, int64_t step, float max_norm,
+                                           float *clip, void *workspace, z3_stream stream,
+                                           z3_stream gather_stream) {
+    const char *fn = "z3_model_step_clipped";
+    try {
+        const ClipStep c{clips, max_norm, clip, workspace};
+        return model_step(fn, units, n_units, full, n_full, hp, step, stream, gather_stream, &c);
+    } catch (const std::bad_alloc &) {
+        return fail_host_memory(fn);
     }
 }
 

@@ -80,6 +80,8 @@ class Model:
         self.full = torch.empty(max([u.L.psi for u in units if u.resident is None] or [1]),
                                 dtype=torch.bfloat16, device=dev)
         self.t = 0
+        self.clip = None                # [norm, coef] of the last clipped step
+        self._clip_args = None
 
     @property
     def psi(self) -> int:
@@ -100,6 +102,26 @@ class Model:
         return [(u.L, u.shards, u.master, u.m, u.v, u.grads, u.w.grad_stride,
                  1.0 / u.w.n_ranks, u.resident, u.hp) for u in self.units]
 
+    def clip_args(self):
+        """What a clipped step keeps beside the units' state: each unit's
+        reduced fp32 gradient and its sums of squares, the norm's workspace
+        and [norm, coef].  Allocated by the first clipped step."""
+        if self._clip_args is None:
+            self._clip_args = [(torch.zeros(u.L.psi_padded, dtype=torch.float32, device=self.dev),
+                                torch.zeros(u.L.sumsq_len, dtype=torch.float64, device=self.dev))
+                               for u in self.units]
+            self._workspace = z3.grad_norm_workspace(self.dev)
+            self.clip = torch.zeros(2, dtype=torch.float32, device=self.dev)
+        return self._clip_args
+
+    def _clipped_step(self, full, hp: dict, t: int, max_norm: float, stream, gather_stream,
+                      on_gather):
+        if on_gather is not None:
+            raise NotImplementedError("the call-by-call schedule does not clip")
+        z3.z3_model_step_clipped(self.unit_args(), self.clip_args(), full, hp, t, max_norm,
+                                 self.clip, self._workspace, stream=stream,
+                                 gather_stream=gather_stream)
+
     @staticmethod
     def _update(u: Unit, hp: dict, t: int, stream):
         z3.z3_reduce_scatter_adam(u.L, u.grads, u.w.grad_stride, 1.0 / u.w.n_ranks, None,
@@ -107,8 +129,13 @@ class Model:
         if u.resident is not None:
             z3.z3_allgather(u.L, u.shards, u.resident, stream=stream)
 
-    def step(self, hp: dict, stream=None, t: int | None = None, on_gather=None):
+    def step(self, hp: dict, stream=None, t: int | None = None, on_gather=None,
+             max_norm: float | None = None):
         """One training step, scheduled by the library (z3_model_step).
+        With `max_norm` the gradients of all units are clipped to that global
+        norm first (z3_model_step_clipped); `clip` then holds [norm, coef] on
+        the device, coef NaN where the norm was not finite and the step was
+        left out.  That takes 4 more bytes per element (the fp32 gradients).
         With `on_gather(phase, index)` the same schedule is issued call by
         call from here instead, and the hook is called after each gather is
         enqueued, with the transient buffer holding that unit's parameters
@@ -117,6 +144,9 @@ class Model:
         if t is None:
             self.t += 1
             t = self.t
+        if max_norm is not None:
+            self._clipped_step([self.full], hp, t, max_norm, stream, None, on_gather)
+            return
         if on_gather is None:
             z3.z3_model_step(self.unit_args(), [self.full], hp, t, stream=stream)
             return
@@ -164,10 +194,14 @@ class PrefetchModel(Model):
         self.bufs = [self.full] + [torch.empty_like(self.full) for _ in range(depth)]
         self.gstream = torch.cuda.Stream(device=dev)
 
-    def step(self, hp: dict, stream=None, t: int | None = None, on_gather=None):
+    def step(self, hp: dict, stream=None, t: int | None = None, on_gather=None,
+             max_norm: float | None = None):
         if t is None:
             self.t += 1
             t = self.t
+        if max_norm is not None:
+            self._clipped_step(self.bufs, hp, t, max_norm, stream, self.gstream, on_gather)
+            return
         if on_gather is None:
             z3.z3_model_step(self.unit_args(), self.bufs, hp, t, stream=stream,
                              gather_stream=self.gstream)

@@ -28,7 +28,12 @@ EXPORTS = ("z3_layout_create", "z3_layout_destroy", "z3_layout_info", "z3_layout
            "z3_adam_shard_step", "z3_reduce_scatter_adam", "z3_step_layer",
            "z3_allreduce", "z3_scatter", "z3_reshard", "z3_model_step",
            "z3_host_step_create", "z3_host_step_run", "z3_host_step_destroy",
-           "z3_step_layer_noalloc", "z3_status_string", "z3_last_error")
+           "z3_step_layer_noalloc", "z3_grad_norm_workspace_bytes", "z3_grad_norm", "z3_clip",
+           "z3_sumsq_len", "z3_reduce_scatter_norm", "z3_adam_shard_step_clipped",
+           "z3_model_step_clipped", "z3_status_string", "z3_last_error")
+
+# enum z3_dtype
+Z3_BF16, Z3_F32, Z3_SUMSQ = range(3)
 
 
 class Z3Error(RuntimeError):
@@ -50,6 +55,18 @@ class Unit(ctypes.Structure):
                 ("grads", ctypes.c_void_p), ("grad_stride", ctypes.c_int64),
                 ("scale", ctypes.c_float), ("resident", ctypes.c_void_p),
                 ("hp", ctypes.POINTER(AdamHP))]
+
+
+class Tensor(ctypes.Structure):
+    """struct z3_tensor."""
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ClipUnit(ctypes.Structure):
+    """struct z3_clip_unit."""
+    _fields_ = [("grad_shards", ctypes.c_void_p), ("sumsq", ctypes.c_void_p),
+                ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class Traffic(ctypes.Structure):
@@ -102,6 +119,14 @@ def load():
             "z3_host_step_run": (st, [vp, vp, vp, vp, f32, vp, vp, vp, hp, i64, vp, vp]),
             "z3_host_step_destroy": (None, [vp]),
             "z3_step_layer_noalloc": (st, [vp, vp, vp, i64, f32, vp, vp, vp, hp, i64, vp]),
+            "z3_grad_norm_workspace_bytes": (st, [ctypes.POINTER(i64)]),
+            "z3_grad_norm": (st, [vp, i32, f32, vp, vp, vp]),
+            "z3_clip": (st, [vp, i32, vp, vp]),
+            "z3_sumsq_len": (st, [vp, ctypes.POINTER(i64)]),
+            "z3_reduce_scatter_norm": (st, [vp, vp, i64, vp, f32, i32, vp, vp]),
+            "z3_adam_shard_step_clipped": (st, [vp, vp, vp, vp, vp, vp, hp, i64, vp, vp]),
+            "z3_model_step_clipped": (st, [ctypes.POINTER(Unit), ctypes.POINTER(ClipUnit), i32,
+                                           ctypes.POINTER(vp), i32, hp, i64, f32, vp, vp, vp, vp]),
             "z3_status_string": (ctypes.c_char_p, [st]),
             "z3_last_error": (ctypes.c_size_t, [ctypes.c_char_p, ctypes.c_size_t]),
         }
@@ -190,6 +215,9 @@ class Layout:
         arrs = [(ctypes.c_int64 * self.n_params)() for _ in range(4)]
         _check(lib.z3_layout_params(h, *[ctypes.cast(a, ctypes.c_void_p) for a in arrs]))
         self.numel, self.shard_numel, self.shard_off, self.full_off = (list(a) for a in arrs)
+        n = ctypes.c_int64()
+        _check(lib.z3_sumsq_len(h, ctypes.byref(n)))
+        self.sumsq_len = n.value        # doubles of z3_reduce_scatter_norm's sumsq
 
     @property
     def handle(self):
@@ -326,6 +354,15 @@ def z3_model_step(units, full, hp, step: int, stream=None, gather_stream=None):
     step's hyperparameters, else this unit's own; full: one transient buffer,
     or D + 1 of them for the prefetching schedule (then gather_stream is
     required)."""
+    arr, fulls, _keep = _unit_args(units, full)
+    h = _hp(hp)
+    _check(load().z3_model_step(arr, len(units), fulls, len(full), ctypes.byref(h), step,
+                                _stream(stream),
+                                None if gather_stream is None else _stream(gather_stream)))
+
+
+def _unit_args(units, full):
+    """z3_model_step's unit array and transient buffers, and what they point to."""
     b16, f32 = _dtypes()
     arr = (Unit * len(units))()
     own_hp = []                     # kept alive until the call returns
@@ -346,10 +383,115 @@ def z3_model_step(units, full, hp, step: int, stream=None, gather_stream=None):
         if res is None:
             need = max(need, L.psi)
     fulls = (ctypes.c_void_p * len(full))(*[_dev(f, b16, need, "full") for f in full])
+    return arr, fulls, own_hp
+
+
+# ---------------------------------------------------------------------------
+# gradient clipping by the global norm
+# ---------------------------------------------------------------------------
+
+class TensorList:
+    """A list of tensors for z3_grad_norm and z3_clip, laid out once and kept
+    alive: bf16 or fp32 CUDA tensors of any lengths (contiguous; views into
+    flat buffers may start at any element), and `sumsq`, fp64 tensors that
+    z3_reduce_scatter_norm wrote."""
+
+    def __init__(self, tensors, sumsq=()):
+        import torch
+        b16, f32 = _dtypes()
+        tensors, sumsq = list(tensors), list(sumsq)
+        self._keep = tensors + sumsq
+        self.n = len(self._keep)
+        self.array = (Tensor * self.n)()
+        for i, t in enumerate(tensors):
+            ptr = _dev(t, b16 + f32, 0, f"tensors[{i}]")
+            self.array[i] = Tensor(ptr, t.numel(), Z3_F32 if t.dtype in f32 else Z3_BF16, 0)
+        for i, t in enumerate(sumsq):
+            ptr = _dev(t, (torch.float64,), 0, f"sumsq[{i}]")
+            self.array[len(tensors) + i] = Tensor(ptr, t.numel(), Z3_SUMSQ, 0)
+
+    def __len__(self):
+        return self.n
+
+
+def grad_norm_workspace(device=None):
+    """A zero-filled workspace for z3_grad_norm and z3_model_step_clipped."""
+    import torch
+    n = ctypes.c_int64()
+    _check(load().z3_grad_norm_workspace_bytes(ctypes.byref(n)))
+    return torch.zeros(n.value, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def _workspace(t):
+    import torch
+    n = ctypes.c_int64()
+    _check(load().z3_grad_norm_workspace_bytes(ctypes.byref(n)))
+    return _dev(t, (torch.uint8,), n.value, "workspace")
+
+
+def z3_grad_norm(tensors, max_norm: float, clip, workspace, stream=None):
+    """tensors: a TensorList, or a sequence of tensors to make one of; clip:
+    fp32 [2], receives {norm, coef}; workspace: grad_norm_workspace()."""
+    _, f32 = _dtypes()
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors)
+    _check(load().z3_grad_norm(tensors.array, tensors.n, max_norm, _dev(clip, f32, 2, "clip"),
+                               _workspace(workspace), _stream(stream)))
+
+
+def z3_clip(tensors, clip, stream=None):
+    """Scales the tensors in place by the coef that z3_grad_norm left in clip."""
+    _, f32 = _dtypes()
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors)
+    _check(load().z3_clip(tensors.array, tensors.n, _dev(clip, f32, 2, "clip"),
+                          _stream(stream)))
+
+
+def z3_reduce_scatter_norm(layout: Layout, grads, grad_stride: int, grad_shards, scale: float,
+                           sumsq, accumulate: bool = False, stream=None):
+    """sumsq: fp64 [layout.sumsq_len], for TensorList(..., sumsq=[...])."""
+    import torch
+    b16, f32 = _dtypes()
+    _check(load().z3_reduce_scatter_norm(
+        layout.handle, _dev(grads, b16, layout.n_ranks * grad_stride, "grads"), grad_stride,
+        _dev(grad_shards, f32, layout.psi_padded, "grad_shards"), scale, 1 if accumulate else 0,
+        _dev(sumsq, (torch.float64,), layout.sumsq_len, "sumsq"), _stream(stream)))
+
+
+def z3_adam_shard_step_clipped(layout: Layout, master, m, v, grad_shards, shards, hp, step: int,
+                               clip, stream=None):
+    b16, f32 = _dtypes()
+    T = layout.psi_padded
     h = _hp(hp)
-    _check(load().z3_model_step(arr, len(units), fulls, len(full), ctypes.byref(h), step,
-                                _stream(stream),
-                                None if gather_stream is None else _stream(gather_stream)))
+    _check(load().z3_adam_shard_step_clipped(
+        layout.handle, _dev(master, f32, T, "master"), _dev(m, f32, T, "m"),
+        _dev(v, f32, T, "v"), _dev(grad_shards, f32, T, "grad_shards"),
+        _dev(shards, b16, T, "shards"), ctypes.byref(h), step, _dev(clip, f32, 2, "clip"),
+        _stream(stream)))
+
+
+def z3_model_step_clipped(units, clips, full, hp, step: int, max_norm: float, clip, workspace,
+                          stream=None, gather_stream=None):
+    """z3_model_step with the gradients clipped by their global norm.  units,
+    full and gather_stream as there; clips: for each unit (grad_shards, sumsq[,
+    accumulate]); clip and workspace as for z3_grad_norm."""
+    import torch
+    _, f32 = _dtypes()
+    if len(clips) != len(units):
+        raise ValueError(f"clips: {len(clips)} for {len(units)} units")
+    arr, fulls, _keep = _unit_args(units, full)
+    carr = (ClipUnit * len(units))()
+    for i, (u, c) in enumerate(zip(units, clips)):
+        L = u[0]
+        carr[i] = ClipUnit(_dev(c[0], f32, L.psi_padded, "grad_shards"),
+                           _dev(c[1], (torch.float64,), L.sumsq_len, "sumsq"),
+                           1 if len(c) > 2 and c[2] else 0, 0)
+    h = _hp(hp)
+    _check(load().z3_model_step_clipped(
+        arr, carr, len(units), fulls, len(full), ctypes.byref(h), step, max_norm,
+        _dev(clip, f32, 2, "clip"), _workspace(workspace), _stream(stream),
+        None if gather_stream is None else _stream(gather_stream)))
 
 
 def _host(t, dtypes, numel: int, name: str):

@@ -1,0 +1,208 @@
+"""Gradient clipping on the CPU: what the entry points refuse, with the status
+and the words of each refusal, and the lengths that they tell.  Made-up device
+addresses are only used in a child process that sees no device."""
+import ctypes
+import math
+
+import pytest
+
+from optimizer_state_gb300 import build as z3build
+from optimizer_state_gb300 import z3
+
+A = 1 << 32                       # an aligned made-up address
+
+
+@pytest.fixture(scope="module")
+def lib():
+    z3build.build()
+    return z3.load()
+
+
+def tensors(*ts):
+    arr = (z3.Tensor * len(ts))(*[z3.Tensor(*t, 0) for t in ts])
+    return arr, len(ts)
+
+
+def test_sumsq_len_counts_the_reduce_tiles(lib):
+    # one sum per CTA: 128 vectors of 8 elements of one (parameter, rank) slice
+    assert z3.Layout([1024 * 8], 8).sumsq_len == 8
+    assert z3.Layout([1024 * 8 * 2, 64], 8).sumsq_len == 8 * 2 + 8
+    # S = 2049: a slice that starts inside a vector touches 257 of them
+    assert z3.Layout([1024 * 8 * 2, 8], 8).sumsq_len == 8 * 3 + 8
+    assert z3.Layout([0, 0], 4).sumsq_len == 0
+    assert z3.Layout([64] * 41, 8).sumsq_len == 41 * 8      # two launch tables
+    n = ctypes.c_int64()
+    assert lib.z3_sumsq_len(None, ctypes.byref(n)) == z3.Z3_ERR_INVALID_ARG
+    assert lib.z3_sumsq_len(z3.Layout([5], 1).handle, None) == z3.Z3_ERR_INVALID_ARG
+    assert lib.z3_grad_norm_workspace_bytes(None) == z3.Z3_ERR_INVALID_ARG
+
+
+@pytest.mark.no_device
+def test_grad_norm_and_clip_refusals(lib):
+    clip, ws = A, A + (1 << 20)
+    d = A + (1 << 30)
+
+    def norm(ts, n=None, max_norm=1.0, clip=clip, ws=ws):
+        arr, k = ts if isinstance(ts, tuple) and isinstance(ts[0], ctypes.Array) else tensors(*ts)
+        return lib.z3_grad_norm(arr, k if n is None else n, max_norm, clip, ws, None), \
+            z3.last_error()
+
+    def scale(ts, n=None, clip=clip):
+        arr, k = tensors(*ts)
+        return lib.z3_clip(arr, k if n is None else n, clip, None), z3.last_error()
+
+    ok = (d, 100, z3.Z3_F32)
+    inv, ali, ovf = z3.Z3_ERR_INVALID_ARG, z3.Z3_ERR_ALIGNMENT, z3.Z3_ERR_OVERFLOW
+    for bad in (0.0, -1.0, math.nan, -math.inf):
+        s, msg = norm([ok], max_norm=bad)
+        assert s == inv and "max_norm" in msg, bad
+    for call in (norm, scale):
+        s, msg = call([ok], n=-1)
+        assert s == inv and "n < 0" in msg
+        s, msg = call([(d, 100, 3)])
+        assert s == inv and "tensors[0]" in msg and "dtype" in msg
+        s, msg = call([ok, (d, -1, z3.Z3_F32)])
+        assert s == inv and "tensors[1]" in msg and "numel" in msg
+        s, msg = call([(None, 1, z3.Z3_F32)])
+        assert s == inv and "NULL" in msg
+        s, msg = call([(d + 2, 1, z3.Z3_F32)])
+        assert s == ali
+        s, msg = call([(d + 1, 1, z3.Z3_BF16)])
+        assert s == ali
+        s, msg = call([(d, 1 << 62, z3.Z3_F32)])
+        assert s == ovf
+        s, msg = call([(d, 1 << 60, z3.Z3_F32)])       # the end wraps past any address
+        assert s == ovf
+        s, msg = call([ok], clip=None)
+        assert s == inv and "clip" in msg
+        s, msg = call([ok], clip=clip + 4)
+        assert s == ali and "clip" in msg
+        s, msg = call([(clip + 4, 1, z3.Z3_F32)])
+        assert s == inv and "overlaps clip" in msg
+    s, msg = norm([(d + 4, 1, z3.Z3_SUMSQ)])
+    assert s == ali
+    s, msg = norm([ok], ws=None)
+    assert s == inv and "workspace" in msg
+    s, msg = norm([ok], ws=clip)
+    assert s == inv and "overlaps" in msg
+    s, msg = norm([(ws + 16, 1, z3.Z3_BF16)])
+    assert s == inv and "overlaps workspace" in msg
+    assert lib.z3_grad_norm(None, 1, 1.0, clip, ws, None) == inv
+    assert lib.z3_clip(None, 1, clip, None) == inv
+    s, msg = scale([ok, (d, 8, z3.Z3_SUMSQ)])
+    assert s == inv and "sums of squares" in msg
+    # overlapping tensors, in ascending and in other orders
+    s, msg = scale([ok, (d + 396, 4, z3.Z3_F32)])
+    assert s == inv and "tensors[1] overlaps tensors[0]" in msg
+    s, msg = scale([(d + 396, 4, z3.Z3_F32), ok])
+    assert s == inv and "overlaps" in msg
+    s, msg = scale([(d + 4096, 4, z3.Z3_F32), ok, (d + 398, 1, z3.Z3_BF16)])
+    assert s == inv and "tensors[2] overlaps tensors[1]" in msg
+    # what is right gets as far as the launch, which finds no device
+    assert norm([ok, ok, (None, 0, z3.Z3_F32), (d + 2, 1, z3.Z3_BF16)])[0] == z3.Z3_ERR_CUDA
+    assert scale([(d + 400, 4, z3.Z3_F32), ok])[0] == z3.Z3_ERR_CUDA
+
+
+@pytest.mark.no_device
+def test_reduce_scatter_norm_and_clipped_adam_refusals(lib):
+    L = z3.Layout([35, 13, 12], 4)
+    far = A + (1 << 28)
+    inv, ali = z3.Z3_ERR_INVALID_ARG, z3.Z3_ERR_ALIGNMENT
+
+    def st(s):
+        return s, z3.last_error()
+
+    sq = far + (1 << 20)
+    assert lib.z3_reduce_scatter_norm(None, A, 64, far, 0.25, 0, sq, None) == inv
+    s, msg = st(lib.z3_reduce_scatter_norm(L.handle, A, 61, far, 0.25, 0, sq, None))
+    assert s == ali
+    s, msg = st(lib.z3_reduce_scatter_norm(L.handle, A, 56, far, 0.25, 0, sq, None))
+    assert s == inv and "grad_stride" in msg
+    s, msg = st(lib.z3_reduce_scatter_norm(L.handle, A, 64, far, math.inf, 0, sq, None))
+    assert s == inv and "scale" in msg
+    s, msg = st(lib.z3_reduce_scatter_norm(L.handle, A, 64, far, 0.25, 0, None, None))
+    assert s == inv and "sumsq" in msg
+    s, msg = st(lib.z3_reduce_scatter_norm(L.handle, A, 64, far, 0.25, 0, sq + 8, None))
+    assert s == ali and "sumsq" in msg
+    s, msg = st(lib.z3_reduce_scatter_norm(L.handle, A, 64, far, 0.25, 0, far + 16, None))
+    assert s == inv and "overlaps" in msg
+
+    hp = z3.AdamHP(1e-3, 0.9, 0.999, 1e-8, 0.0)
+    bufs = [A + i * (1 << 24) for i in range(6)]
+
+    def adam(b=bufs[:5], hp=hp, step=1, clip=bufs[5]):
+        return st(lib.z3_adam_shard_step_clipped(L.handle, *b, ctypes.byref(hp), step, clip, None))
+
+    assert adam(step=0)[0] == inv
+    assert adam(hp=z3.AdamHP(math.nan, 0.9, 0.999, 1e-8, 0.0))[0] == inv
+    s, msg = adam(clip=None)
+    assert s == inv and "clip" in msg
+    s, msg = adam(clip=bufs[5] + 4)
+    assert s == ali and "clip" in msg
+    s, msg = adam(clip=bufs[2])
+    assert s == inv and "overlaps" in msg
+    assert lib.z3_adam_shard_step_clipped(None, *bufs[:5], ctypes.byref(hp), 1, bufs[5],
+                                          None) == inv
+    # an empty layer is a no-op
+    E = z3.Layout([0], 4)
+    assert lib.z3_reduce_scatter_norm(E.handle, None, 0, None, 1.0, 0, None, None) == z3.Z3_OK
+    assert lib.z3_adam_shard_step_clipped(E.handle, *[None] * 5, ctypes.byref(hp), 1, bufs[5],
+                                          None) == z3.Z3_OK
+
+
+@pytest.mark.no_device
+def test_clipped_model_step_refusals(lib):
+    L = z3.Layout([1000], 4)
+    inv, ali = z3.Z3_ERR_INVALID_ARG, z3.Z3_ERR_ALIGNMENT
+    hp = z3.AdamHP(1e-3, 0.9, 0.999, 1e-8, 0.0)
+    at = iter(range(A, 1 << 40, 1 << 20))
+    units = (z3.Unit * 2)(*[z3.Unit(L.handle.value, next(at), next(at), next(at), next(at),
+                                    next(at), 1000, 0.25, None, None) for _ in range(2)])
+    good = [[next(at), next(at)] for _ in range(2)]
+    full, clip, ws = next(at), next(at), next(at)
+
+    def step(units=units, clips=good, full=full, clip=clip, ws=ws, max_norm=1.0, n=2,
+             null_clips=False):
+        carr = None if null_clips else (z3.ClipUnit * 2)(*[z3.ClipUnit(*c, 0, 0) for c in clips])
+        fulls = (ctypes.c_void_p * 1)(full)
+        return lib.z3_model_step_clipped(units, carr, n, fulls, 1, ctypes.byref(hp), 1, max_norm,
+                                         clip, ws, None, None), z3.last_error()
+
+    s, msg = step(null_clips=True)
+    assert s == inv and "clips" in msg
+    s, msg = step(n=0)
+    assert s == inv and "z3_model_step_clipped" in msg
+    s, msg = step(max_norm=0.0)
+    assert s == inv and "max_norm" in msg
+    for name in ("clip", "ws"):
+        s, msg = step(**{name: None})
+        assert s == inv
+        s, msg = step(**{name: good[0][0] + 4})
+        assert s == ali
+    for i in (0, 1):
+        s, msg = step(clips=[[None, c[1]] if k == i else c for k, c in enumerate(good)])
+        assert s == inv and "grad_shards" in msg
+        s, msg = step(clips=[[c[0], None] if k == i else c for k, c in enumerate(good)])
+        assert s == inv and "sumsq" in msg
+    # every pair of buffers that must be apart
+    for what, kw in (("sumsq", dict(clips=[[good[0][0], good[0][0]], good[1]])),
+                     ("sumsq", dict(clips=[good[0], [good[1][0], good[0][1]]])),
+                     ("grad_shards", dict(clips=[good[0], [good[0][0] + 16, good[1][1]]])),
+                     ("grad_shards", dict(clips=[[units[1].grads, good[0][1]], good[1]])),
+                     ("grad_shards", dict(clips=[[units[0].m, good[0][1]], good[1]])),
+                     ("sumsq", dict(clips=[[good[0][0], units[0].shards], good[1]])),
+                     ("sumsq", dict(clips=[[good[0][0], full], good[1]])),
+                     ("clip", dict(clip=units[1].master)), ("clip", dict(clip=full)),
+                     ("clip", dict(clip=ws)), ("workspace", dict(ws=good[1][1])),
+                     ("workspace", dict(ws=full))):
+        s, msg = step(**kw)
+        assert s == inv and "overlaps" in msg and what in msg, (kw, msg)
+    assert step()[0] == z3.Z3_ERR_CUDA          # all right: no device to launch on
+
+
+def test_bindings_refuse_host_tensors():
+    import torch
+    with pytest.raises(ValueError, match="CUDA"):
+        z3.TensorList([torch.zeros(3)])
+    with pytest.raises(ValueError, match="clips"):
+        z3.z3_model_step_clipped([1, 2], [1], [], {}, 1, 1.0, None, None)
