@@ -23,28 +23,57 @@
 namespace z3 {
 namespace {
 
+// --------------------------------------------------------------------------
+// sums of squares
+// --------------------------------------------------------------------------
+
+// Squares are added in binary32 within one batch of a thread (at most 32
+// elements in two chains), where they are exact to 2^-20, and in binary64
+// beyond it: a binary64 addition for every element would bound the kernels
+// by the few FP64 units (one clipped layer's reduce-scatter took 98 us that
+// way, against 45 us).  A batch whose sum leaves [kSafeLo, kSafeHi] may have
+// lost squares to underflow or overflow; it is summed again with its
+// elements scaled by a power of two.  Above kSafeLo the squares that
+// underflowed change the sum by under 2^-50 of it; scaled up from below
+// kSafeLo, elements stay under 2^55 and the least subnormal's square is
+// 2^-98; scaled down from above kSafeHi, what underflows is under 2^-60 of
+// the sum.  Infinities and NaN stay what they are.
+constexpr float kSafeLo = 0x1p-90f, kSafeHi = 0x1p+120f;
+
+__device__ __forceinline__ bool is_safe(float s) { return s >= kSafeLo && s <= kSafeHi; }
+
+// The scale for a sum that is not safe, and what undoes it on the squares.
+__device__ __forceinline__ float rescale(float s) { return s < kSafeLo ? 0x1p+100f : 0x1p-100f; }
+__device__ __forceinline__ double unscale(float s) { return s < kSafeLo ? 0x1p-200 : 0x1p+200; }
+
 // Sum over the CTA's threads, in a fixed order; valid in thread 0.
 template <int THREADS>
 __device__ __forceinline__ double block_sum(double x) {
-    __shared__ double warp_sum[THREADS / 32];
+    constexpr int WARPS = THREADS / 32;
+    __shared__ double warp_sum[WARPS];
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_down_sync(0xffffffffu, x, d);
     if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = x;
     __syncthreads();
-    double s = 0.0;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < 32) {
+        x = threadIdx.x < WARPS ? warp_sum[threadIdx.x] : 0.0;
 #pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) s += warp_sum[w];
+        for (int d = WARPS / 2; d > 0; d >>= 1) x += __shfl_down_sync(0xffffffffu, x, d);
     }
-    __syncthreads();
-    return s;
+    return x;
 }
 
+// --------------------------------------------------------------------------
+// walking a list of tensors
+// --------------------------------------------------------------------------
+
 // One CTA's part of one tensor: n vectors from p, of which bytes
-// [begin, end) belong to the tensor.
+// [begin, end) belong to the tensor.  Vectors [lo, hi) are the tensor's
+// whole; a partial one before or after them is handled by elements.
 struct Segment {
     unsigned char *p;
     int64_t n, begin, end;
+    int64_t lo, hi;
     int kind;
 };
 
@@ -61,11 +90,60 @@ __device__ __forceinline__ Segment segment(const TAB &tab, int i, int64_t v0, in
     const int head = (int)(e.vec0_ends >> 4) & 15, tail = (int)e.vec0_ends & 15;
     g.begin = s == a ? head : 0;
     g.end = t == b && tail != 0 ? g.n * 16 - 16 + tail : g.n * 16;
+    g.lo = g.begin != 0 ? 1 : 0;
+    g.hi = max(g.lo, g.end / 16);
     return g;
 }
 
+// The byte offset of the element of a partial vector that this thread
+// handles, or -1: threads 0-7 take the first vector's, 8-15 the last's.
+__device__ __forceinline__ int64_t edge_element(const Segment &g, int size) {
+    const int l = threadIdx.x & 7;
+    if (threadIdx.x >= 16 || l * size >= 16) return -1;
+    const bool last = threadIdx.x >= 8;
+    if (last ? g.hi * 16 >= g.end : g.lo == 0) return -1;  // no partial vector there
+    const int64_t x = (last ? g.hi * 16 : 0) + l * size;
+    return x >= g.begin && x < g.end ? x : -1;
+}
+
+// Vectors in flight per thread.
+constexpr int kListBatch = 4;
+
+// Sum of squares of the batch's elements times k.
+template <bool SCALED>
+__device__ __forceinline__ float squares(const uint4 (&w)[kListBatch], int kind, float k) {
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int u = 0; u < kListBatch; ++u) {
+        if (kind == Z3_F32) {
+            float f[4] = {__uint_as_float(w[u].x), __uint_as_float(w[u].y),
+                          __uint_as_float(w[u].z), __uint_as_float(w[u].w)};
+#pragma unroll
+            for (int l = 0; l < 4; l += 2) {
+                const float x = SCALED ? f[l] * k : f[l], y = SCALED ? f[l + 1] * k : f[l + 1];
+                s0 = __fmaf_rn(x, x, s0);
+                s1 = __fmaf_rn(y, y, s1);
+            }
+        } else {
+            float f[8];
+            unpack8(w[u], f);
+#pragma unroll
+            for (int l = 0; l < 8; l += 2) {
+                const float x = SCALED ? f[l] * k : f[l], y = SCALED ? f[l + 1] * k : f[l + 1];
+                s0 = __fmaf_rn(x, x, s0);
+                s1 = __fmaf_rn(y, y, s1);
+            }
+        }
+    }
+    return s0 + s1;
+}
+
+// --------------------------------------------------------------------------
+// the norm
+// --------------------------------------------------------------------------
+
 template <typename TAB>
-__global__ void __launch_bounds__(kListThreads)
+__global__ void __launch_bounds__(kListThreads, kListCtas)
 k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
     pdl_enter();
     const int64_t v0 = tab.vecs * blockIdx.x / tab.grid;
@@ -75,18 +153,27 @@ k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
         if ((int64_t)(tab.e[i].vec0_ends >> 8) >= v1) break;
         const Segment g = segment(tab, i, v0, v1);
         if (g.kind == Z3_SUMSQ) {
+            const double *d = reinterpret_cast<const double *>(g.p);
             for (int64_t x = g.begin / 8 + threadIdx.x; x < g.end / 8; x += kListThreads)
-                sum += reinterpret_cast<const double *>(g.p)[x];
-        } else if (g.kind == Z3_F32) {
-            for (int64_t x = g.begin / 4 + threadIdx.x; x < g.end / 4; x += kListThreads) {
-                const double f = reinterpret_cast<const float *>(g.p)[x];
-                sum += f * f;
-            }
-        } else {
-            for (int64_t x = g.begin / 2 + threadIdx.x; x < g.end / 2; x += kListThreads) {
-                const double f = bf16_to_f32(reinterpret_cast<const uint16_t *>(g.p)[x]);
-                sum += f * f;
-            }
+                sum += d[x];
+            continue;
+        }
+        const uint4 *p = reinterpret_cast<const uint4 *>(g.p);
+        for (int64_t q = g.lo + threadIdx.x; q < g.hi; q += kListBatch * kListThreads) {
+            uint4 w[kListBatch];
+#pragma unroll
+            for (int u = 0; u < kListBatch; ++u)
+                w[u] = q + u * kListThreads < g.hi ? __ldg(p + q + u * kListThreads)
+                                                   : make_uint4(0, 0, 0, 0);
+            const float s = squares<false>(w, g.kind, 1.0f);
+            sum += is_safe(s) ? (double)s
+                              : (double)squares<true>(w, g.kind, rescale(s)) * unscale(s);
+        }
+        const int64_t x = edge_element(g, g.kind == Z3_F32 ? 4 : 2);
+        if (x >= 0) {
+            const double f = g.kind == Z3_F32 ? *reinterpret_cast<const float *>(g.p + x)
+                                              : bf16_to_f32(*reinterpret_cast<const uint16_t *>(g.p + x));
+            sum += f * f;
         }
     }
     sum = block_sum<kListThreads>(sum);
@@ -116,25 +203,53 @@ k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
                                 : norm > o.max_norm ? __fdiv_rn(o.max_norm, norm) : 1.0f;
 }
 
+// --------------------------------------------------------------------------
+// clipping
+// --------------------------------------------------------------------------
+
+__device__ __forceinline__ uint4 scaled(const uint4 &w, int kind, float c) {
+    if (kind == Z3_F32)
+        return make_uint4(__float_as_uint(__fmul_rn(__uint_as_float(w.x), c)),
+                          __float_as_uint(__fmul_rn(__uint_as_float(w.y), c)),
+                          __float_as_uint(__fmul_rn(__uint_as_float(w.z), c)),
+                          __float_as_uint(__fmul_rn(__uint_as_float(w.w), c)));
+    float f[8];
+    unpack8(w, f);
+#pragma unroll
+    for (int l = 0; l < 8; ++l) f[l] = __fmul_rn(f[l], c);
+    return pack8(f);
+}
+
+// Each CTA walks its share backwards: what the norm read last is still in L2.
 template <typename TAB>
-__global__ void __launch_bounds__(kListThreads)
+__global__ void __launch_bounds__(kListThreads, kListCtas)
 k_clip(const __grid_constant__ TAB tab, const float *clip) {
     pdl_enter();
     const float c = __ldcg(clip + 1);
     if (c == 1.0f || isnan(c)) return;  // nothing changes; no step to take
-    const int64_t v0 = tab.vecs * blockIdx.x / tab.grid;
-    const int64_t v1 = tab.vecs * (blockIdx.x + 1) / tab.grid;
-    for (int i = tab.first[blockIdx.x]; i < tab.count; ++i) {
-        if ((int64_t)(tab.e[i].vec0_ends >> 8) >= v1) break;
+    const int b = blockIdx.x;
+    const int64_t v0 = tab.vecs * b / tab.grid;
+    const int64_t v1 = tab.vecs * (b + 1) / tab.grid;
+    for (int i = b + 1 < tab.grid ? tab.first[b + 1] : tab.count - 1; i >= tab.first[b]; --i) {
+        if ((int64_t)(tab.e[i].vec0_ends >> 8) >= v1) continue;
         const Segment g = segment(tab, i, v0, v1);
-        if (g.kind == Z3_F32) {
-            float *f = reinterpret_cast<float *>(g.p);
-            for (int64_t x = g.begin / 4 + threadIdx.x; x < g.end / 4; x += kListThreads)
-                f[x] = __fmul_rn(f[x], c);
-        } else {
-            uint16_t *h = reinterpret_cast<uint16_t *>(g.p);
-            for (int64_t x = g.begin / 2 + threadIdx.x; x < g.end / 2; x += kListThreads)
-                h[x] = f32_to_bf16(__fmul_rn(bf16_to_f32(h[x]), c));
+        uint4 *p = reinterpret_cast<uint4 *>(g.p);
+        for (int64_t q = g.hi - 1 - threadIdx.x; q >= g.lo; q -= kListBatch * kListThreads) {
+            uint4 w[kListBatch];
+#pragma unroll
+            for (int u = 0; u < kListBatch; ++u)
+                if (q - u * kListThreads >= g.lo) w[u] = p[q - u * kListThreads];
+#pragma unroll
+            for (int u = 0; u < kListBatch; ++u)
+                if (q - u * kListThreads >= g.lo) p[q - u * kListThreads] = scaled(w[u], g.kind, c);
+        }
+        const int64_t x = edge_element(g, g.kind == Z3_F32 ? 4 : 2);
+        if (x >= 0 && g.kind == Z3_F32) {
+            float *f = reinterpret_cast<float *>(g.p + x);
+            *f = __fmul_rn(*f, c);
+        } else if (x >= 0) {
+            uint16_t *h = reinterpret_cast<uint16_t *>(g.p + x);
+            *h = f32_to_bf16(__fmul_rn(bf16_to_f32(*h), c));
         }
     }
 }
@@ -143,10 +258,56 @@ k_clip(const __grid_constant__ TAB tab, const float *clip) {
 // ReduceScatter that also leaves one sum of squares per tile
 // --------------------------------------------------------------------------
 
-__device__ __forceinline__ double square(float x) { return (double)x * (double)x; }
+// A thread's share of its tile's sum of squares: s * 2^e, in binary32 where
+// that is safe (e = 0).
+struct TileSum {
+    float s;
+    int e;
+    __device__ __forceinline__ double value() const {
+        return (double)s * (e == 0 ? 1.0 : e < 0 ? 0x1p-200 : 0x1p+200);
+    }
+};
+
+__device__ __forceinline__ TileSum tile_sum(const float g[8]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) s = __fmaf_rn(g[l], g[l], s);
+    if (is_safe(s)) return {s, 0};
+    const int e = s < kSafeLo ? -200 : 200;
+    const float k = e < 0 ? 0x1p+100f : 0x1p-100f;
+    s = 0.0f;
+#pragma unroll
+    for (int l = 0; l < 8; ++l) s = __fmaf_rn(g[l] * k, g[l] * k, s);
+    return {s, s == 0.0f ? 0 : e};
+}
+
+// The sum over the CTA, stored by one thread: in binary32 within each warp,
+// unless one of its lanes could not hold its own share so.
+__device__ __forceinline__ void store_tile_sum(const TileSum &t, double *out) {
+    constexpr int WARPS = kReduceThreads / 32;
+    __shared__ double warp_sum[WARPS];
+    double w;
+    if (__any_sync(0xffffffffu, t.e != 0)) {
+        w = t.value();
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) w += __shfl_down_sync(0xffffffffu, w, d);
+    } else {
+        float s = t.s;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_down_sync(0xffffffffu, s, d);
+        w = s;
+    }
+    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = w;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    w = warp_sum[0];
+#pragma unroll
+    for (int i = 1; i < WARPS; ++i) w += warp_sum[i];
+    *out = w;
+}
 
 template <int PHI, bool ACC, bool EARLY>
-__device__ __forceinline__ double reduce_norm_vector(const ReduceNormArgs &a, int n_ranks,
+__device__ __forceinline__ TileSum reduce_norm_vector(const ReduceNormArgs &a, int n_ranks,
                                                      int64_t x0, int64_t delta) {
     float g[8];
     fold_vector<PHI>(a.grads, a.stride, a.scale, n_ranks, x0, delta, g);
@@ -158,16 +319,13 @@ __device__ __forceinline__ double reduce_norm_vector(const ReduceNormArgs &a, in
     }
     if constexpr (EARLY) pdl_enter();
     st8f(a.grad_shards + x0, g);
-    double s = 0.0;
-#pragma unroll
-    for (int l = 0; l < 8; ++l) s += square(g[l]);
-    return s;
+    return tile_sum(g);
 }
 
 template <bool ACC>
-__device__ __noinline__ double reduce_norm_edges(const ReduceNormArgs a, int n_ranks, int64_t x0,
-                                                 int64_t delta, int64_t c0, int64_t c_end,
-                                                 int64_t valid_end) {
+__device__ __noinline__ TileSum reduce_norm_edges(const ReduceNormArgs a, int n_ranks, int64_t x0,
+                                                  int64_t delta, int64_t c0, int64_t c_end,
+                                                  int64_t valid_end) {
     double s = 0.0;
     for (int l = 0; l < kVec; ++l) {
         const int64_t x = x0 + l;
@@ -178,9 +336,10 @@ __device__ __noinline__ double reduce_norm_edges(const ReduceNormArgs a, int n_r
             if constexpr (ACC) g = __fadd_rn(a.grad_shards[x], g);
         }
         a.grad_shards[x] = g;
-        s += square(g);
+        s += (double)g * (double)g;
     }
-    return s;
+    if (s == 0.0 || is_safe((float)s)) return {(float)s, 0};
+    return s < kSafeLo ? TileSum{(float)(s * 0x1p+200), -200} : TileSum{(float)(s * 0x1p-200), 200};
 }
 
 template <bool ALIGNED, bool ACC, bool EARLY>
@@ -195,7 +354,7 @@ k_reduce_norm(const __grid_constant__ Tab tab, const ReduceNormArgs a) {
     const int64_t delta = e.F + tr.r * e.s - c0;
     const int64_t x0 = (c0 / kVec + tr.t * (int64_t)kReduceThreads + threadIdx.x) * kVec;
     const int n = tab.n_ranks;
-    double s = 0.0;
+    TileSum s;
     if (x0 >= c0 && x0 + kVec <= valid_end) {
         if constexpr (ALIGNED) {
             s = reduce_norm_vector<0, ACC, EARLY>(a, n, x0, delta);
@@ -213,10 +372,10 @@ k_reduce_norm(const __grid_constant__ Tab tab, const ReduceNormArgs a) {
         }
     } else {
         if constexpr (EARLY) pdl_enter();
-        if (x0 < c_end) s = reduce_norm_edges<ACC>(a, n, x0, delta, c0, c_end, valid_end);
+        s = x0 < c_end ? reduce_norm_edges<ACC>(a, n, x0, delta, c0, c_end, valid_end)
+                       : TileSum{0.0f, 0};
     }
-    s = block_sum<kReduceThreads>(s);
-    if (threadIdx.x == 0) a.sumsq[blockIdx.x] = s;
+    store_tile_sum(s, a.sumsq + blockIdx.x);
 }
 
 // --------------------------------------------------------------------------

@@ -17,7 +17,8 @@ namespace z3 {
 // equal, contiguous share of the run, so tensors of any lengths balance.
 constexpr int kSMs = 152;
 constexpr int kListThreads = 512;
-constexpr int kListMaxGrid = 4 * kSMs;
+constexpr int kListCtas = 3;  // resident on an SM
+constexpr int kListMaxGrid = kListCtas * kSMs;
 
 struct ListEntry {
     uint64_t base_kind;  // address rounded down to 16 bytes | z3_dtype
