@@ -303,9 +303,9 @@ typedef struct z3_tensor {
     int32_t reserved;
 } z3_tensor;
 
-/* Bytes of z3_grad_norm's workspace (device memory, 16-byte aligned).  The
- * caller fills it with zeros once; every call leaves it ready for the next.
- * Calls that may overlap on the GPU need a workspace each. */
+/* Bytes of z3_grad_norm's workspace (device memory, 16-byte aligned).  What
+ * it holds before a call does not matter, and nothing is kept in it from one
+ * call for the next; calls that may overlap on the GPU need one each. */
 z3_status z3_grad_norm_workspace_bytes(int64_t *bytes);
 
 /* The global norm of n tensors and its factor, written to clip (float [2],

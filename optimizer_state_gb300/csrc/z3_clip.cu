@@ -28,23 +28,41 @@ namespace {
 // --------------------------------------------------------------------------
 
 // Squares are added in binary32 within one batch of a thread (at most 32
-// elements in two chains), where they are exact to 2^-20, and in binary64
-// beyond it: a binary64 addition for every element would bound the kernels
-// by the few FP64 units (one clipped layer's reduce-scatter took 98 us that
-// way, against 45 us).  A batch whose sum leaves [kSafeLo, kSafeHi] may have
-// lost squares to underflow or overflow; it is summed again with its
-// elements scaled by a power of two.  Above kSafeLo the squares that
-// underflowed change the sum by under 2^-50 of it; scaled up from below
-// kSafeLo, elements stay under 2^55 and the least subnormal's square is
-// 2^-98; scaled down from above kSafeHi, what underflows is under 2^-60 of
-// the sum.  Infinities and NaN stay what they are.
-constexpr float kSafeLo = 0x1p-90f, kSafeHi = 0x1p+120f;
+// elements in two chains, exact to 2^-20), and the batches' sums in pairs of
+// binary32 (48 bits).  FP64 units are few: an SM takes 16 cycles for a warp's
+// binary64 addition.  With one for every element the reduce-scatter of a
+// d = 1024 layer with its norm took 98 us instead of 45, and with one for
+// every batch and for every step of the CTAs' trees the norm of 700 tensors
+// (10 MB) took 11.5 us instead of 6.  A CTA's sum is then stored as binary64.
+//
+// A batch whose sum leaves [kSafeLo, kSafeHi] may have lost squares to
+// underflow or overflow; it is summed again with its elements scaled by a
+// power of two, and goes to a binary64 sum of its own.  Above kSafeLo the
+// squares that underflowed change the sum by under 2^-50 of it; scaled up
+// from below kSafeLo, elements stay under 2^55 and the least subnormal's
+// square is 2^-98; scaled down from above kSafeHi, the squares that underflow
+// are those of elements under 2^5.  2^30 safe batches do not overflow.
+// Infinities and NaN stay what they are.
+constexpr float kSafeLo = 0x1p-90f, kSafeHi = 0x1p+90f;
 
 __device__ __forceinline__ bool is_safe(float s) { return s >= kSafeLo && s <= kSafeHi; }
 
 // The scale for a sum that is not safe, and what undoes it on the squares.
-__device__ __forceinline__ float rescale(float s) { return s < kSafeLo ? 0x1p+100f : 0x1p-100f; }
-__device__ __forceinline__ double unscale(float s) { return s < kSafeLo ? 0x1p-200 : 0x1p+200; }
+__device__ __forceinline__ float rescale(float s) { return s < kSafeLo ? 0x1p+100f : 0x1p-80f; }
+__device__ __forceinline__ double unscale(float s) { return s < kSafeLo ? 0x1p-200 : 0x1p+160; }
+
+struct Sum {
+    float hi = 0.0f, lo = 0.0f;  // hi + lo: the safe batches
+    double rare = 0.0;           // the others
+
+    // hi + s exactly as the rounded sum and its error (Knuth's two-sum)
+    __device__ __forceinline__ void add(float s) {
+        const float t = hi + s;
+        const float b = t - hi;
+        lo += (hi - (t - b)) + (s - b);
+        hi = t;
+    }
+};
 
 // Sum over the CTA's threads, in a fixed order; valid in thread 0.
 template <int THREADS>
@@ -63,144 +81,309 @@ __device__ __forceinline__ double block_sum(double x) {
     return x;
 }
 
+template <int THREADS>
+__device__ __forceinline__ double block_sum(Sum s) {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ float2 warp_sum[WARPS];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float hi = __shfl_down_sync(0xffffffffu, s.hi, d);
+        const float lo = __shfl_down_sync(0xffffffffu, s.lo, d);
+        s.add(hi);
+        s.lo += lo;
+    }
+    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = make_float2(s.hi, s.lo);
+    double rare = 0.0;
+    if (__syncthreads_or(s.rare != 0.0)) rare = block_sum<THREADS>(s.rare);
+    if (threadIdx.x >= 32) return 0.0;
+    if (threadIdx.x < WARPS) {
+        s.hi = warp_sum[threadIdx.x].x;
+        s.lo = warp_sum[threadIdx.x].y;
+    }
+#pragma unroll
+    for (int d = WARPS / 2; d > 0; d >>= 1) {
+        const float hi = __shfl_down_sync(0xffffffffu, s.hi, d);
+        const float lo = __shfl_down_sync(0xffffffffu, s.lo, d);
+        s.add(hi);
+        s.lo += lo;
+    }
+    return (double)s.hi + (double)s.lo + rare;
+}
+
 // --------------------------------------------------------------------------
 // walking a list of tensors
 // --------------------------------------------------------------------------
 
-// One CTA's part of one tensor: n vectors from p, of which bytes
-// [begin, end) belong to the tensor.  Vectors [lo, hi) are the tensor's
-// whole; a partial one before or after them is handled by elements.
-struct Segment {
+__device__ __forceinline__ int64_t first_vec(const ListEntry &e) {
+    return (int64_t)(e.vec0_ends >> 8);
+}
+
+// The entry that holds vector v of the run, among entries lo..hi.
+__device__ __forceinline__ int find_entry(const ListEntry *e, int lo, int hi, int64_t v) {
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_vec(e[mid]) <= v) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <typename TAB>
+__device__ __forceinline__ int find_entry(const TAB &tab, int64_t v) {
+    const int b = (int)(v >> tab.shift);
+    return find_entry(tab.e, tab.first[b], tab.first[b + 1], v);
+}
+
+// One vector of the run: bytes [begin, end) of the 16 at p belong to the
+// tensor.  begin = end = 0: no vector.
+struct VecRef {
     unsigned char *p;
-    int64_t n, begin, end;
-    int64_t lo, hi;
-    int kind;
+    int kind, begin, end;
+    __device__ __forceinline__ bool whole() const { return end - begin == 16; }
+    __device__ __forceinline__ bool partial() const { return end - begin != 16 && end != 0; }
 };
 
-// The part of entry i that lies in vectors [v0, v1) of the run.
-template <typename TAB>
-__device__ __forceinline__ Segment segment(const TAB &tab, int i, int64_t v0, int64_t v1) {
-    const ListEntry &e = tab.e[i];
-    const int64_t a = (int64_t)(e.vec0_ends >> 8), b = (int64_t)(tab.e[i + 1].vec0_ends >> 8);
-    const int64_t s = max(v0, a), t = min(v1, b);
-    Segment g;
-    g.kind = (int)(e.base_kind & 15);
-    g.p = reinterpret_cast<unsigned char *>(e.base_kind & ~(uint64_t)15) + (s - a) * 16;
-    g.n = t - s;
+// Vector v, of entry e whose successor is next.
+__device__ __forceinline__ VecRef vec_ref(const ListEntry &e, const ListEntry &next, int64_t v) {
+    const int64_t a = first_vec(e);
     const int head = (int)(e.vec0_ends >> 4) & 15, tail = (int)e.vec0_ends & 15;
-    g.begin = s == a ? head : 0;
-    g.end = t == b && tail != 0 ? g.n * 16 - 16 + tail : g.n * 16;
-    g.lo = g.begin != 0 ? 1 : 0;
-    g.hi = max(g.lo, g.end / 16);
-    return g;
+    VecRef r;
+    r.kind = (int)(e.base_kind & 15);
+    r.p = reinterpret_cast<unsigned char *>(e.base_kind & ~(uint64_t)15) + (v - a) * 16;
+    r.begin = v == a ? head : 0;
+    r.end = v + 1 == first_vec(next) && tail != 0 ? tail : 16;
+    return r;
 }
 
-// The byte offset of the element of a partial vector that this thread
-// handles, or -1: threads 0-7 take the first vector's, 8-15 the last's.
-__device__ __forceinline__ int64_t edge_element(const Segment &g, int size) {
-    const int l = threadIdx.x & 7;
-    if (threadIdx.x >= 16 || l * size >= 16) return -1;
-    const bool last = threadIdx.x >= 8;
-    if (last ? g.hi * 16 >= g.end : g.lo == 0) return -1;  // no partial vector there
-    const int64_t x = (last ? g.hi * 16 : 0) + l * size;
-    return x >= g.begin && x < g.end ? x : -1;
+// The tensor's bytes of a partial vector, zeros in place of the others.
+__device__ __noinline__ uint4 load_partial(const VecRef r) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int x = 0; x < 16; x += 2)
+        if (x >= r.begin && x < r.end)
+            w[x / 4] |= (uint32_t)*reinterpret_cast<const uint16_t *>(r.p + x) << (x % 4 * 8);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Vectors in flight per thread.
-constexpr int kListBatch = 4;
+__device__ __noinline__ void store_partial(const VecRef r, const uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int x = 0; x < 16; x += 2)
+        if (x >= r.begin && x < r.end)
+            *reinterpret_cast<uint16_t *>(r.p + x) = (uint16_t)(w[x / 4] >> (x % 4 * 8));
+}
 
-// Sum of squares of the batch's elements times k.
-template <bool SCALED>
-__device__ __forceinline__ float squares(const uint4 (&w)[kListBatch], int kind, float k) {
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-    for (int u = 0; u < kListBatch; ++u) {
-        if (kind == Z3_F32) {
-            float f[4] = {__uint_as_float(w[u].x), __uint_as_float(w[u].y),
-                          __uint_as_float(w[u].z), __uint_as_float(w[u].w)};
-#pragma unroll
-            for (int l = 0; l < 4; l += 2) {
-                const float x = SCALED ? f[l] * k : f[l], y = SCALED ? f[l + 1] * k : f[l + 1];
-                s0 = __fmaf_rn(x, x, s0);
-                s1 = __fmaf_rn(y, y, s1);
-            }
-        } else {
-            float f[8];
-            unpack8(w[u], f);
-#pragma unroll
-            for (int l = 0; l < 8; l += 2) {
-                const float x = SCALED ? f[l] * k : f[l], y = SCALED ? f[l + 1] * k : f[l + 1];
-                s0 = __fmaf_rn(x, x, s0);
-                s1 = __fmaf_rn(y, y, s1);
-            }
-        }
+// A tile of U vectors per thread.  Most tiles of long tensors hold whole
+// vectors of one tensor; the others stage their entries in shared memory
+// and every thread finds its vectors' own.
+template <int U>
+struct Tile {
+    static constexpr int kVecs = U * kListThreads;
+    int64_t v0, v1;       // its vectors of the run
+    unsigned char *p;     // where they lie, when one tensor holds them whole
+    int kind;
+    int64_t past;         // the end of that tensor's whole vectors in the run
+    int lo, n;            // else: its entries, lo.. of the table, n of them
+
+    template <typename TAB>
+    __device__ __forceinline__ bool locate(const TAB &tab, int64_t t) {
+        v0 = t * kVecs;
+        v1 = min(v0 + kVecs, tab.vecs);
+        lo = find_entry(tab, v0);
+        const ListEntry &e = tab.e[lo], &next = tab.e[lo + 1];
+        const VecRef a = vec_ref(e, next, v0);
+        past = first_vec(next) - ((e.vec0_ends & 15) != 0);
+        p = a.p;
+        kind = a.kind;
+        return a.begin == 0 && v1 <= past;
     }
-    return s0 + s1;
-}
+
+    // Every thread of the CTA takes part.
+    template <typename TAB>
+    __device__ __forceinline__ void stage(const TAB &tab, ListEntry *staged) {
+        n = find_entry(tab, v1 - 1) - lo + 1;
+        __syncthreads();  // the last tile's entries are done with
+        for (int k = threadIdx.x; k <= n; k += kListThreads) staged[k] = tab.e[lo + k];
+        __syncthreads();
+    }
+
+    __device__ __forceinline__ VecRef ref(const ListEntry *staged, int u) const {
+        const int64_t v = v0 + u * kListThreads + threadIdx.x;
+        if (v >= v1) return VecRef{nullptr, 0, 0, 0};
+        const int i = find_entry(staged, 0, n - 1, v);
+        return vec_ref(staged[i], staged[i + 1], v);
+    }
+};
 
 // --------------------------------------------------------------------------
 // the norm
 // --------------------------------------------------------------------------
 
-template <typename TAB>
-__global__ void __launch_bounds__(kListThreads, kListCtas)
-k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
-    pdl_enter();
-    const int64_t v0 = tab.vecs * blockIdx.x / tab.grid;
-    const int64_t v1 = tab.vecs * (blockIdx.x + 1) / tab.grid;
-    double sum = 0.0;
-    for (int i = tab.first[blockIdx.x]; i < tab.count; ++i) {
-        if ((int64_t)(tab.e[i].vec0_ends >> 8) >= v1) break;
-        const Segment g = segment(tab, i, v0, v1);
-        if (g.kind == Z3_SUMSQ) {
-            const double *d = reinterpret_cast<const double *>(g.p);
-            for (int64_t x = g.begin / 8 + threadIdx.x; x < g.end / 8; x += kListThreads)
-                sum += d[x];
-            continue;
-        }
-        const uint4 *p = reinterpret_cast<const uint4 *>(g.p);
-        for (int64_t q = g.lo + threadIdx.x; q < g.hi; q += kListBatch * kListThreads) {
-            uint4 w[kListBatch];
+// Adds the squares of two bf16 values: mixed-precision multiply-adds take
+// them as they are, in half the instructions of widening them first.
+__device__ __forceinline__ void add_squares(uint32_t w, float &s0, float &s1) {
+    asm("{\n\t"
+        ".reg .b16 x, y;\n\t"
+        "mov.b32 {x, y}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, x, x, %0;\n\t"
+        "fma.rn.f32.bf16 %1, y, y, %1;\n\t"
+        "}"
+        : "+f"(s0), "+f"(s1)
+        : "r"(w));
+}
+
+// Adds the squares of the elements of a vector, times k each, to two chains.
+template <bool SCALED>
+__device__ __forceinline__ void squares(const uint4 &w, bool f32, float k, float &s0, float &s1) {
+    if (f32) {
+        const float f[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z),
+                            __uint_as_float(w.w)};
 #pragma unroll
-            for (int u = 0; u < kListBatch; ++u)
-                w[u] = q + u * kListThreads < g.hi ? __ldg(p + q + u * kListThreads)
-                                                   : make_uint4(0, 0, 0, 0);
-            const float s = squares<false>(w, g.kind, 1.0f);
-            sum += is_safe(s) ? (double)s
-                              : (double)squares<true>(w, g.kind, rescale(s)) * unscale(s);
+        for (int l = 0; l < 4; l += 2) {
+            const float x = SCALED ? f[l] * k : f[l], y = SCALED ? f[l + 1] * k : f[l + 1];
+            s0 = __fmaf_rn(x, x, s0);
+            s1 = __fmaf_rn(y, y, s1);
         }
-        const int64_t x = edge_element(g, g.kind == Z3_F32 ? 4 : 2);
-        if (x >= 0) {
-            const double f = g.kind == Z3_F32 ? *reinterpret_cast<const float *>(g.p + x)
-                                              : bf16_to_f32(*reinterpret_cast<const uint16_t *>(g.p + x));
-            sum += f * f;
+    } else if (!SCALED) {
+        add_squares(w.x, s0, s1);
+        add_squares(w.y, s0, s1);
+        add_squares(w.z, s0, s1);
+        add_squares(w.w, s0, s1);
+    } else {
+        float f[8];
+        unpack8(w, f);
+#pragma unroll
+        for (int l = 0; l < 8; l += 2) {
+            const float x = SCALED ? f[l] * k : f[l], y = SCALED ? f[l + 1] * k : f[l + 1];
+            s0 = __fmaf_rn(x, x, s0);
+            s1 = __fmaf_rn(y, y, s1);
         }
     }
-    sum = block_sum<kListThreads>(sum);
-    // the last CTA to store its partial adds them all, in CTA order
-    __shared__ bool last;
-    if (threadIdx.x == 0) {
-        o.ws->partial[blockIdx.x] = sum;
-        __threadfence();
-        last = atomicInc(&o.ws->ticket, gridDim.x - 1) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    double all = 0.0;
-    for (int b = threadIdx.x; b < (int)gridDim.x; b += kListThreads)
-        all += __ldcg(&o.ws->partial[b]);
-    all = block_sum<kListThreads>(all);
-    if (threadIdx.x != 0) return;
-    if (!o.first) all += __ldcg(&o.ws->carry);
-    if (!o.last) {
-        o.ws->carry = all;
+}
+
+// Adds a batch of U vectors of gradients; f32(u): vector u holds fp32, not bf16.
+template <int U, typename F32>
+__device__ __forceinline__ void add_batch(Sum &sum, const uint4 (&w)[U], F32 f32) {
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) squares<false>(w[u], f32(u), 1.0f, s0, s1);
+    const float s = s0 + s1;
+    if (is_safe(s)) {
+        sum.add(s);
         return;
     }
-    const float norm = (float)sqrt(all);
+    s0 = s1 = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) squares<true>(w[u], f32(u), rescale(s), s0, s1);
+    if (s0 + s1 != 0.0f) sum.rare += (double)(s0 + s1) * unscale(s);
+}
+
+// Adds a vector of two sums of squares.
+__device__ __forceinline__ void add_sums(Sum &sum, const uint4 &w) {
+    sum.rare += __hiloint2double(w.y, w.x) + __hiloint2double(w.w, w.z);
+}
+
+constexpr int kNormU = 3;
+
+// The run's last vectors, 64 MB, are left in L2 for the clipping that
+// follows from the end; those before are read with the streaming hint, so
+// that they make no room for themselves.  Norm and clipping of 1.41 GB: 612
+// us, against 628 without the hint; 617 with 32 MB, 614 with 160 MB.
+constexpr int64_t kNormKeep = (64ll << 20) / 16;
+constexpr int kFinishThreads = 256;
+
+__device__ __forceinline__ void write_clip(const NormOut &o, double sum) {
+    const float norm = (float)sqrt(sum);
     o.clip[0] = norm;
     o.clip[1] = !isfinite(norm) ? __int_as_float(0x7fc00000)
                                 : norm > o.max_norm ? __fdiv_rn(o.max_norm, norm) : 1.0f;
+}
+
+template <typename TAB>
+__global__ void __launch_bounds__(kListThreads, kNormCtas)
+k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
+    using T = Tile<kNormU>;
+    __shared__ ListEntry staged[T::kVecs + 1];
+    pdl_enter();
+    Sum sum;
+    const int64_t passing = tab.vecs - kNormKeep;
+    const int64_t tiles = (tab.vecs + T::kVecs - 1) / T::kVecs;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        T tile{};
+        uint4 w[kNormU];
+        if (tile.locate(tab, t)) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(tile.p) + threadIdx.x;
+            const int n = (int)(tile.v1 - tile.v0) - (int)threadIdx.x;
+#pragma unroll
+            for (int u = 0; u < kNormU; ++u)
+                w[u] = u * kListThreads >= n ? make_uint4(0, 0, 0, 0)
+                       : tile.v0 < passing   ? __ldcs(p + u * kListThreads)
+                                             : __ldg(p + u * kListThreads);
+            if (tile.kind == Z3_F32) {
+                add_batch(sum, w, [](int) { return true; });
+            } else if (tile.kind == Z3_BF16) {
+                add_batch(sum, w, [](int) { return false; });
+            } else {
+#pragma unroll
+                for (int u = 0; u < kNormU; ++u) add_sums(sum, w[u]);
+            }
+            continue;
+        }
+        tile.stage(tab, staged);
+        int kind[kNormU];
+        bool partial = false;
+#pragma unroll
+        for (int u = 0; u < kNormU; ++u) {
+            const VecRef r = tile.ref(staged, u);
+            w[u] = r.whole() ? __ldg(reinterpret_cast<const uint4 *>(r.p))
+                             : make_uint4(0, 0, 0, 0);
+            kind[u] = r.kind;
+            partial |= r.partial();
+        }
+#pragma unroll
+        for (int u = 0; u < kNormU; ++u) {
+            if (kind[u] != Z3_SUMSQ) continue;
+            add_sums(sum, w[u]);
+            w[u] = make_uint4(0, 0, 0, 0);
+        }
+        add_batch(sum, w, [&](int u) { return kind[u] == Z3_F32; });
+        if (!partial) continue;
+#pragma unroll 1
+        for (int u = 0; u < kNormU; ++u) {
+            const VecRef r = tile.ref(staged, u);
+            if (!r.partial()) continue;
+            const uint4 x[1] = {load_partial(r)};
+            if (r.kind == Z3_SUMSQ) add_sums(sum, x[0]);
+            else add_batch(sum, x, [&](int) { return r.kind == Z3_F32; });
+        }
+    }
+    const double all = block_sum<kListThreads>(sum);
+    if (threadIdx.x != 0) return;
+    if (o.alone) write_clip(o, all);
+    else o.ws->partial[blockIdx.x] = all;
+}
+
+// Adds the n partials of the launch before it, in CTA order, to the sums of
+// the call's earlier launches.  As a launch of its own it starts while the
+// partials are computed, and its wait for them is shorter than a ticket
+// taken by every CTA and a last one's sum: 912 tickets at one address took
+// 1 us more, one ticket 2 us.
+__global__ void __launch_bounds__(kFinishThreads) k_norm_finish(const NormOut o, int n) {
+    pdl_enter();
+    constexpr int PER = (kNormMaxGrid + kFinishThreads - 1) / kFinishThreads;
+    double x[PER];  // all loads in flight at once
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = i * kFinishThreads + threadIdx.x;
+        x[i] = b < n ? o.ws->partial[b] : 0.0;
+    }
+    double sum = x[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) sum += x[i];
+    sum = block_sum<kFinishThreads>(sum);
+    if (threadIdx.x != 0) return;
+    if (!o.first) sum += o.ws->carry;
+    if (o.last) write_clip(o, sum);
+    else o.ws->carry = sum;
 }
 
 // --------------------------------------------------------------------------
@@ -220,38 +403,46 @@ __device__ __forceinline__ uint4 scaled(const uint4 &w, int kind, float c) {
     return pack8(f);
 }
 
-// Each CTA walks its share backwards: what the norm read last is still in L2.
+constexpr int kClipU = 2;
+
+// One tile per CTA, the last tiles first: what the norm read last is still
+// in L2.
 template <typename TAB>
-__global__ void __launch_bounds__(kListThreads, kListCtas)
+__global__ void __launch_bounds__(kListThreads, 8)
 k_clip(const __grid_constant__ TAB tab, const float *clip) {
+    using T = Tile<kClipU>;
+    __shared__ ListEntry staged[T::kVecs + 1];
     pdl_enter();
-    const float c = __ldcg(clip + 1);
+    const float c = clip[1];
+    T tile{};
+    const bool one = tile.locate(tab, (int64_t)gridDim.x - 1 - blockIdx.x);
     if (c == 1.0f || isnan(c)) return;  // nothing changes; no step to take
-    const int b = blockIdx.x;
-    const int64_t v0 = tab.vecs * b / tab.grid;
-    const int64_t v1 = tab.vecs * (b + 1) / tab.grid;
-    for (int i = b + 1 < tab.grid ? tab.first[b + 1] : tab.count - 1; i >= tab.first[b]; --i) {
-        if ((int64_t)(tab.e[i].vec0_ends >> 8) >= v1) continue;
-        const Segment g = segment(tab, i, v0, v1);
-        uint4 *p = reinterpret_cast<uint4 *>(g.p);
-        for (int64_t q = g.hi - 1 - threadIdx.x; q >= g.lo; q -= kListBatch * kListThreads) {
-            uint4 w[kListBatch];
+    if (one) {
+        uint4 *p = reinterpret_cast<uint4 *>(tile.p) + threadIdx.x;
+        const int n = (int)(tile.v1 - tile.v0) - (int)threadIdx.x;
+        uint4 w[kClipU];
 #pragma unroll
-            for (int u = 0; u < kListBatch; ++u)
-                if (q - u * kListThreads >= g.lo) w[u] = p[q - u * kListThreads];
+        for (int u = 0; u < kClipU; ++u)
+            if (u * kListThreads < n) w[u] = p[u * kListThreads];
 #pragma unroll
-            for (int u = 0; u < kListBatch; ++u)
-                if (q - u * kListThreads >= g.lo) p[q - u * kListThreads] = scaled(w[u], g.kind, c);
-        }
-        const int64_t x = edge_element(g, g.kind == Z3_F32 ? 4 : 2);
-        if (x >= 0 && g.kind == Z3_F32) {
-            float *f = reinterpret_cast<float *>(g.p + x);
-            *f = __fmul_rn(*f, c);
-        } else if (x >= 0) {
-            uint16_t *h = reinterpret_cast<uint16_t *>(g.p + x);
-            *h = f32_to_bf16(__fmul_rn(bf16_to_f32(*h), c));
-        }
+        for (int u = 0; u < kClipU; ++u)
+            if (u * kListThreads < n) p[u * kListThreads] = scaled(w[u], tile.kind, c);
+        return;
     }
+    tile.stage(tab, staged);
+    VecRef r[kClipU];
+    uint4 w[kClipU];
+#pragma unroll
+    for (int u = 0; u < kClipU; ++u) {
+        r[u] = tile.ref(staged, u);
+        if (r[u].whole()) w[u] = *reinterpret_cast<const uint4 *>(r[u].p);
+    }
+#pragma unroll
+    for (int u = 0; u < kClipU; ++u)
+        if (r[u].whole()) *reinterpret_cast<uint4 *>(r[u].p) = scaled(w[u], r[u].kind, c);
+#pragma unroll
+    for (int u = 0; u < kClipU; ++u)
+        if (r[u].partial()) store_partial(r[u], scaled(load_partial(r[u]), r[u].kind, c));
 }
 
 // --------------------------------------------------------------------------
@@ -264,7 +455,7 @@ struct TileSum {
     float s;
     int e;
     __device__ __forceinline__ double value() const {
-        return (double)s * (e == 0 ? 1.0 : e < 0 ? 0x1p-200 : 0x1p+200);
+        return (double)s * (e == 0 ? 1.0 : e < 0 ? 0x1p-200 : 0x1p+160);
     }
 };
 
@@ -273,8 +464,8 @@ __device__ __forceinline__ TileSum tile_sum(const float g[8]) {
 #pragma unroll
     for (int l = 0; l < 8; ++l) s = __fmaf_rn(g[l], g[l], s);
     if (is_safe(s)) return {s, 0};
-    const int e = s < kSafeLo ? -200 : 200;
-    const float k = e < 0 ? 0x1p+100f : 0x1p-100f;
+    const int e = s < kSafeLo ? -200 : 160;
+    const float k = rescale(s);
     s = 0.0f;
 #pragma unroll
     for (int l = 0; l < 8; ++l) s = __fmaf_rn(g[l] * k, g[l] * k, s);
@@ -339,7 +530,7 @@ __device__ __noinline__ TileSum reduce_norm_edges(const ReduceNormArgs a, int n_
         s += (double)g * (double)g;
     }
     if (s == 0.0 || is_safe((float)s)) return {(float)s, 0};
-    return s < kSafeLo ? TileSum{(float)(s * 0x1p+200), -200} : TileSum{(float)(s * 0x1p-200), 200};
+    return s < kSafeLo ? TileSum{(float)(s * 0x1p+200), -200} : TileSum{(float)(s * 0x1p-160), 160};
 }
 
 template <bool ALIGNED, bool ACC, bool EARLY>
@@ -441,15 +632,37 @@ int32_t fill(TAB &tab, const z3_tensor *tensors, int32_t n, int32_t at) {
     tab.e[tab.count].base_kind = 0;
     tab.e[tab.count].vec0_ends = (uint64_t)vecs << 8;
     tab.vecs = vecs;
-    tab.grid = (int32_t)std::min<int64_t>(kListMaxGrid,
-                                          std::max<int64_t>(1, vecs / (2 * kListThreads)));
+    tab.shift = 0;
+    while ((vecs >> tab.shift) >= kListBuckets) ++tab.shift;
     int32_t i = 0;
-    for (int32_t b = 0; b < tab.grid; ++b) {
-        const uint64_t v0 = (uint64_t)(vecs * b / tab.grid);
-        while (i + 1 < tab.count && (tab.e[i + 1].vec0_ends >> 8) <= v0) ++i;
+    for (int64_t b = 0; b <= (vecs >> tab.shift) + 1; ++b) {
+        while (i + 1 < tab.count && (int64_t)(tab.e[i + 1].vec0_ends >> 8) <= b << tab.shift) ++i;
         tab.first[b] = (uint16_t)i;
     }
     return at;
+}
+
+template <int U, typename TAB>
+int64_t tiles_of(const TAB &tab) {
+    return (tab.vecs + U * kListThreads - 1) / (U * kListThreads);
+}
+
+// launch() for a kernel with a table, which it does not copy on its way to
+// the runtime.
+template <typename TAB, typename ARG>
+void launch_list(void (*kernel)(TAB, ARG), int64_t grid, cudaStream_t stream, const TAB &tab,
+                 const ARG &arg) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)kListThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[2] = {const_cast<TAB *>(&tab), const_cast<ARG *>(&arg)};
+    (void)cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), args);
 }
 
 template <typename TAB>
@@ -460,7 +673,11 @@ void norm_launches(const z3_tensor *tensors, int32_t n, NormOut o, cudaStream_t 
     do {
         at = fill(tab, tensors, n, at);
         o.last = at == n;
-        launch(k_grad_norm<TAB>, tab.grid, kListThreads, stream, tab, o);
+        const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kNormMaxGrid,
+                                                                    tiles_of<kNormU>(tab)));
+        o.alone = o.first && o.last && grid == 1;
+        launch_list(k_grad_norm<TAB>, grid, stream, tab, o);
+        if (!o.alone) launch(k_norm_finish, 1, kFinishThreads, stream, o, (int)grid);
         o.first = 0;
     } while (at < n);
 }
@@ -470,7 +687,8 @@ void clip_launches(const z3_tensor *tensors, int32_t n, const float *clip, cudaS
     TAB tab;
     for (int32_t at = 0; at < n;) {
         at = fill(tab, tensors, n, at);
-        if (tab.count > 0) launch(k_clip<TAB>, tab.grid, kListThreads, stream, tab, clip);
+        if (tab.count > 0)
+            launch_list(k_clip<TAB>, tiles_of<kClipU>(tab), stream, tab, clip);
     }
 }
 
@@ -482,8 +700,9 @@ void clip_launches(const z3_tensor *tensors, int32_t n, const float *clip, cudaS
 
 cudaError_t launch_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm, float *clip,
                              NormWorkspace *ws, cudaStream_t stream) {
-    const NormOut o{clip, ws, max_norm, 0, 0};
+    const NormOut o{clip, ws, max_norm, 0, 0, 0};
     if (n <= ListSmall::kCap) norm_launches<ListSmall>(tensors, n, o, stream);
+    else if (n <= ListMedium::kCap) norm_launches<ListMedium>(tensors, n, o, stream);
     else norm_launches<ListLarge>(tensors, n, o, stream);
     return cudaGetLastError();
 }
@@ -491,6 +710,7 @@ cudaError_t launch_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm
 cudaError_t launch_clip(const z3_tensor *tensors, int32_t n, const float *clip,
                         cudaStream_t stream) {
     if (n <= ListSmall::kCap) clip_launches<ListSmall>(tensors, n, clip, stream);
+    else if (n <= ListMedium::kCap) clip_launches<ListMedium>(tensors, n, clip, stream);
     else clip_launches<ListLarge>(tensors, n, clip, stream);
     return cudaGetLastError();
 }

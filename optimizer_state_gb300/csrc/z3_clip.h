@@ -13,12 +13,11 @@
 namespace z3 {
 
 // A list of tensors is walked as one run of 16-byte vectors, each tensor
-// contributing the aligned vectors that its bytes touch.  Every CTA takes an
-// equal, contiguous share of the run, so tensors of any lengths balance.
+// contributing the aligned vectors that its bytes touch, and the run is cut
+// into tiles of kListTile vectors, whatever the tensors' lengths.
 constexpr int kSMs = 152;
-constexpr int kListThreads = 512;
-constexpr int kListCtas = 3;  // resident on an SM
-constexpr int kListMaxGrid = kListCtas * kSMs;
+constexpr int kListThreads = 256;
+constexpr int kListBuckets = 512;
 
 struct ListEntry {
     uint64_t base_kind;  // address rounded down to 16 bytes | z3_dtype
@@ -27,29 +26,32 @@ struct ListEntry {
                          // tensor starts and (0: on a boundary) ends
 };
 
-// One launch's tensors (a kernel parameter).  first[b] is the entry in which
-// CTA b's share starts; entry `count` only closes the last tensor.
+// One launch's tensors (a kernel parameter).  first[b] is the entry that
+// holds vector b << shift, so that a lookup searches between two buckets
+// only; entry `count` closes the last tensor.
 template <int CAP>
 struct ListTab {
     static constexpr int kCap = CAP;
     int32_t count;
-    int32_t grid;
+    int32_t shift;
     int64_t vecs;
-    uint16_t first[kListMaxGrid];
+    uint16_t first[kListBuckets + 2];
     ListEntry e[CAP + 1];
 };
 
-// Two sizes: the first stays within the classic 4 KB of kernel parameters,
-// the second within the 32,764 bytes that sm_103 takes.
-using ListSmall = ListTab<160>;
+// The first size stays within the classic 4 KB of kernel parameters, the
+// last within the 32,764 bytes that sm_103 takes; copying a table to the GPU
+// costs a launch 3 us at the last size.
+using ListSmall = ListTab<180>;
+using ListMedium = ListTab<700>;
 using ListLarge = ListTab<1900>;
 
-// Device workspace of z3_grad_norm; zero-filled once by the caller.
+// Device workspace of z3_grad_norm.
+constexpr int kNormCtas = 7;                     // resident on an SM
+constexpr int kNormMaxGrid = kNormCtas * kSMs;
 struct NormWorkspace {
-    uint32_t ticket;  // CTAs that have stored their partial; 0 between launches
-    uint32_t pad_;
-    double carry;     // sum over the earlier launches of a call
-    double partial[kListMaxGrid];
+    double partial[kNormMaxGrid];  // one per CTA of a launch
+    double carry;                  // sum over the earlier launches of a call
 };
 
 struct NormOut {
@@ -57,7 +59,8 @@ struct NormOut {
     NormWorkspace *ws;
     float max_norm;
     int32_t first;  // this launch is the call's first: no carry
-    int32_t last;   // and its last: write clip
+    int32_t last;   // its last: write clip
+    int32_t alone;  // both, with one CTA: no partials
 };
 
 struct ReduceNormArgs {

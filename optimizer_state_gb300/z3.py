@@ -11,6 +11,7 @@ with an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -160,7 +161,9 @@ def _check(status: int):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: torch.cuda.current_stream() builds a stream object
+        # around it, which takes as long as a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -414,19 +417,23 @@ class TensorList:
         return self.n
 
 
-def grad_norm_workspace(device=None):
-    """A zero-filled workspace for z3_grad_norm and z3_model_step_clipped."""
-    import torch
+@functools.cache
+def _workspace_bytes() -> int:
     n = ctypes.c_int64()
     _check(load().z3_grad_norm_workspace_bytes(ctypes.byref(n)))
-    return torch.zeros(n.value, dtype=torch.uint8, device="cuda" if device is None else device)
+    return n.value
+
+
+def grad_norm_workspace(device=None):
+    """A workspace for z3_grad_norm and z3_model_step_clipped."""
+    import torch
+    return torch.empty(_workspace_bytes(), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
 
 
 def _workspace(t):
     import torch
-    n = ctypes.c_int64()
-    _check(load().z3_grad_norm_workspace_bytes(ctypes.byref(n)))
-    return _dev(t, (torch.uint8,), n.value, "workspace")
+    return _dev(t, (torch.uint8,), _workspace_bytes(), "workspace")
 
 
 def z3_grad_norm(tensors, max_norm: float, clip, workspace, stream=None):
