@@ -303,27 +303,42 @@ typedef struct z3_tensor {
     int32_t reserved;
 } z3_tensor;
 
+/* Opaque, library-owned host object: a list of tensors, checked and laid out
+ * for the kernels once.  It holds their addresses, not their contents:
+ * gradients that are written to the same buffers every step keep their list,
+ * others need a new one.  Immutable after creation; may be shared between
+ * threads. */
+typedef struct z3_tensor_list z3_tensor_list;
+
+/* Makes a list of n tensors, of different types and lengths, in any order;
+ * they may be empty and, for the norm, overlap.  n = 0 is an empty list.  On
+ * success *out owns host memory released by z3_tensor_list_destroy.  Errors:
+ * out NULL, n < 0, tensors NULL (n > 0), a negative numel, data NULL, an
+ * unknown dtype (INVALID_ARG); data not aligned to its element (ALIGNMENT);
+ * a size beyond the address space (OVERFLOW). */
+z3_status z3_tensor_list_create(const z3_tensor *tensors, int32_t n, z3_tensor_list **out);
+
+/* Releases a list (NULL is a no-op). */
+void z3_tensor_list_destroy(z3_tensor_list *list);
+
 /* Bytes of z3_grad_norm's workspace (device memory, 16-byte aligned).  What
  * it holds before a call does not matter, and nothing is kept in it from one
  * call for the next; calls that may overlap on the GPU need one each. */
 z3_status z3_grad_norm_workspace_bytes(int64_t *bytes);
 
-/* The global norm of n tensors and its factor, written to clip (float [2],
- * device).  The tensors are read; they may be of different types, may
- * overlap and may be empty (n = 0: norm 0).  A Z3_SUMSQ tensor adds its
- * elements as they are.  max_norm > 0; +Inf measures without clipping.
- * Errors: n < 0, tensors NULL (n > 0), a negative numel, an unknown dtype,
- * max_norm not > 0, clip or workspace overlapping a tensor or each other
- * (INVALID_ARG); data not aligned to its element (ALIGNMENT); a size beyond
- * int64 (OVERFLOW). */
-z3_status z3_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm, float *clip,
+/* The global norm of the list's tensors and its factor, written to clip
+ * (float [2], device).  A Z3_SUMSQ tensor adds its elements as they are; an
+ * empty list has the norm 0.  max_norm > 0; +Inf measures without clipping.
+ * Errors: max_norm not > 0, clip or workspace overlapping a tensor or each
+ * other (INVALID_ARG). */
+z3_status z3_grad_norm(const z3_tensor_list *list, float max_norm, float *clip,
                        void *workspace, z3_stream stream);
 
-/* Clips n tensors in place: g = coef * g in binary32, rounded once to the
- * tensor's type.  Nothing is written where coef is 1 or NaN.  clip is read.
- * Errors: those of z3_grad_norm, a Z3_SUMSQ tensor, and tensors that overlap
- * one another or clip (INVALID_ARG). */
-z3_status z3_clip(const z3_tensor *tensors, int32_t n, const float *clip, z3_stream stream);
+/* Clips the list's tensors in place: g = coef * g in binary32, rounded once to
+ * the tensor's type.  Nothing is written where coef is 1 or NaN.  clip is
+ * read.  Errors: a Z3_SUMSQ tensor, tensors that overlap one another or clip
+ * (INVALID_ARG). */
+z3_status z3_clip(const z3_tensor_list *list, const float *clip, z3_stream stream);
 
 /* Length (doubles) of the sumsq buffer of z3_reduce_scatter_norm. */
 z3_status z3_sumsq_len(const z3_layout *layout, int64_t *len);

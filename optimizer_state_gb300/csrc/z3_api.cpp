@@ -369,61 +369,19 @@ z3_status check_clip_unit(const char *fn, const z3_layout *L, const z3_clip_unit
     return st;
 }
 
-// Checks a list of tensors; with `written`, also that it holds no sums and
-// that its tensors are disjoint.  `others` are buffers that must not overlap
-// a tensor.
-z3_status check_list(const char *fn, const z3_tensor *tensors, int32_t n, const Buf *others,
-                     int n_others, bool written) {
-    const std::string name = fn;
-    auto at = [&](int32_t i) { return name + ": tensors[" + std::to_string(i) + "]"; };
-    if (n < 0) return fail(Z3_ERR_INVALID_ARG, name + ": n < 0");
-    if (n > 0 && tensors == nullptr) return fail(Z3_ERR_INVALID_ARG, name + ": tensors is NULL");
-    uintptr_t past = 0;         // the end of the tensors so far, while they ascend
-    bool ascending = true;
-    for (int32_t i = 0; i < n; ++i) {
-        const z3_tensor &t = tensors[i];
-        if (t.dtype != Z3_BF16 && t.dtype != Z3_F32 && t.dtype != Z3_SUMSQ)
-            return fail(Z3_ERR_INVALID_ARG, at(i) + ": unknown dtype");
-        if (written && t.dtype == Z3_SUMSQ)
-            return fail(Z3_ERR_INVALID_ARG, at(i) + " holds sums of squares: nothing to clip");
-        if (t.numel < 0) return fail(Z3_ERR_INVALID_ARG, at(i) + ": numel < 0");
-        if (t.numel == 0) continue;
-        if (t.data == nullptr) return fail(Z3_ERR_INVALID_ARG, at(i) + ": data is NULL");
-        const int64_t size = list_dtype_bytes(t.dtype);
+// A buffer of the call that must not overlap a listed tensor.
+z3_status check_apart(const char *fn, const z3_tensor_list *list, const Buf &buf) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(buf.ptr), z = a + (uintptr_t)buf.bytes;
+    if (a >= list->hi || z <= list->lo) return Z3_OK;
+    for (size_t i = 0; i < list->tensors.size(); ++i) {
+        const z3_tensor &t = list->tensors[i];
         const uintptr_t lo = reinterpret_cast<uintptr_t>(t.data);
-        int64_t bytes;
-        uintptr_t hi;
-        if (__builtin_mul_overflow(t.numel, size, &bytes) ||
-            __builtin_add_overflow(lo, (uintptr_t)bytes, &hi) || hi > (uintptr_t)INT64_MAX >> 8)
-            return fail(Z3_ERR_OVERFLOW, at(i) + ": size overflows");
-        if (lo % (uintptr_t)size != 0)
-            return fail(Z3_ERR_ALIGNMENT, at(i) + " is not aligned to its elements");
-        for (int k = 0; k < n_others; ++k) {
-            const uintptr_t o = reinterpret_cast<uintptr_t>(others[k].ptr);
-            if (lo < o + (uintptr_t)others[k].bytes && o < hi)
-                return fail(Z3_ERR_INVALID_ARG, at(i) + " overlaps " + others[k].name);
-        }
-        ascending = ascending && lo >= past;
-        past = hi;
+        const int64_t size = t.dtype == Z3_BF16 ? 2 : t.dtype == Z3_F32 ? 4 : 8;
+        if (lo < z && a < lo + (uintptr_t)(t.numel * size))
+            return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": tensors[" +
+                                                std::to_string(list->index[i]) + "] overlaps " +
+                                                buf.name);
     }
-    if (!written || ascending) return Z3_OK;
-    struct Extent {
-        uintptr_t lo, hi;
-        int32_t i;
-    };
-    std::vector<Extent> ext;
-    ext.reserve((size_t)n);
-    for (int32_t i = 0; i < n; ++i) {
-        if (tensors[i].numel == 0) continue;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(tensors[i].data);
-        ext.push_back({lo, lo + (uintptr_t)(tensors[i].numel * list_dtype_bytes(tensors[i].dtype)),
-                       i});
-    }
-    std::sort(ext.begin(), ext.end(), [](const Extent &a, const Extent &b) { return a.lo < b.lo; });
-    for (size_t k = 1; k < ext.size(); ++k)
-        if (ext[k].lo < ext[k - 1].hi)
-            return fail(Z3_ERR_INVALID_ARG, at(ext[k].i) + " overlaps tensors[" +
-                                                std::to_string(ext[k - 1].i) + "]");
     return Z3_OK;
 }
 }  // namespace
@@ -442,38 +400,38 @@ extern "C" z3_status z3_sumsq_len(const z3_layout *L, int64_t *len) {
     return Z3_OK;
 }
 
-extern "C" z3_status z3_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm,
-                                  float *clip, void *workspace, z3_stream stream) {
+extern "C" z3_status z3_grad_norm(const z3_tensor_list *list, float max_norm, float *clip,
+                                  void *workspace, z3_stream stream) {
     const char *fn = "z3_grad_norm";
-    try {
-        z3_status st = check_clip_out(fn, max_norm, clip, workspace);
-        if (st != Z3_OK) return st;
-        const Buf others[2] = {{clip, 8, "clip"},
-                               {workspace, sizeof(NormWorkspace), "workspace"}};
-        st = check_list(fn, tensors, n, others, 2, false);
-        if (st != Z3_OK) return st;
-        Range range("z3/grad_norm");
-        return launched(fn, launch_grad_norm(tensors, n, max_norm, clip,
-                                             (NormWorkspace *)workspace, (cudaStream_t)stream));
-    } catch (const std::bad_alloc &) {
-        return fail_host_memory(fn);
-    }
+    if (list == nullptr) return fail(Z3_ERR_INVALID_ARG, "z3_grad_norm: list is NULL");
+    z3_status st = check_clip_out(fn, max_norm, clip, workspace);
+    if (st != Z3_OK) return st;
+    st = check_apart(fn, list, {clip, 8, "clip"});
+    if (st != Z3_OK) return st;
+    st = check_apart(fn, list, {workspace, sizeof(NormWorkspace), "workspace"});
+    if (st != Z3_OK) return st;
+    Range range("z3/grad_norm");
+    return launched(fn, launch_grad_norm(list, max_norm, clip, (NormWorkspace *)workspace,
+                                         (cudaStream_t)stream));
 }
 
-extern "C" z3_status z3_clip(const z3_tensor *tensors, int32_t n, const float *clip,
-                             z3_stream stream) {
+extern "C" z3_status z3_clip(const z3_tensor_list *list, const float *clip, z3_stream stream) {
     const char *fn = "z3_clip";
-    try {
-        const Buf others[1] = {{clip, 8, "clip"}};
-        z3_status st = check_bufs(fn, others, 1);
-        if (st != Z3_OK) return st;
-        st = check_list(fn, tensors, n, others, 1, true);
-        if (st != Z3_OK) return st;
-        Range range("z3/clip");
-        return launched(fn, launch_clip(tensors, n, clip, (cudaStream_t)stream));
-    } catch (const std::bad_alloc &) {
-        return fail_host_memory(fn);
-    }
+    if (list == nullptr) return fail(Z3_ERR_INVALID_ARG, "z3_clip: list is NULL");
+    if (list->sums >= 0)
+        return fail(Z3_ERR_INVALID_ARG, "z3_clip: tensors[" + std::to_string(list->sums) +
+                                            "] holds sums of squares: nothing to clip");
+    if (list->clash[0] >= 0)
+        return fail(Z3_ERR_INVALID_ARG, "z3_clip: tensors[" + std::to_string(list->clash[0]) +
+                                            "] overlaps tensors[" +
+                                            std::to_string(list->clash[1]) + "]");
+    const Buf bufs[1] = {{clip, 8, "clip"}};
+    z3_status st = check_bufs(fn, bufs, 1);
+    if (st != Z3_OK) return st;
+    st = check_apart(fn, list, bufs[0]);
+    if (st != Z3_OK) return st;
+    Range range("z3/clip");
+    return launched(fn, launch_clip(list, clip, (cudaStream_t)stream));
 }
 
 extern "C" z3_status z3_reduce_scatter_norm(const z3_layout *L, const uint16_t *grads,
@@ -503,8 +461,7 @@ extern "C" z3_status z3_adam_shard_step_clipped(const z3_layout *L, float *maste
                                                 z3_stream stream) {
     const char *fn = "z3_adam_shard_step_clipped";
     if (L == nullptr) return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": layout is NULL");
-    AdamClipArgs c{};
-    AdamArgs &a = c.a;
+    AdamArgs a{};
     z3_status st = adam_constants(fn, hp, step, &a.k);
     if (st != Z3_OK) return st;
     const int64_t T = L->psi_padded;
@@ -520,11 +477,10 @@ extern "C" z3_status z3_adam_shard_step_clipped(const z3_layout *L, float *maste
     a.grad = grad_shards;
     a.shards = shards;
     a.total = T;
-    c.clip = clip;
     if (flat_blocks(T, kAdamThreads) > 0x7fffffff)
         return fail(Z3_ERR_OVERFLOW, std::string(fn) + ": grid too large");
     Range range("z3/Adam(clipped)");
-    return launched(fn, launch_adam_clipped(c, (cudaStream_t)stream, false));
+    return launched(fn, launch_adam_clipped(&a, 1, clip, (cudaStream_t)stream));
 }
 
 namespace {
@@ -583,7 +539,11 @@ z3_status model_step(const char *fn, const z3_unit *units, int32_t n_units,
     std::vector<ReduceArgs> args((size_t)n_units);
     std::vector<int64_t> grad_bytes((size_t)n_units, 0);
     std::vector<z3_tensor> sums;   // every unit's sums of squares: the norm's list
-    if (c != nullptr) sums.reserve((size_t)n_units);
+    std::vector<AdamArgs> updates; // every unit's update
+    if (c != nullptr) {
+        sums.reserve((size_t)n_units);
+        updates.reserve((size_t)n_units);
+    }
     for (int32_t i = 0; i < n_units; ++i) {
         const z3_unit &u = units[i];
         z3_status st = prepare_rs_adam(fn, u.layout, u.grads, u.grad_stride, u.scale, nullptr,
@@ -599,6 +559,10 @@ z3_status model_step(const char *fn, const z3_unit *units, int32_t n_units,
         if (c != nullptr) {
             st = check_clip_unit(fn, u.layout, c->units[i], &sums);
             if (st != Z3_OK) return st;
+            if (flat_blocks(T, kAdamThreads) > 0x7fffffff)
+                return fail(Z3_ERR_OVERFLOW, name + ": grid too large");
+            updates.push_back({u.master, u.m, u.v, c->units[i].grad_shards, u.shards, T,
+                               args[(size_t)i].k});
         }
         for (int32_t k = 0; k < n_full; ++k) {
             const Buf bufs[7] = {{full[k], full_bytes, "full[k]"},
@@ -688,6 +652,11 @@ z3_status model_step(const char *fn, const z3_unit *units, int32_t n_units,
             open.push_back(&x);
         }
     }
+    z3_tensor_list norm_list;
+    if (c != nullptr) {
+        z3_status st = build_list(fn, sums.data(), (int32_t)sums.size(), &norm_list);
+        if (st != Z3_OK) return st;
+    }
     const cudaStream_t s = (cudaStream_t)stream;
     const int nb = n_full;
     std::vector<bool> buffer_used((size_t)nb, false);
@@ -724,35 +693,25 @@ z3_status model_step(const char *fn, const z3_unit *units, int32_t n_units,
         return run_allgather(L, units[i].shards, units[i].resident, s, false);
     };
     // The rest of a clipped step, once every unit is reduced: the norm, every
-    // unit's update, and the resident units' gathers.  Units go in forward
-    // order, the reverse of the backward pass: the gradients reduced last are
-    // still in L2.  The first update reads what the norm kernel before it
-    // writes; a later one follows an update of another unit (or its resident
-    // gather), which writes nothing that it reads.
+    // unit's update, and the resident units' gathers.
     auto finish = [&]() -> z3_status {
         if (c == nullptr) return Z3_OK;
         {
             Range r("z3/grad_norm");
-            z3_status fs = launched(fn, launch_grad_norm(sums.data(), (int32_t)sums.size(),
-                                                         c->max_norm, c->clip,
+            z3_status fs = launched(fn, launch_grad_norm(&norm_list, c->max_norm, c->clip,
                                                          (NormWorkspace *)c->workspace, s));
             if (fs != Z3_OK) return fs;
         }
-        bool early = false;
+        {
+            Range r("z3/Adam(clipped)");
+            z3_status fs = launched(fn, launch_adam_clipped(updates.data(), n_units, c->clip, s));
+            if (fs != Z3_OK) return fs;
+        }
         for (int32_t i = 0; i < n_units; ++i) {
             const z3_unit &u = units[i];
-            const int64_t T = u.layout->psi_padded;
-            if (T == 0) continue;
-            Range r("z3/Adam(clipped)");
-            const AdamClipArgs a{{u.master, u.m, u.v, c->units[i].grad_shards, u.shards, T,
-                                  args[(size_t)i].k},
-                                 c->clip};
-            z3_status fs = launched(fn, launch_adam_clipped(a, s, early));
-            if (fs != Z3_OK) return fs;
-            early = true;
-            if (u.resident == nullptr) continue;
-            Range r2("z3/AllGather(resident)");
-            fs = run_allgather(u.layout, u.shards, u.resident, s, false);
+            if (u.resident == nullptr || u.layout->psi == 0) continue;
+            Range r("z3/AllGather(resident)");
+            z3_status fs = run_allgather(u.layout, u.shards, u.resident, s, false);
             if (fs != Z3_OK) return fs;
         }
         return Z3_OK;

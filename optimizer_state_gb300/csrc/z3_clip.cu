@@ -15,13 +15,23 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <limits>
+#include <vector>
 
 #include "z3_clip.h"
 #include "z3_device.cuh"
 
 namespace z3 {
 namespace {
+
+// pdl_enter() the other way round: the next kernel may start before this
+// one's primary has completed, so that it is resident by the time this short
+// kernel ends (reduce-scatter with norm of a d = 1024 layer, one after the
+// other: 45 us, against 49).  The next kernel still waits for this one,
+// which completes after its primary; it must not be one that reads early.
+__device__ __forceinline__ void pdl_enter_early() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // --------------------------------------------------------------------------
 // sums of squares
@@ -368,7 +378,7 @@ k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
 // taken by every CTA and a last one's sum: 912 tickets at one address took
 // 1 us more, one ticket 2 us.
 __global__ void __launch_bounds__(kFinishThreads) k_norm_finish(const NormOut o, int n) {
-    pdl_enter();
+    pdl_enter_early();
     constexpr int PER = (kNormMaxGrid + kFinishThreads - 1) / kFinishThreads;
     double x[PER];  // all loads in flight at once
 #pragma unroll
@@ -570,20 +580,31 @@ k_reduce_norm(const __grid_constant__ Tab tab, const ReduceNormArgs a) {
 }
 
 // --------------------------------------------------------------------------
-// Adam over the flat [N][S] shard buffers on coef * gradient
+// Adam over the flat [N][S] shard buffers of one or several units, on coef *
+// gradient
 // --------------------------------------------------------------------------
 
-template <bool EARLY>
-__global__ void __launch_bounds__(kAdamThreads) k_adam_clipped(const AdamClipArgs c) {
-    if constexpr (!EARLY) pdl_enter();
-    const AdamArgs &a = c.a;
-    const int64_t x0 = ((int64_t)blockIdx.x * kAdamThreads + threadIdx.x) * kVec;
-    const float coef = __ldcg(c.clip + 1);
-    if (isnan(coef)) {  // no step to take
-        if constexpr (EARLY) pdl_enter();
-        return;
+// Bound by HBM: 16 bytes read and 14 written per element.  One launch for all
+// units: the 25 updates of the 24-layer model took 1.57 ms as launches of
+// their own, 1.51 ms as one.  Reading the state before the wait for the norm
+// did not help (a d = 1024 layer's step: 113 us with it, 111 without).
+template <typename UNITS>
+__global__ void __launch_bounds__(kAdamThreads)
+k_adam_clipped(const __grid_constant__ UNITS units, const float *clip) {
+    pdl_enter();
+    const float coef = clip[1];
+    if (isnan(coef)) return;  // no step to take
+    int i = 0;
+    if constexpr (UNITS::kCap > 1) {
+        int hi = units.count - 1;
+        while (i < hi) {
+            const int mid = (i + hi + 1) >> 1;
+            if (units.block0[mid] <= blockIdx.x) i = mid; else hi = mid - 1;
+        }
     }
-    if (x0 >= a.total) return;
+    const AdamArgs &a = units.u[i];
+    const int64_t x0 =
+        ((int64_t)(blockIdx.x - units.block0[i]) * kAdamThreads + threadIdx.x) * kVec;
     if (x0 + kVec <= a.total) {
         float g[8], p[8], m[8], v[8];
         ld8f(a.grad + x0, g);
@@ -592,13 +613,11 @@ __global__ void __launch_bounds__(kAdamThreads) k_adam_clipped(const AdamClipArg
         ld8f(a.v + x0, v);
 #pragma unroll
         for (int l = 0; l < 8; ++l) adam1(__fmul_rn(g[l], coef), p[l], m[l], v[l], a.k);
-        if constexpr (EARLY) pdl_enter();
         st8f(a.master + x0, p);
         st8f(a.m + x0, m);
         st8f(a.v + x0, v);
         *reinterpret_cast<uint4 *>(a.shards + x0) = pack8(p);
     } else {
-        if constexpr (EARLY) pdl_enter();
         for (int64_t x = x0; x < a.total; ++x) {
             float p = a.master[x], m = a.m[x], v = a.v[x];
             adam1(__fmul_rn(a.grad[x], coef), p, m, v, a.k);
@@ -611,41 +630,8 @@ __global__ void __launch_bounds__(kAdamThreads) k_adam_clipped(const AdamClipArg
 }
 
 // --------------------------------------------------------------------------
-// launch tables of a tensor list
+// launches over a tensor list
 // --------------------------------------------------------------------------
-
-// Fills tab from tensors[at...], as many as it holds; returns the next index.
-template <typename TAB>
-int32_t fill(TAB &tab, const z3_tensor *tensors, int32_t n, int32_t at) {
-    tab.count = 0;
-    int64_t vecs = 0;
-    for (; at < n && tab.count < TAB::kCap; ++at) {
-        const z3_tensor &t = tensors[at];
-        if (t.numel == 0) continue;
-        const uint64_t a = reinterpret_cast<uintptr_t>(t.data);
-        const uint64_t z = a + (uint64_t)(t.numel * list_dtype_bytes(t.dtype));
-        ListEntry &e = tab.e[tab.count++];
-        e.base_kind = (a & ~(uint64_t)15) | (uint64_t)t.dtype;
-        e.vec0_ends = (uint64_t)vecs << 8 | (a & 15) << 4 | (z & 15);
-        vecs += (int64_t)((z + 15) / 16 - a / 16);
-    }
-    tab.e[tab.count].base_kind = 0;
-    tab.e[tab.count].vec0_ends = (uint64_t)vecs << 8;
-    tab.vecs = vecs;
-    tab.shift = 0;
-    while ((vecs >> tab.shift) >= kListBuckets) ++tab.shift;
-    int32_t i = 0;
-    for (int64_t b = 0; b <= (vecs >> tab.shift) + 1; ++b) {
-        while (i + 1 < tab.count && (int64_t)(tab.e[i + 1].vec0_ends >> 8) <= b << tab.shift) ++i;
-        tab.first[b] = (uint16_t)i;
-    }
-    return at;
-}
-
-template <int U, typename TAB>
-int64_t tiles_of(const TAB &tab) {
-    return (tab.vecs + U * kListThreads - 1) / (U * kListThreads);
-}
 
 // launch() for a kernel with a table, which it does not copy on its way to
 // the runtime.
@@ -665,31 +651,28 @@ void launch_list(void (*kernel)(TAB, ARG), int64_t grid, cudaStream_t stream, co
     (void)cudaLaunchKernelExC(&cfg, reinterpret_cast<const void *>(kernel), args);
 }
 
-template <typename TAB>
-void norm_launches(const z3_tensor *tensors, int32_t n, NormOut o, cudaStream_t stream) {
-    TAB tab;
-    int32_t at = 0;
-    o.first = 1;
-    do {
-        at = fill(tab, tensors, n, at);
-        o.last = at == n;
-        const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kNormMaxGrid,
-                                                                    tiles_of<kNormU>(tab)));
-        o.alone = o.first && o.last && grid == 1;
-        launch_list(k_grad_norm<TAB>, grid, stream, tab, o);
-        if (!o.alone) launch(k_norm_finish, 1, kFinishThreads, stream, o, (int)grid);
-        o.first = 0;
-    } while (at < n);
+template <int U, typename TAB>
+int64_t tiles_of(const TAB &tab) {
+    return (tab.vecs + U * kListThreads - 1) / (U * kListThreads);
 }
 
 template <typename TAB>
-void clip_launches(const z3_tensor *tensors, int32_t n, const float *clip, cudaStream_t stream) {
-    TAB tab;
-    for (int32_t at = 0; at < n;) {
-        at = fill(tab, tensors, n, at);
-        if (tab.count > 0)
-            launch_list(k_clip<TAB>, tiles_of<kClipU>(tab), stream, tab, clip);
+void norm_launches(const std::vector<TAB> &tabs, NormOut o, cudaStream_t stream) {
+    for (const TAB &tab : tabs) {
+        const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(kNormMaxGrid,
+                                                                    tiles_of<kNormU>(tab)));
+        o.first = &tab == &tabs.front();
+        o.last = &tab == &tabs.back();
+        o.alone = o.first && o.last && grid == 1;
+        launch_list(k_grad_norm<TAB>, grid, stream, tab, o);
+        if (!o.alone) launch(k_norm_finish, 1, kFinishThreads, stream, o, (int)grid);
     }
+}
+
+template <typename TAB>
+void clip_launches(const std::vector<TAB> &tabs, const float *clip, cudaStream_t stream) {
+    for (const TAB &tab : tabs)
+        if (tab.count > 0) launch_list(k_clip<TAB>, tiles_of<kClipU>(tab), stream, tab, clip);
 }
 
 }  // namespace
@@ -698,20 +681,19 @@ void clip_launches(const z3_tensor *tensors, int32_t n, const float *clip, cudaS
 // launchers
 // --------------------------------------------------------------------------
 
-cudaError_t launch_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm, float *clip,
+cudaError_t launch_grad_norm(const z3_tensor_list *list, float max_norm, float *clip,
                              NormWorkspace *ws, cudaStream_t stream) {
     const NormOut o{clip, ws, max_norm, 0, 0, 0};
-    if (n <= ListSmall::kCap) norm_launches<ListSmall>(tensors, n, o, stream);
-    else if (n <= ListMedium::kCap) norm_launches<ListMedium>(tensors, n, o, stream);
-    else norm_launches<ListLarge>(tensors, n, o, stream);
+    norm_launches(list->small, o, stream);
+    norm_launches(list->medium, o, stream);
+    norm_launches(list->large, o, stream);
     return cudaGetLastError();
 }
 
-cudaError_t launch_clip(const z3_tensor *tensors, int32_t n, const float *clip,
-                        cudaStream_t stream) {
-    if (n <= ListSmall::kCap) clip_launches<ListSmall>(tensors, n, clip, stream);
-    else if (n <= ListMedium::kCap) clip_launches<ListMedium>(tensors, n, clip, stream);
-    else clip_launches<ListLarge>(tensors, n, clip, stream);
+cudaError_t launch_clip(const z3_tensor_list *list, const float *clip, cudaStream_t stream) {
+    clip_launches(list->small, clip, stream);
+    clip_launches(list->medium, clip, stream);
+    clip_launches(list->large, clip, stream);
     return cudaGetLastError();
 }
 
@@ -740,10 +722,29 @@ cudaError_t launch_reduce_norm(const z3_layout *L, const ReduceNormArgs &a, bool
     return cudaGetLastError();
 }
 
-cudaError_t launch_adam_clipped(const AdamClipArgs &a, cudaStream_t stream, bool early) {
-    const int64_t blocks = flat_blocks(a.a.total, kAdamThreads);
-    if (early) launch(k_adam_clipped<true>, blocks, kAdamThreads, stream, a);
-    else launch(k_adam_clipped<false>, blocks, kAdamThreads, stream, a);
+namespace {
+template <typename UNITS>
+void adam_launches(const AdamArgs *a, int32_t n, const float *clip, cudaStream_t stream) {
+    UNITS t;
+    for (int32_t i = 0; i < n;) {
+        int64_t blocks = 0;
+        for (t.count = 0; i < n && t.count < UNITS::kCap; ++i) {
+            const int64_t b = flat_blocks(a[i].total, kAdamThreads);
+            if (b == 0) continue;
+            if (t.count > 0 && blocks + b > 0x7fffffff) break;
+            t.block0[t.count] = (uint32_t)blocks;
+            t.u[t.count++] = a[i];
+            blocks += b;
+        }
+        if (t.count > 0) launch(k_adam_clipped<UNITS>, blocks, kAdamThreads, stream, t, clip);
+    }
+}
+}  // namespace
+
+cudaError_t launch_adam_clipped(const AdamArgs *a, int32_t n, const float *clip,
+                                cudaStream_t stream) {
+    if (n == 1) adam_launches<AdamUnits<1>>(a, n, clip, stream);
+    else adam_launches<AdamUnits<40>>(a, n, clip, stream);
     return cudaGetLastError();
 }
 

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <vector>
 
 #include "z3_launch.h"
 
@@ -54,6 +55,23 @@ struct NormWorkspace {
     double carry;                  // sum over the earlier launches of a call
 };
 
+}  // namespace z3
+
+// Immutable once built.  Its tables are of the least size that holds all
+// tensors in one launch, or several of the largest.
+struct z3_tensor_list {
+    std::vector<z3_tensor> tensors;     // those with elements
+    std::vector<int32_t> index;         // their places in the caller's list
+    uintptr_t lo = UINTPTR_MAX, hi = 0; // the addresses they span
+    int32_t sums = -1;                  // a tensor that holds sums of squares, if any
+    int32_t clash[2] = {-1, -1};        // two tensors that overlap, if any do
+    std::vector<z3::ListSmall> small;
+    std::vector<z3::ListMedium> medium;
+    std::vector<z3::ListLarge> large;
+};
+
+namespace z3 {
+
 struct NormOut {
     float *clip;  // {norm, coef}
     NormWorkspace *ws;
@@ -71,15 +89,14 @@ struct ReduceNormArgs {
     double *sumsq;  // one per tile, over the layout's reduce tables in order
 };
 
-struct AdamClipArgs {
-    AdamArgs a;
-    const float *clip;
+// One launch's units (a kernel parameter); unit i's first CTA is block0[i].
+template <int CAP>
+struct AdamUnits {
+    static constexpr int kCap = CAP;
+    int32_t count;
+    uint32_t block0[CAP];
+    AdamArgs u[CAP];
 };
-
-// Bytes of one element of a listed tensor.
-inline int64_t list_dtype_bytes(int32_t dtype) {
-    return dtype == Z3_BF16 ? 2 : dtype == Z3_F32 ? 4 : 8;
-}
 
 // Tiles of the layout's reduce tables: the length of a sumsq buffer.
 inline int64_t sumsq_len(const z3_layout *L) {
@@ -88,15 +105,18 @@ inline int64_t sumsq_len(const z3_layout *L) {
     return n;
 }
 
-cudaError_t launch_grad_norm(const z3_tensor *tensors, int32_t n, float max_norm, float *clip,
+// Checks the tensors and fills the list (z3_list.cpp); host memory may throw.
+z3_status build_list(const char *fn, const z3_tensor *tensors, int32_t n, z3_tensor_list *list);
+
+cudaError_t launch_grad_norm(const z3_tensor_list *list, float max_norm, float *clip,
                              NormWorkspace *ws, cudaStream_t stream);
-cudaError_t launch_clip(const z3_tensor *tensors, int32_t n, const float *clip,
-                        cudaStream_t stream);
+cudaError_t launch_clip(const z3_tensor_list *list, const float *clip, cudaStream_t stream);
 // early: as for launch_reduce (the stream's previous kernel, enqueued by the
 // same call, writes none of grads and grad_shards)
 cudaError_t launch_reduce_norm(const z3_layout *L, const ReduceNormArgs &a, bool accumulate,
                                cudaStream_t stream, bool early);
-// early: the previous kernel writes none of master, m, v, the gradient and clip
-cudaError_t launch_adam_clipped(const AdamClipArgs &a, cudaStream_t stream, bool early);
+// The units' updates, in as few launches as hold them.
+cudaError_t launch_adam_clipped(const AdamArgs *a, int32_t n, const float *clip,
+                                cudaStream_t stream);
 
 }  // namespace z3

@@ -29,7 +29,8 @@ EXPORTS = ("z3_layout_create", "z3_layout_destroy", "z3_layout_info", "z3_layout
            "z3_adam_shard_step", "z3_reduce_scatter_adam", "z3_step_layer",
            "z3_allreduce", "z3_scatter", "z3_reshard", "z3_model_step",
            "z3_host_step_create", "z3_host_step_run", "z3_host_step_destroy",
-           "z3_step_layer_noalloc", "z3_grad_norm_workspace_bytes", "z3_grad_norm", "z3_clip",
+           "z3_step_layer_noalloc", "z3_tensor_list_create", "z3_tensor_list_destroy",
+           "z3_grad_norm_workspace_bytes", "z3_grad_norm", "z3_clip",
            "z3_sumsq_len", "z3_reduce_scatter_norm", "z3_adam_shard_step_clipped",
            "z3_model_step_clipped", "z3_status_string", "z3_last_error")
 
@@ -121,8 +122,10 @@ def load():
             "z3_host_step_destroy": (None, [vp]),
             "z3_step_layer_noalloc": (st, [vp, vp, vp, i64, f32, vp, vp, vp, hp, i64, vp]),
             "z3_grad_norm_workspace_bytes": (st, [ctypes.POINTER(i64)]),
-            "z3_grad_norm": (st, [vp, i32, f32, vp, vp, vp]),
-            "z3_clip": (st, [vp, i32, vp, vp]),
+            "z3_tensor_list_create": (st, [ctypes.POINTER(Tensor), i32, ctypes.POINTER(vp)]),
+            "z3_tensor_list_destroy": (None, [vp]),
+            "z3_grad_norm": (st, [vp, f32, vp, vp, vp]),
+            "z3_clip": (st, [vp, vp, vp]),
             "z3_sumsq_len": (st, [vp, ctypes.POINTER(i64)]),
             "z3_reduce_scatter_norm": (st, [vp, vp, i64, vp, f32, i32, vp, vp]),
             "z3_adam_shard_step_clipped": (st, [vp, vp, vp, vp, vp, vp, hp, i64, vp, vp]),
@@ -158,11 +161,17 @@ def _check(status: int):
         raise Z3Error(status, last_error())
 
 
+@functools.cache
+def _torch():
+    import torch
+    return torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
         # the handle alone: torch.cuda.current_stream() builds a stream object
         # around it, which takes as long as a launch
+        torch = _torch()
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
@@ -179,10 +188,9 @@ def _dev(t, dtypes, numel: int, name: str):
         return t
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    here = _torch().cuda.current_device()
+    if t.get_device() != here:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{here}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if not t.is_contiguous():
@@ -192,8 +200,9 @@ def _dev(t, dtypes, numel: int, name: str):
     return t.data_ptr()
 
 
+@functools.cache
 def _dtypes():
-    import torch
+    torch = _torch()
     return (torch.bfloat16, torch.int16, torch.uint16), (torch.float32,)
 
 
@@ -394,27 +403,46 @@ def _unit_args(units, full):
 # ---------------------------------------------------------------------------
 
 class TensorList:
-    """A list of tensors for z3_grad_norm and z3_clip, laid out once and kept
-    alive: bf16 or fp32 CUDA tensors of any lengths (contiguous; views into
-    flat buffers may start at any element), and `sumsq`, fp64 tensors that
-    z3_reduce_scatter_norm wrote."""
+    """Owns a ``z3_tensor_list`` handle (z3_tensor_list_create / _destroy), and
+    keeps the tensors alive: bf16 or fp32 CUDA tensors of any lengths
+    (contiguous; views into flat buffers may start at any element), and
+    `sumsq`, fp64 tensors that z3_reduce_scatter_norm wrote."""
 
     def __init__(self, tensors, sumsq=()):
         import torch
         b16, f32 = _dtypes()
+        lib = load()
         tensors, sumsq = list(tensors), list(sumsq)
         self._keep = tensors + sumsq
-        self.n = len(self._keep)
-        self.array = (Tensor * self.n)()
+        arr = (Tensor * len(self._keep))()
         for i, t in enumerate(tensors):
-            ptr = _dev(t, b16 + f32, 0, f"tensors[{i}]")
-            self.array[i] = Tensor(ptr, t.numel(), Z3_F32 if t.dtype in f32 else Z3_BF16, 0)
+            arr[i] = Tensor(_dev(t, b16 + f32, 0, f"tensors[{i}]"), t.numel(),
+                            Z3_F32 if t.dtype in f32 else Z3_BF16, 0)
         for i, t in enumerate(sumsq):
-            ptr = _dev(t, (torch.float64,), 0, f"sumsq[{i}]")
-            self.array[len(tensors) + i] = Tensor(ptr, t.numel(), Z3_SUMSQ, 0)
+            arr[len(tensors) + i] = Tensor(_dev(t, (torch.float64,), 0, f"sumsq[{i}]"),
+                                           t.numel(), Z3_SUMSQ, 0)
+        h = ctypes.c_void_p()
+        _check(lib.z3_tensor_list_create(arr, len(arr), ctypes.byref(h)))
+        self._h = h
+        self._lib = lib
 
     def __len__(self):
-        return self.n
+        return len(self._keep)
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None) is not None and self._h.value:
+            self._lib.z3_tensor_list_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001 - interpreter shutdown
+            pass
 
 
 @functools.cache
@@ -432,8 +460,7 @@ def grad_norm_workspace(device=None):
 
 
 def _workspace(t):
-    import torch
-    return _dev(t, (torch.uint8,), _workspace_bytes(), "workspace")
+    return _dev(t, (_torch().uint8,), _workspace_bytes(), "workspace")
 
 
 def z3_grad_norm(tensors, max_norm: float, clip, workspace, stream=None):
@@ -442,7 +469,7 @@ def z3_grad_norm(tensors, max_norm: float, clip, workspace, stream=None):
     _, f32 = _dtypes()
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
-    _check(load().z3_grad_norm(tensors.array, tensors.n, max_norm, _dev(clip, f32, 2, "clip"),
+    _check(load().z3_grad_norm(tensors.handle, max_norm, _dev(clip, f32, 2, "clip"),
                                _workspace(workspace), _stream(stream)))
 
 
@@ -451,8 +478,7 @@ def z3_clip(tensors, clip, stream=None):
     _, f32 = _dtypes()
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
-    _check(load().z3_clip(tensors.array, tensors.n, _dev(clip, f32, 2, "clip"),
-                          _stream(stream)))
+    _check(load().z3_clip(tensors.handle, _dev(clip, f32, 2, "clip"), _stream(stream)))
 
 
 def z3_reduce_scatter_norm(layout: Layout, grads, grad_stride: int, grad_shards, scale: float,

@@ -18,11 +18,6 @@ def lib():
     return z3.load()
 
 
-def tensors(*ts):
-    arr = (z3.Tensor * len(ts))(*[z3.Tensor(*t, 0) for t in ts])
-    return arr, len(ts)
-
-
 def test_sumsq_len_counts_the_reduce_tiles(lib):
     # one sum per CTA: 128 vectors of 8 elements of one (parameter, rank) slice
     assert z3.Layout([1024 * 8], 8).sumsq_len == 8
@@ -37,70 +32,97 @@ def test_sumsq_len_counts_the_reduce_tiles(lib):
     assert lib.z3_grad_norm_workspace_bytes(None) == z3.Z3_ERR_INVALID_ARG
 
 
+class List:
+    """A z3_tensor_list of (address, numel, dtype) triples, and its status."""
+
+    def __init__(self, lib, *ts, n=None):
+        self.lib = lib
+        arr = (z3.Tensor * len(ts))(*[z3.Tensor(*t, 0) for t in ts])
+        self.h = ctypes.c_void_p(7)
+        self.status = lib.z3_tensor_list_create(arr, len(ts) if n is None else n,
+                                                ctypes.byref(self.h))
+        self.message = z3.last_error()
+
+    def __del__(self):
+        self.lib.z3_tensor_list_destroy(self.h)
+
+
+@pytest.mark.no_device
+def test_tensor_list_refusals(lib):
+    d = A + (1 << 30)
+    ok = (d, 100, z3.Z3_F32)
+    inv, ali, ovf = z3.Z3_ERR_INVALID_ARG, z3.Z3_ERR_ALIGNMENT, z3.Z3_ERR_OVERFLOW
+    for ts, n, status, words in (
+            ([ok], -1, inv, "n < 0"),
+            ([(d, 100, 3)], None, inv, "tensors[0]: unknown dtype"),
+            ([(d, 100, -1)], None, inv, "unknown dtype"),
+            ([ok, (d, -1, z3.Z3_F32)], None, inv, "tensors[1]: numel"),
+            ([(None, 1, z3.Z3_F32)], None, inv, "NULL"),
+            ([(d + 2, 1, z3.Z3_F32)], None, ali, "tensors[0]"),
+            ([ok, (d + 1, 1, z3.Z3_BF16)], None, ali, "tensors[1]"),
+            ([(d + 4, 1, z3.Z3_SUMSQ)], None, ali, "tensors[0]"),
+            ([(d, 1 << 62, z3.Z3_F32)], None, ovf, "tensors[0]"),
+            ([(d, 1 << 60, z3.Z3_F32)], None, ovf, "tensors[0]"),   # past any address
+            ([((1 << 64) - 64, 32, z3.Z3_F32)], None, ovf, "tensors[0]")):
+        x = List(lib, *ts, n=n)
+        assert (x.status, x.h.value) == (status, None) and words in x.message, (ts, x.message)
+    h = ctypes.c_void_p()
+    assert lib.z3_tensor_list_create(None, 1, ctypes.byref(h)) == inv
+    assert lib.z3_tensor_list_create(None, 0, None) == inv
+    assert lib.z3_tensor_list_create(None, 0, ctypes.byref(h)) == z3.Z3_OK
+    lib.z3_tensor_list_destroy(h)
+    lib.z3_tensor_list_destroy(None)  # no-op
+
+
 @pytest.mark.no_device
 def test_grad_norm_and_clip_refusals(lib):
     clip, ws = A, A + (1 << 20)
     d = A + (1 << 30)
-
-    def norm(ts, n=None, max_norm=1.0, clip=clip, ws=ws):
-        arr, k = ts if isinstance(ts, tuple) and isinstance(ts[0], ctypes.Array) else tensors(*ts)
-        return lib.z3_grad_norm(arr, k if n is None else n, max_norm, clip, ws, None), \
-            z3.last_error()
-
-    def scale(ts, n=None, clip=clip):
-        arr, k = tensors(*ts)
-        return lib.z3_clip(arr, k if n is None else n, clip, None), z3.last_error()
-
     ok = (d, 100, z3.Z3_F32)
-    inv, ali, ovf = z3.Z3_ERR_INVALID_ARG, z3.Z3_ERR_ALIGNMENT, z3.Z3_ERR_OVERFLOW
+    inv, ali = z3.Z3_ERR_INVALID_ARG, z3.Z3_ERR_ALIGNMENT
+
+    def norm(*ts, max_norm=1.0, clip=clip, ws=ws):
+        x = List(lib, *ts)
+        assert x.status == z3.Z3_OK
+        return lib.z3_grad_norm(x.h, max_norm, clip, ws, None), z3.last_error()
+
+    def scale(*ts, clip=clip):
+        x = List(lib, *ts)
+        assert x.status == z3.Z3_OK
+        return lib.z3_clip(x.h, clip, None), z3.last_error()
+
     for bad in (0.0, -1.0, math.nan, -math.inf):
-        s, msg = norm([ok], max_norm=bad)
+        s, msg = norm(ok, max_norm=bad)
         assert s == inv and "max_norm" in msg, bad
     for call in (norm, scale):
-        s, msg = call([ok], n=-1)
-        assert s == inv and "n < 0" in msg
-        s, msg = call([(d, 100, 3)])
-        assert s == inv and "tensors[0]" in msg and "dtype" in msg
-        s, msg = call([ok, (d, -1, z3.Z3_F32)])
-        assert s == inv and "tensors[1]" in msg and "numel" in msg
-        s, msg = call([(None, 1, z3.Z3_F32)])
-        assert s == inv and "NULL" in msg
-        s, msg = call([(d + 2, 1, z3.Z3_F32)])
-        assert s == ali
-        s, msg = call([(d + 1, 1, z3.Z3_BF16)])
-        assert s == ali
-        s, msg = call([(d, 1 << 62, z3.Z3_F32)])
-        assert s == ovf
-        s, msg = call([(d, 1 << 60, z3.Z3_F32)])       # the end wraps past any address
-        assert s == ovf
-        s, msg = call([ok], clip=None)
+        s, msg = call(ok, clip=None)
         assert s == inv and "clip" in msg
-        s, msg = call([ok], clip=clip + 4)
+        s, msg = call(ok, clip=clip + 4)
         assert s == ali and "clip" in msg
-        s, msg = call([(clip + 4, 1, z3.Z3_F32)])
-        assert s == inv and "overlaps clip" in msg
-    s, msg = norm([(d + 4, 1, z3.Z3_SUMSQ)])
-    assert s == ali
-    s, msg = norm([ok], ws=None)
+        s, msg = call((d, 1, z3.Z3_F32), (d + 16, 0, z3.Z3_F32), (clip + 4, 1, z3.Z3_F32))
+        assert s == inv and "tensors[2] overlaps clip" in msg
+    s, msg = norm(ok, ws=None)
     assert s == inv and "workspace" in msg
-    s, msg = norm([ok], ws=clip)
+    s, msg = norm(ok, ws=ws + 8)
+    assert s == ali and "workspace" in msg
+    s, msg = norm(ok, ws=clip)
     assert s == inv and "overlaps" in msg
-    s, msg = norm([(ws + 16, 1, z3.Z3_BF16)])
+    s, msg = norm((ws + 16, 1, z3.Z3_BF16))
     assert s == inv and "overlaps workspace" in msg
-    assert lib.z3_grad_norm(None, 1, 1.0, clip, ws, None) == inv
-    assert lib.z3_clip(None, 1, clip, None) == inv
-    s, msg = scale([ok, (d, 8, z3.Z3_SUMSQ)])
-    assert s == inv and "sums of squares" in msg
+    assert lib.z3_grad_norm(None, 1.0, clip, ws, None) == inv
+    assert lib.z3_clip(None, clip, None) == inv
+    s, msg = scale(ok, (d + 4096, 8, z3.Z3_SUMSQ))
+    assert s == inv and "tensors[1] holds sums of squares" in msg
     # overlapping tensors, in ascending and in other orders
-    s, msg = scale([ok, (d + 396, 4, z3.Z3_F32)])
+    s, msg = scale(ok, (d + 396, 4, z3.Z3_F32))
     assert s == inv and "tensors[1] overlaps tensors[0]" in msg
-    s, msg = scale([(d + 396, 4, z3.Z3_F32), ok])
+    s, msg = scale((d + 396, 4, z3.Z3_F32), ok)
     assert s == inv and "overlaps" in msg
-    s, msg = scale([(d + 4096, 4, z3.Z3_F32), ok, (d + 398, 1, z3.Z3_BF16)])
-    assert s == inv and "tensors[2] overlaps tensors[1]" in msg
+    s, msg = scale((None, 0, z3.Z3_F32), (d + 4096, 4, z3.Z3_F32), ok, (d + 398, 1, z3.Z3_BF16))
+    assert s == inv and "tensors[3] overlaps tensors[2]" in msg
     # what is right gets as far as the launch, which finds no device
-    assert norm([ok, ok, (None, 0, z3.Z3_F32), (d + 2, 1, z3.Z3_BF16)])[0] == z3.Z3_ERR_CUDA
-    assert scale([(d + 400, 4, z3.Z3_F32), ok])[0] == z3.Z3_ERR_CUDA
+    assert norm(ok, ok, (None, 0, z3.Z3_F32), (d + 2, 1, z3.Z3_BF16))[0] == z3.Z3_ERR_CUDA
+    assert scale((d + 400, 4, z3.Z3_F32), ok)[0] == z3.Z3_ERR_CUDA
 
 
 @pytest.mark.no_device
