@@ -103,24 +103,49 @@ class Model:
                  1.0 / u.w.n_ranks, u.resident, u.hp) for u in self.units]
 
     def clip_args(self):
-        """What a clipped step keeps beside the units' state: each unit's
-        reduced fp32 gradient and its sums of squares, the norm's workspace
-        and [norm, coef].  Allocated by the first clipped step."""
+        """What a clipped step keeps beside the units' state: for each unit its
+        reduced fp32 gradient and its sums of squares, and for all of them
+        the norm's list and workspace and [norm, coef].  Allocated by the
+        first clipped step."""
         if self._clip_args is None:
             self._clip_args = [(torch.zeros(u.L.psi_padded, dtype=torch.float32, device=self.dev),
                                 torch.zeros(u.L.sumsq_len, dtype=torch.float64, device=self.dev))
                                for u in self.units]
+            self._sums = z3.TensorList([], sumsq=[sq for _, sq in self._clip_args])
             self._workspace = z3.grad_norm_workspace(self.dev)
             self.clip = torch.zeros(2, dtype=torch.float32, device=self.dev)
         return self._clip_args
 
-    def _clipped_step(self, full, hp: dict, t: int, max_norm: float, stream, gather_stream,
-                      on_gather):
-        if on_gather is not None:
-            raise NotImplementedError("the call-by-call schedule does not clip")
-        z3.z3_model_step_clipped(self.unit_args(), self.clip_args(), full, hp, t, max_norm,
-                                 self.clip, self._workspace, stream=stream,
-                                 gather_stream=gather_stream)
+    def _library_step(self, full, hp: dict, t: int, max_norm, stream, gather_stream=None):
+        if max_norm is None:
+            z3.z3_model_step(self.unit_args(), full, hp, t, stream=stream,
+                             gather_stream=gather_stream)
+        else:
+            clips = self.clip_args()
+            z3.z3_model_step_clipped(self.unit_args(), clips, full, hp, t, max_norm, self.clip,
+                                     self._workspace, stream=stream, gather_stream=gather_stream)
+
+    def _backward(self, i: int, hp: dict, t: int, max_norm, stream):
+        """What follows the backward compute of unit i: its update, or in a
+        clipped step its reduced gradient and sums of squares."""
+        u = self.units[i]
+        if max_norm is None:
+            self._update(u, hp, t, stream)
+        else:
+            gs, sq = self.clip_args()[i]
+            z3.z3_reduce_scatter_norm(u.L, u.grads, u.w.grad_stride, gs, 1.0 / u.w.n_ranks, sq,
+                                      stream=stream)
+
+    def _finish(self, hp: dict, t: int, max_norm, stream):
+        """The rest of a clipped step, once every unit is reduced."""
+        if max_norm is None:
+            return
+        z3.z3_grad_norm(self._sums, max_norm, self.clip, self._workspace, stream=stream)
+        for u, (gs, _) in zip(self.units, self.clip_args()):
+            z3.z3_adam_shard_step_clipped(u.L, u.master, u.m, u.v, gs, u.shards, u.hp or hp, t,
+                                          self.clip, stream=stream)
+            if u.resident is not None:
+                z3.z3_allgather(u.L, u.shards, u.resident, stream=stream)
 
     @staticmethod
     def _update(u: Unit, hp: dict, t: int, stream):
@@ -144,11 +169,8 @@ class Model:
         if t is None:
             self.t += 1
             t = self.t
-        if max_norm is not None:
-            self._clipped_step([self.full], hp, t, max_norm, stream, None, on_gather)
-            return
         if on_gather is None:
-            z3.z3_model_step(self.unit_args(), [self.full], hp, t, stream=stream)
+            self._library_step([self.full], hp, t, max_norm, stream)
             return
         for i, u in enumerate(self.units):            # forward
             if u.resident is None:
@@ -159,7 +181,8 @@ class Model:
             if u.resident is None:
                 z3.z3_allgather(u.L, u.shards, self.full, stream=stream)
             on_gather("backward", i)
-            self._update(u, hp, t, stream)
+            self._backward(i, hp, t, max_norm, stream)
+        self._finish(hp, t, max_norm, stream)
 
 
 def _torch_stream(stream):
@@ -199,12 +222,8 @@ class PrefetchModel(Model):
         if t is None:
             self.t += 1
             t = self.t
-        if max_norm is not None:
-            self._clipped_step(self.bufs, hp, t, max_norm, stream, self.gstream, on_gather)
-            return
         if on_gather is None:
-            z3.z3_model_step(self.unit_args(), self.bufs, hp, t, stream=stream,
-                             gather_stream=self.gstream)
+            self._library_step(self.bufs, hp, t, max_norm, stream, self.gstream)
             return
         if self.depth != 1:
             raise NotImplementedError("the call-by-call schedule prefetches one unit ahead")
@@ -239,9 +258,10 @@ class PrefetchModel(Model):
                     g.wait_event(freed[nxt % 2])       # buffer of unit i+1 is free again
                 gather(nxt)                            # prefetch one unit ahead
             main.wait_event(gathered[i])
-            self._update(u, hp, t, main.cuda_stream)
+            self._backward(i, hp, t, max_norm, main.cuda_stream)
             freed[i % 2].record(main)
         main.wait_stream(g)
+        self._finish(hp, t, max_norm, main.cuda_stream)
 
 
 def full_step_model(dev, seed: int = 0, prefetch: int = 0, bucket_layers: int = 1,

@@ -12,7 +12,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import itertools
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -402,6 +404,20 @@ def _unit_args(units, full):
 # gradient clipping by the global norm
 # ---------------------------------------------------------------------------
 
+def _records(tensors, kinds, name):
+    """The fields of z3_tensor for each tensor, one after the other; kinds: the
+    z3_dtype of each dtype allowed."""
+    here = _torch().cuda.current_device() if tensors and tensors[0].is_cuda else None
+    for i, t in enumerate(tensors):
+        kind = kinds.get(t.dtype)
+        if kind is None or not t.is_cuda or t.get_device() != here or not t.is_contiguous():
+            _dev(t, tuple(kinds), 0, f"{name}[{i}]")    # says what is wrong
+        yield t.data_ptr()
+        yield t.numel()
+        yield kind
+        yield 0
+
+
 class TensorList:
     """Owns a ``z3_tensor_list`` handle (z3_tensor_list_create / _destroy), and
     keeps the tensors alive: bf16 or fp32 CUDA tensors of any lengths
@@ -409,20 +425,17 @@ class TensorList:
     `sumsq`, fp64 tensors that z3_reduce_scatter_norm wrote."""
 
     def __init__(self, tensors, sumsq=()):
-        import torch
+        torch = _torch()
         b16, f32 = _dtypes()
         lib = load()
         tensors, sumsq = list(tensors), list(sumsq)
         self._keep = tensors + sumsq
-        arr = (Tensor * len(self._keep))()
-        for i, t in enumerate(tensors):
-            arr[i] = Tensor(_dev(t, b16 + f32, 0, f"tensors[{i}]"), t.numel(),
-                            Z3_F32 if t.dtype in f32 else Z3_BF16, 0)
-        for i, t in enumerate(sumsq):
-            arr[len(tensors) + i] = Tensor(_dev(t, (torch.float64,), 0, f"sumsq[{i}]"),
-                                           t.numel(), Z3_SUMSQ, 0)
+        n = len(self._keep)
+        arr = (Tensor * n).from_buffer_copy(struct.pack("Pqii" * n, *itertools.chain(
+            _records(tensors, {d: Z3_BF16 for d in b16} | {d: Z3_F32 for d in f32}, "tensors"),
+            _records(sumsq, {torch.float64: Z3_SUMSQ}, "sumsq"))))
         h = ctypes.c_void_p()
-        _check(lib.z3_tensor_list_create(arr, len(arr), ctypes.byref(h)))
+        _check(lib.z3_tensor_list_create(arr, n, ctypes.byref(h)))
         self._h = h
         self._lib = lib
 

@@ -408,8 +408,30 @@ def test_unclipped_and_stopped_steps(z3, prefetch):
     b.step(HP, max_norm=1e6)
     assert same(before, model_bits(b))
     assert b.clip[0] == math.inf and b.clip[1].isnan()
-    with pytest.raises(NotImplementedError):
-        b.step(HP, max_norm=1.0, on_gather=lambda *a: None)
+
+
+@pytest.mark.parametrize("prefetch", [0, 1])
+@pytest.mark.parametrize("max_norm", [0.01, 1e6])
+def test_clipped_step_issued_call_by_call(z3, prefetch, max_norm):
+    """The schedule with hooks, from Python, gives the library's step."""
+    a, b = make_model(prefetch, (1,)), make_model(prefetch, (1,))
+    seen = []
+    for _ in range(2):
+        a.step(HP, max_norm=max_norm)
+        b.step(HP, max_norm=max_norm, on_gather=lambda phase, i: seen.append((phase, i)))
+    assert same(model_bits(a), model_bits(b)) and torch.equal(a.clip, b.clip)
+    n = len(UNITS)
+    assert sorted(seen) == sorted(2 * [(p, i) for p in ("backward", "forward") for i in range(n)])
+
+
+def test_clipped_step_of_empty_units(z3, clip, ws):
+    L = z3.Layout([0], 4)
+    e = torch.empty(0, device="cuda")
+    unit = (L, e.to(B16), e, e, e, e.to(B16), 0, 0.25)
+    sq = torch.empty(0, dtype=torch.float64, device="cuda")
+    z3.z3_model_step_clipped([unit, unit], [(e, sq)] * 2, [torch.empty(8, dtype=B16, device="cuda")],
+                             HP, 1, 1.0, clip, ws)
+    assert clip.tolist() == [0.0, 1.0]
 
 
 def test_clipped_step_accumulates_micro_batches(z3, orc, clip, ws):
