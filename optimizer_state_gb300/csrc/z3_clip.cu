@@ -43,7 +43,7 @@ __device__ __forceinline__ void pdl_enter_early() {
 // binary64 addition.  With one for every element the reduce-scatter of a
 // d = 1024 layer with its norm took 98 us instead of 45, and with one for
 // every batch and for every step of the CTAs' trees the norm of 700 tensors
-// (10 MB) took 11.5 us instead of 6.  A CTA's sum is then stored as binary64.
+// (10 MB) took 11.5 us instead of 9.8.  A CTA's sum is then stored as binary64.
 //
 // A batch whose sum leaves [kSafeLo, kSafeHi] may have lost squares to
 // underflow or overflow; it is summed again with its elements scaled by a
@@ -165,7 +165,7 @@ __device__ __forceinline__ VecRef vec_ref(const ListEntry &e, const ListEntry &n
 }
 
 // The tensor's bytes of a partial vector, zeros in place of the others.
-__device__ __noinline__ uint4 load_partial(const VecRef r) {
+__device__ __forceinline__ uint4 load_partial(const VecRef r) {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int x = 0; x < 16; x += 2)
@@ -270,6 +270,12 @@ __device__ __forceinline__ void squares(const uint4 &w, bool f32, float k, float
     }
 }
 
+// Out of line, so that batches of zeros (the rows of an embedding that no token
+// used) branch around its binary64 instructions.
+__device__ __noinline__ double add_rare(double rare, float s, double k) {
+    return rare + (double)s * k;
+}
+
 // Adds a batch of U vectors of gradients; f32(u): vector u holds fp32, not bf16.
 template <int U, typename F32>
 __device__ __forceinline__ void add_batch(Sum &sum, const uint4 (&w)[U], F32 f32) {
@@ -284,7 +290,7 @@ __device__ __forceinline__ void add_batch(Sum &sum, const uint4 (&w)[U], F32 f32
     s0 = s1 = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) squares<true>(w[u], f32(u), rescale(s), s0, s1);
-    if (s0 + s1 != 0.0f) sum.rare += (double)(s0 + s1) * unscale(s);
+    if (s0 + s1 != 0.0f) sum.rare = add_rare(sum.rare, s0 + s1, unscale(s));
 }
 
 // Adds a vector of two sums of squares.
@@ -292,6 +298,12 @@ __device__ __forceinline__ void add_sums(Sum &sum, const uint4 &w) {
     sum.rare += __hiloint2double(w.y, w.x) + __hiloint2double(w.w, w.z);
 }
 
+// With the CTAs resident on an SM (kNormCtas) this sets how much is in flight.
+// 3 and 6 were taken over 4 and 6, which reads 1.41 GB in 197 us instead of
+// 201 after reads, but takes 654 us instead of 610 for norm and clipping one
+// after the other: its reads crowd out the write-back of what the clipping
+// before left in L2.  Lists of small tensors are fastest with 3 and 6 too (700
+// of them, 10 MB: 7.7 us; 2 and 8: 7.6; 4 and 6: 7.9; 3 and 7: 8.5).
 constexpr int kNormU = 3;
 
 // The run's last vectors, 64 MB, are left in L2 for the clipping that
@@ -340,31 +352,27 @@ k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
         }
         tile.stage(tab, staged);
         int kind[kNormU];
-        bool partial = false;
+        bool sums = false;
 #pragma unroll
         for (int u = 0; u < kNormU; ++u) {
             const VecRef r = tile.ref(staged, u);
             w[u] = r.whole() ? __ldg(reinterpret_cast<const uint4 *>(r.p))
                              : make_uint4(0, 0, 0, 0);
             kind[u] = r.kind;
-            partial |= r.partial();
+            if (r.partial()) w[u] = load_partial(r);
+            sums |= r.kind == Z3_SUMSQ;
         }
+        // a branch of the whole warp: as predicated instructions these binary64
+        // additions would take the FP64 units' time in every mixed tile
+        if (__any_sync(0xffffffffu, sums)) {
 #pragma unroll
-        for (int u = 0; u < kNormU; ++u) {
-            if (kind[u] != Z3_SUMSQ) continue;
-            add_sums(sum, w[u]);
-            w[u] = make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < kNormU; ++u) {
+                if (kind[u] != Z3_SUMSQ) continue;
+                add_sums(sum, w[u]);
+                w[u] = make_uint4(0, 0, 0, 0);
+            }
         }
         add_batch(sum, w, [&](int u) { return kind[u] == Z3_F32; });
-        if (!partial) continue;
-#pragma unroll 1
-        for (int u = 0; u < kNormU; ++u) {
-            const VecRef r = tile.ref(staged, u);
-            if (!r.partial()) continue;
-            const uint4 x[1] = {load_partial(r)};
-            if (r.kind == Z3_SUMSQ) add_sums(sum, x[0]);
-            else add_batch(sum, x, [&](int) { return r.kind == Z3_F32; });
-        }
     }
     const double all = block_sum<kListThreads>(sum);
     if (threadIdx.x != 0) return;

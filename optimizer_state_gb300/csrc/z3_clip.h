@@ -48,7 +48,7 @@ using ListMedium = ListTab<700>;
 using ListLarge = ListTab<1900>;
 
 // Device workspace of z3_grad_norm.
-constexpr int kNormCtas = 7;                     // resident on an SM
+constexpr int kNormCtas = 6;                     // resident on an SM
 constexpr int kNormMaxGrid = kNormCtas * kSMs;
 struct NormWorkspace {
     double partial[kNormMaxGrid];  // one per CTA of a launch
