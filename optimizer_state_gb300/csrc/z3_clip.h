@@ -78,7 +78,6 @@ struct NormOut {
     float max_norm;
     int32_t first;  // this launch is the call's first: no carry
     int32_t last;   // its last: write clip
-    int32_t alone;  // both, with one CTA: no partials
 };
 
 struct ReduceNormArgs {

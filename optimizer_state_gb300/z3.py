@@ -91,6 +91,8 @@ def library_path() -> str:
 def load():
     """Load the CUDA library (built by ``optimizer_state_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -90,6 +90,8 @@ LISTS = [
     [17] * 159, [17] * 160, [17] * 161,    # around the first launch table's size
     [5] * 1901,                            # more tensors than one launch takes
     [4099] * 200,
+    # around what one CTA, eight of them and one cluster take, of either type
+    [24576], [24577], [49151], [49152], [49153], [98304], [98305], [49100, 60, 49000, 200],
 ]
 
 
