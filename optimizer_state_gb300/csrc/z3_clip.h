@@ -15,8 +15,8 @@ namespace z3 {
 
 // A list of tensors is walked as one run of 16-byte vectors, each tensor
 // contributing the aligned vectors that its bytes touch, and the run is cut
-// into tiles of kListTile vectors, whatever the tensors' lengths.
-constexpr int kSMs = 152;
+// into equal tiles, whatever the tensors' lengths.
+constexpr int kSMs = 152;  // of a GB300
 constexpr int kListThreads = 256;
 constexpr int kListBuckets = 512;
 
@@ -41,8 +41,9 @@ struct ListTab {
 };
 
 // The first size stays within the classic 4 KB of kernel parameters, the
-// last within the 32,764 bytes that sm_103 takes; copying a table to the GPU
-// costs a launch 3 us at the last size.
+// last within the 32,764 bytes that sm_103 takes.  A table travels with its
+// launch: 2.3 us of host time with the first size, 3.5 with the second, 9
+// with the last.
 using ListSmall = ListTab<180>;
 using ListMedium = ListTab<700>;
 using ListLarge = ListTab<1900>;
