@@ -3,6 +3,7 @@ and the words of each refusal, and the lengths that they tell.  Made-up device
 addresses are only used in a child process that sees no device."""
 import ctypes
 import math
+import subprocess
 
 import pytest
 
@@ -16,6 +17,25 @@ A = 1 << 32                       # an aligned made-up address
 def lib():
     z3build.build()
     return z3.load()
+
+
+def test_structs_are_laid_out_as_in_the_header(tmp_path):
+    """The binding's structures against a C compiler's."""
+    fields = {"z3_tensor": (z3.Tensor, ["data", "numel", "dtype", "reserved"]),
+              "z3_clip_unit": (z3.ClipUnit, ["grad_shards", "sumsq", "accumulate", "reserved"])}
+    lines = [f'printf("%zu %zu\\n", sizeof({n}), offsetof({n}, {f}));'
+             for n, (_, fs) in fields.items() for f in fs]
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include "z3.h"\nint main(void) {\n' +
+                   "\n".join(lines) + "\nreturn 0;\n}\n")
+    exe = tmp_path / "sizes"
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", f"-I{z3build.INCLUDE}", str(src), "-o",
+                    str(exe)], check=True)
+    got = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
+    want = [x for c, fs in fields.values() for f in fs
+            for x in (ctypes.sizeof(c), getattr(c, f).offset)]
+    assert list(map(int, got)) == want
+    assert (z3.Z3_BF16, z3.Z3_F32, z3.Z3_SUMSQ) == (0, 1, 2)
 
 
 def test_sumsq_len_counts_the_reduce_tiles(lib):

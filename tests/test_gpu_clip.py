@@ -220,6 +220,31 @@ def test_same_call_same_bits_and_stream_and_graph(z3, clip, ws):
     assert torch.equal(out[:, :2], first.expand(64, 2)) and not out[:, 2:].any()
 
 
+@pytest.mark.parametrize("lengths", [[7], [5000, 3], [17] * 300, [100003, 65537]])
+def test_norm_and_clip_in_turn(z3, clip, ws, lengths):
+    """Forty times one after the other without a wait: every norm is of what
+    the clipping before it wrote."""
+    _, views = back_to_back(lengths, F32, 1.0, 8, shift=1)
+    tl = z3.TensorList(views)
+    out = torch.zeros(40, 4, device="cuda")
+    want = [exact_norm(views) * 0.9 ** (i + 1) for i in range(40)]
+    for i in range(40):
+        z3.z3_grad_norm(tl, want[i], out[i, :2], ws)
+        z3.z3_clip(tl, out[i, :2])
+    got = out[1:, 0].cpu().double().numpy()
+    # each pass rounds every element once more, by 2^-24 at most, and coef too
+    assert np.all(np.abs(got / want[:-1] - 1) <= NORM_TOL + COEF_TOL + 2.0 ** -23)
+
+
+def test_nan_in_an_earlier_launch_of_a_long_list(z3, clip, ws):
+    _, views = back_to_back([5] * 4000, B16, 1.0, 9)
+    z3.z3_grad_norm(views, 1.0, clip, ws)
+    check_norm(clip, exact_norm(views), 1.0)
+    views[3][2] = math.nan
+    z3.z3_grad_norm(views, 1.0, clip, ws)
+    assert clip.isnan().all()
+
+
 def test_a_tensor_longer_than_32_bits(z3, clip, ws):
     n = 2 ** 32 + 11                        # 8.6 GB of bf16
     t = torch.zeros(n, dtype=B16, device="cuda")
@@ -424,6 +449,28 @@ def test_clipped_step_issued_call_by_call(z3, prefetch, max_norm):
     assert same(model_bits(a), model_bits(b)) and torch.equal(a.clip, b.clip)
     n = len(UNITS)
     assert sorted(seen) == sorted(2 * [(p, i) for p in ("backward", "forward") for i in range(n)])
+
+
+def test_clipped_step_of_many_units(z3):
+    """More units than one launch's tables of the norm and of the update hold."""
+    from optimizer_state_gb300 import schedule
+    dev = torch.device("cuda")
+
+    def model():
+        gen = I.make_generator(2, "cuda")
+        return schedule.Model([schedule.Unit(I.Workload(f"u{i}", ((i % 7 * 11,), (300,)), 3, 0.02,
+                                                        1e-3), dev, gen) for i in range(190)], dev)
+    a, b, c = model(), model(), model()
+    a.step(HP)
+    b.step(HP, max_norm=1e6)
+    assert same(model_bits(a), model_bits(b))
+    want = exact_norm([gs for gs, _ in b.clip_args()])
+    check_norm(b.clip, want, 1e6)
+    c.step(HP, max_norm=0.5 * want)
+    check_norm(c.clip, want, np.float32(0.5 * want))
+    c2 = model()
+    c2.step(HP, max_norm=0.5 * want, on_gather=lambda *a: None)
+    assert same(model_bits(c), model_bits(c2)) and not same(model_bits(b), model_bits(c))
 
 
 def test_clipped_step_of_empty_units(z3, clip, ws):
