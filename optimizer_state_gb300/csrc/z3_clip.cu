@@ -137,19 +137,16 @@ __device__ __forceinline__ int64_t first_vec(const ListEntry &e) {
     return (int64_t)(e.vec0_ends >> 8);
 }
 
-// The entry that holds vector v of the run, among entries lo..hi.
-__device__ __forceinline__ int find_entry(const ListEntry *e, int lo, int hi, int64_t v) {
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_vec(e[mid]) <= v) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
-
+// The entry that holds vector v of the run.
 template <typename TAB>
 __device__ __forceinline__ int find_entry(const TAB &tab, int64_t v) {
     const int b = (int)(v >> tab.shift);
-    return find_entry(tab.e, tab.first[b], tab.first[b + 1], v);
+    int lo = tab.first[b], hi = tab.first[b + 1];
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_vec(tab.e[mid]) <= v) lo = mid; else hi = mid - 1;
+    }
+    return lo;
 }
 
 // One vector of the run: bytes [begin, end) of the 16 at p belong to the
@@ -160,18 +157,6 @@ struct VecRef {
     __device__ __forceinline__ bool whole() const { return end - begin == 16; }
     __device__ __forceinline__ bool partial() const { return end - begin != 16 && end != 0; }
 };
-
-// Vector v, of entry e whose successor is next.
-__device__ __forceinline__ VecRef vec_ref(const ListEntry &e, const ListEntry &next, int64_t v) {
-    const int64_t a = first_vec(e);
-    const int head = (int)(e.vec0_ends >> 4) & 15, tail = (int)e.vec0_ends & 15;
-    VecRef r;
-    r.kind = (int)(e.base_kind & 15);
-    r.p = reinterpret_cast<unsigned char *>(e.base_kind & ~(uint64_t)15) + (v - a) * 16;
-    r.begin = v == a ? head : 0;
-    r.end = v + 1 == first_vec(next) && tail != 0 ? tail : 16;
-    return r;
-}
 
 // The tensor's bytes of a partial vector, zeros in place of the others.
 __device__ __forceinline__ uint4 load_partial(const VecRef r) {
@@ -191,6 +176,13 @@ __device__ __noinline__ void store_partial(const VecRef r, const uint4 v) {
             *reinterpret_cast<uint16_t *>(r.p + x) = (uint16_t)(w[x / 4] >> (x % 4 * 8));
 }
 
+// An entry as a tile of several sees it, in vectors from the tile's first.
+struct StagedEntry {
+    unsigned char *base;  // where the tile's first vector would lie in this tensor
+    int32_t start;        // the tensor's first vector (-1: before the tile)
+    uint32_t ends;        // kind << 16 | head << 8 | tail
+};
+
 // A tile of U vectors per thread.  Most tiles of long tensors hold whole
 // vectors of one tensor; the others stage their entries in shared memory
 // and every thread finds its vectors' own.
@@ -200,7 +192,6 @@ struct Tile {
     int64_t v0, v1;       // its vectors of the run
     unsigned char *p;     // where they lie, when one tensor holds them whole
     int kind;
-    int64_t past;         // the end of that tensor's whole vectors in the run
     int lo, n;            // else: its entries, lo.. of the table, n of them
 
     template <typename TAB>
@@ -208,28 +199,48 @@ struct Tile {
         v0 = t * kVecs;
         v1 = min(v0 + kVecs, tab.vecs);
         lo = find_entry(tab, v0);
-        const ListEntry &e = tab.e[lo], &next = tab.e[lo + 1];
-        const VecRef a = vec_ref(e, next, v0);
-        past = first_vec(next) - ((e.vec0_ends & 15) != 0);
-        p = a.p;
-        kind = a.kind;
-        return a.begin == 0 && v1 <= past;
+        const ListEntry &e = tab.e[lo];
+        const int64_t a = first_vec(e), z = first_vec(tab.e[lo + 1]);
+        const bool head = (e.vec0_ends & 0xf0) != 0, tail = (e.vec0_ends & 15) != 0;
+        p = reinterpret_cast<unsigned char *>(e.base_kind & ~(uint64_t)15) + (v0 - a) * 16;
+        kind = (int)(e.base_kind & 15);
+        return !(head && v0 == a) && v1 <= z - tail;
     }
 
     // Every thread of the CTA takes part.
     template <typename TAB>
-    __device__ __forceinline__ void stage(const TAB &tab, ListEntry *staged) {
+    __device__ __forceinline__ void stage(const TAB &tab, StagedEntry *staged) {
         n = find_entry(tab, v1 - 1) - lo + 1;
         __syncthreads();  // the last tile's entries are done with
-        for (int k = threadIdx.x; k <= n; k += kListThreads) staged[k] = tab.e[lo + k];
+        for (int k = threadIdx.x; k <= n; k += kListThreads) {
+            const ListEntry &e = tab.e[lo + k];
+            const int64_t a = first_vec(e) - v0;
+            StagedEntry s;
+            s.base = reinterpret_cast<unsigned char *>(e.base_kind & ~(uint64_t)15) - a * 16;
+            s.start = (int32_t)min(max(a, (int64_t)-1), (int64_t)kVecs + 1);
+            s.ends = (uint32_t)(e.base_kind & 15) << 16 | (uint32_t)(e.vec0_ends & 0xf0) << 4 |
+                     (uint32_t)(e.vec0_ends & 15);
+            staged[k] = s;
+        }
         __syncthreads();
     }
 
-    __device__ __forceinline__ VecRef ref(const ListEntry *staged, int u) const {
-        const int64_t v = v0 + u * kListThreads + threadIdx.x;
-        if (v >= v1) return VecRef{nullptr, 0, 0, 0};
-        const int i = find_entry(staged, 0, n - 1, v);
-        return vec_ref(staged[i], staged[i + 1], v);
+    __device__ __forceinline__ VecRef ref(const StagedEntry *staged, int u) const {
+        const int v = u * kListThreads + (int)threadIdx.x;
+        if (v >= (int)(v1 - v0)) return VecRef{nullptr, 0, 0, 0};
+        int i = 0, hi = n - 1;
+        while (i < hi) {
+            const int mid = (i + hi + 1) >> 1;
+            if (staged[mid].start <= v) i = mid; else hi = mid - 1;
+        }
+        const StagedEntry s = staged[i];
+        const int tail = (int)(s.ends & 0xff);
+        VecRef r;
+        r.p = s.base + v * 16;
+        r.kind = (int)(s.ends >> 16);
+        r.begin = v == s.start ? (int)(s.ends >> 8 & 0xff) : 0;
+        r.end = tail != 0 && v + 1 == staged[i + 1].start ? tail : 16;
+        return r;
     }
 };
 
@@ -358,7 +369,7 @@ __global__ void __launch_bounds__(kListThreads, kNormCtas)
 k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
     if constexpr (CLUSTER) cluster_arrive();
     using T = Tile<kNormU>;
-    __shared__ ListEntry staged[T::kVecs + 1];
+    __shared__ StagedEntry staged[T::kVecs + 1];
     pdl_enter();
     Sum sum;
     const int64_t passing = tab.vecs - kNormKeep;
@@ -477,7 +488,7 @@ template <typename TAB>
 __global__ void __launch_bounds__(kListThreads, 8)
 k_clip(const __grid_constant__ TAB tab, const float *clip) {
     using T = Tile<kClipU>;
-    __shared__ ListEntry staged[T::kVecs + 1];
+    __shared__ StagedEntry staged[T::kVecs + 1];
     pdl_enter();
     const float c = clip[1];
     T tile{};

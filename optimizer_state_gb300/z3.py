@@ -171,12 +171,18 @@ def _torch():
     return torch
 
 
+@functools.cache
+def _current_device():
+    """torch.cuda.current_device without its check that CUDA is up: called
+    with a CUDA tensor at hand."""
+    return _torch()._C._cuda_getDevice
+
+
 def _stream(stream):
     if stream is None:
         # the handle alone: torch.cuda.current_stream() builds a stream object
         # around it, which takes as long as a launch
-        torch = _torch()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _torch()._C._cuda_getCurrentRawStream(_torch().cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -192,9 +198,9 @@ def _dev(t, dtypes, numel: int, name: str):
         return t
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    here = _torch().cuda.current_device()
-    if t.get_device() != here:
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{here}")
+    if t.get_device() != _current_device()():
+        raise ValueError(f"{name}: on {t.device}, but the current device is "
+                         f"cuda:{_torch().cuda.current_device()}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
     if not t.is_contiguous():
