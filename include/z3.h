@@ -44,7 +44,8 @@
  *   - Device calls validate every argument on the host, then enqueue on the
  *     caller's stream and return; a launch failure returns Z3_ERR_CUDA.
  *     Errors during execution surface at the caller's next synchronisation.
- *   - Device buffers must start on a 16-byte boundary (Z3_ERR_ALIGNMENT);
+ *   - Device buffers must start on a 16-byte boundary (Z3_ERR_ALIGNMENT;
+ *     listed tensors, see z3_tensor, on one of their elements);
  *     grad_stride must be a multiple of 8 elements (Z3_ERR_ALIGNMENT) and
  *     >= Psi (Z3_ERR_INVALID_ARG).  Interior offsets (o_p, F_p, S) may be
  *     anything.

@@ -52,7 +52,8 @@ __device__ __forceinline__ void pdl_enter_early() {
 // binary64 addition.  With one for every element the reduce-scatter of a
 // d = 1024 layer with its norm took 98 us instead of 45, and with one for
 // every batch and for every step of the CTAs' trees the norm of 700 tensors
-// (10 MB) took 11.5 us instead of 9.8.  A CTA's sum is then stored as binary64.
+// (10 MB) took 11.5 us instead of 9.8 (7.3 now).  A CTA's sum is stored as
+// binary64.
 //
 // A batch whose sum leaves [kSafeLo, kSafeHi] may have lost squares to
 // underflow or overflow; it is summed again with its elements scaled by a
@@ -323,8 +324,9 @@ __device__ __forceinline__ void add_sums(Sum &sum, const uint4 &w) {
 // 3 and 6 were taken over 4 and 6, which reads 1.41 GB in 197 us instead of
 // 201 after reads, but takes 654 us instead of 610 for norm and clipping one
 // after the other: its reads crowd out the write-back of what the clipping
-// before left in L2.  Lists of small tensors are fastest with 3 and 6 too (700
-// of them, 10 MB: 7.7 us; 2 and 8: 7.6; 4 and 6: 7.9; 3 and 7: 8.5).
+// before left in L2.  Lists of small tensors are near their best with 3 and 6
+// too (700 of them, 10 MB, measured together: 7.7 us; 2 and 8: 7.6; 4 and 6:
+// 7.9; 3 and 7: 8.5).
 constexpr int kNormU = 3;
 
 // Lists of few tiles (12 KB each) take one launch: a cluster of at most the
