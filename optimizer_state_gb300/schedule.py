@@ -160,7 +160,9 @@ class Model:
         With `max_norm` the gradients of all units are clipped to that global
         norm first (z3_model_step_clipped); `clip` then holds [norm, coef] on
         the device, coef NaN where the norm was not finite and the step was
-        left out.  That takes 4 more bytes per element (the fp32 gradients).
+        left out (it keeps its number: the host does not know of it; a caller
+        that reads `clip` may pass the same `t` again).  That takes 4 more
+        bytes per element (the fp32 gradients).
         With `on_gather(phase, index)` the same schedule is issued call by
         call from here instead, and the hook is called after each gather is
         enqueued, with the transient buffer holding that unit's parameters
