@@ -82,6 +82,7 @@ class Model:
         self.t = 0
         self.clip = None                # [norm, coef] of the last clipped step
         self._clip_args = None
+        self._clip_stream = None        # where they were allocated, until a step has used them
 
     @property
     def psi(self) -> int:
@@ -102,26 +103,49 @@ class Model:
         return [(u.L, u.shards, u.master, u.m, u.v, u.grads, u.w.grad_stride,
                  1.0 / u.w.n_ranks, u.resident, u.hp) for u in self.units]
 
-    def clip_args(self):
+    def clip_args(self, stream=None):
         """What a clipped step keeps beside the units' state: for each unit its
         reduced fp32 gradient and its sums of squares, and for all of them
-        the norm's list and workspace and [norm, coef].  Allocated by the
-        first clipped step."""
+        the norm's list and workspace and [norm, coef].  Allocated and zeroed
+        by the first call, in the order of `stream` (None: the current one):
+        by the first clipped step on its own stream, or by a call before it.
+        A step that is to be captured wants that call first, or its graph
+        holds the zeroing too."""
         if self._clip_args is None:
-            self._clip_args = [(torch.zeros(u.L.psi_padded, dtype=torch.float32, device=self.dev),
-                                torch.zeros(u.L.sumsq_len, dtype=torch.float64, device=self.dev))
-                               for u in self.units]
-            self._sums = z3.TensorList([], sumsq=[sq for _, sq in self._clip_args])
-            self._workspace = z3.grad_norm_workspace(self.dev)
-            self.clip = torch.zeros(2, dtype=torch.float32, device=self.dev)
+            self._clip_stream = _torch_stream(stream)
+            with torch.cuda.stream(self._clip_stream):
+                self._clip_args = [
+                    (torch.zeros(u.L.psi_padded, dtype=torch.float32, device=self.dev),
+                     torch.zeros(u.L.sumsq_len, dtype=torch.float64, device=self.dev))
+                    for u in self.units]
+                self._sums = z3.TensorList([], sumsq=[sq for _, sq in self._clip_args])
+                self._workspace = z3.grad_norm_workspace(self.dev)
+                self.clip = torch.zeros(2, dtype=torch.float32, device=self.dev)
         return self._clip_args
+
+    def _step_clip_args(self, stream):
+        """clip_args() for a step on `stream`.  The first step waits there for
+        the stream that they were allocated on, where that is another: the
+        zeroing, and whatever used that memory before, come first.  A capture
+        cannot wait for what is outside it (its graph runs after what its
+        capture came after), so the wait is left to the next step."""
+        clips = self.clip_args(stream)
+        if self._clip_stream is not None:
+            s = _torch_stream(stream)
+            if s.cuda_stream != self._clip_stream.cuda_stream:
+                with torch.cuda.stream(s):
+                    if torch.cuda.is_current_stream_capturing():
+                        return clips
+                s.wait_stream(self._clip_stream)
+            self._clip_stream = None
+        return clips
 
     def _library_step(self, full, hp: dict, t: int, max_norm, stream, gather_stream=None):
         if max_norm is None:
             z3.z3_model_step(self.unit_args(), full, hp, t, stream=stream,
                              gather_stream=gather_stream)
         else:
-            clips = self.clip_args()
+            clips = self._step_clip_args(stream)
             z3.z3_model_step_clipped(self.unit_args(), clips, full, hp, t, max_norm, self.clip,
                                      self._workspace, stream=stream, gather_stream=gather_stream)
 
@@ -132,7 +156,7 @@ class Model:
         if max_norm is None:
             self._update(u, hp, t, stream)
         else:
-            gs, sq = self.clip_args()[i]
+            gs, sq = self._step_clip_args(stream)[i]
             z3.z3_reduce_scatter_norm(u.L, u.grads, u.w.grad_stride, gs, 1.0 / u.w.n_ranks, sq,
                                       stream=stream)
 
