@@ -364,6 +364,10 @@ __device__ __forceinline__ void write_clip(const NormOut &o, double sum) {
 // TB/s), 707 MB of bf16 104 us.  With a contiguous share of the run for each
 // CTA the same read was 5% slower.
 //
+// Its loads are plain ones (or streaming): this kernel may be resident while the
+// one before it, a clipping, writes what it will read, and the non-coherent
+// path is for memory that nothing writes meanwhile.
+//
 // CLUSTER: the grid is one cluster, whose first CTA adds the others' sums and
 // writes the result.
 template <typename TAB, bool CLUSTER>
@@ -386,7 +390,7 @@ k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
             for (int u = 0; u < kNormU; ++u)
                 w[u] = u * kListThreads >= n ? make_uint4(0, 0, 0, 0)
                        : tile.v0 < passing   ? __ldcs(p + u * kListThreads)
-                                             : __ldg(p + u * kListThreads);
+                                             : p[u * kListThreads];
             if (tile.kind == Z3_F32) {
                 add_batch(sum, w, [](int) { return true; });
             } else if (tile.kind == Z3_BF16) {
@@ -403,8 +407,7 @@ k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
 #pragma unroll
         for (int u = 0; u < kNormU; ++u) {
             const VecRef r = tile.ref(staged, u);
-            w[u] = r.whole() ? __ldg(reinterpret_cast<const uint4 *>(r.p))
-                             : make_uint4(0, 0, 0, 0);
+            w[u] = r.whole() ? *reinterpret_cast<const uint4 *>(r.p) : make_uint4(0, 0, 0, 0);
             kind[u] = r.kind;
             if (r.partial()) w[u] = load_partial(r);
             sums |= r.kind == Z3_SUMSQ;

@@ -1,0 +1,27 @@
+"""What the kernel sources may not hold, read as text.
+
+Kernels are launched with programmatic stream serialisation: one may be
+resident while the kernel before it still writes what it will read.  The
+non-coherent load path (ld.global.nc, __ldg, which the compiler may also move
+across the wait for that kernel) is for memory that nothing writes while the
+reading kernel runs, so it is no path for buffers that a library call writes."""
+import os
+import re
+
+import pytest
+
+from optimizer_state_gb300 import build
+
+NON_COHERENT = re.compile(r"__ldg\b|__ldlu\b|\bld\.global(?:\.\w+)*\.nc\b|\bldu\.global\b")
+
+
+def code(name):
+    """A source file without its comments."""
+    with open(os.path.join(build.CSRC, name)) as f:
+        text = f.read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+@pytest.mark.parametrize("name", ["z3_clip.cu"])
+def test_no_non_coherent_loads(name):
+    assert NON_COHERENT.findall(code(name)) == []
