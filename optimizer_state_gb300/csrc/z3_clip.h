@@ -82,7 +82,7 @@ struct NormOut {
 };
 
 struct ReduceNormArgs {
-    const uint16_t *__restrict__ grads;  // [N][stride] bf16
+    const uint16_t *grads;  // [N][stride] bf16
     int64_t stride;
     float scale;
     float *grad_shards;

@@ -42,8 +42,12 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float f[8]) {
     f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
 }
 
-__device__ __forceinline__ uint4 ld_nc(const uint16_t *p) {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+// Eight bf16 values from a 16-byte boundary.  A plain load: the kernel may have
+// started while the one before it still writes them (pdl_enter), which is
+// not what the non-coherent path is for; nor may the compiler move a plain
+// load across the wait.  No const pointer is __restrict__ for the same reason.
+__device__ __forceinline__ uint4 ld8b(const uint16_t *p) {
+    return *reinterpret_cast<const uint4 *>(p);
 }
 
 // Elements [PHI, PHI+8) of the 16-element window (lo, hi) of bf16 values.
@@ -167,8 +171,8 @@ __device__ __forceinline__ void fold_vector(const uint16_t *grads, int64_t strid
         for (int u = 0; u < RB; ++u) {
             if (k0 + u < n_ranks) {
                 const uint16_t *rp = gp + (int64_t)(k0 + u) * stride;
-                lo[u] = ld_nc(rp);
-                hi[u] = PHI ? ld_nc(rp + kVec) : lo[u];
+                lo[u] = ld8b(rp);
+                hi[u] = PHI ? ld8b(rp + kVec) : lo[u];
             }
         }
 #pragma unroll

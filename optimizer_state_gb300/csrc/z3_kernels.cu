@@ -43,7 +43,7 @@ namespace {
 // --------------------------------------------------------------------------
 
 struct GatherArgs {
-    const uint16_t *__restrict__ shards;
+    const uint16_t *shards;
     uint16_t *__restrict__ full;
 };
 
@@ -63,8 +63,8 @@ __device__ __forceinline__ void gather_tile(const Tab &tab, const GatherArgs &a,
         if (q < qend && x0[i] >= d0 && x0[i] + kVec <= d0 + len) {
             const int64_t src = x0[i] - delta - PHI;  // aligned: x0 - delta == PHI (mod 8)
             if (PHI == 0 || src + 2 * kVec <= tab.total) {
-                const uint4 lo = ld_nc(a.shards + src);
-                const uint4 hi = PHI ? ld_nc(a.shards + src + kVec) : lo;
+                const uint4 lo = ld8b(a.shards + src);
+                const uint4 hi = PHI ? ld8b(a.shards + src + kVec) : lo;
                 val[i] = window8<PHI>(lo, hi);
                 fast[i] = true;
             }
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kFlatThreads, 4) k_allreduce(const AllreduceAr
             uint4 w[kRankBatch];
 #pragma unroll
             for (int u = 0; u < kRankBatch; ++u)
-                if (k0 + u < a.n_ranks) w[u] = ld_nc(gp + (int64_t)(k0 + u) * a.stride);
+                if (k0 + u < a.n_ranks) w[u] = ld8b(gp + (int64_t)(k0 + u) * a.stride);
 #pragma unroll
             for (int u = 0; u < kRankBatch; ++u) {
                 if (k0 + u < a.n_ranks) {
@@ -442,7 +442,7 @@ struct SrcTab {
 template <typename T>
 __global__ void __launch_bounds__(kReduceThreads)
 k_reshard(const __grid_constant__ Tab tab, const __grid_constant__ SrcTab src_tab,
-          const T *__restrict__ src, T *__restrict__ dst) {
+          const T *src, T *__restrict__ dst) {
     static_assert(sizeof(T) == 2 || sizeof(T) == 4, "bf16 or fp32 words");
     pdl_enter();
     const TileRef tr = locate<true>(tab, blockIdx.x);

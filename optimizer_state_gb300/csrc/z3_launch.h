@@ -30,7 +30,7 @@ enum Mode : int {
 };
 
 struct ReduceArgs {
-    const uint16_t *__restrict__ grads;  // [N][stride] bf16
+    const uint16_t *grads;  // [N][stride] bf16
     int64_t stride;
     float scale;
     float *out;             // grad_shards (kRS, kRSAcc, kRSAdamOut)
@@ -43,7 +43,7 @@ struct ReduceArgs {
 };
 
 struct PartitionArgs {
-    const float *__restrict__ full;
+    const float *full;
     uint16_t *__restrict__ shards;
     float *__restrict__ master;
     float *__restrict__ m;
@@ -61,7 +61,7 @@ struct AdamArgs {
 };
 
 struct AllreduceArgs {
-    const uint16_t *__restrict__ grads;
+    const uint16_t *grads;
     int64_t stride;
     float *__restrict__ out;
     int64_t psi;
@@ -70,7 +70,7 @@ struct AllreduceArgs {
 };
 
 struct ScatterArgs {
-    const float *__restrict__ full;
+    const float *full;
     float *__restrict__ shards;
 };
 

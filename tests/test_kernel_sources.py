@@ -22,6 +22,9 @@ def code(name):
     return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
 
 
-@pytest.mark.parametrize("name", ["z3_clip.cu"])
+@pytest.mark.parametrize("name", sorted(n for n in os.listdir(build.CSRC)
+                                        if n.endswith((".cu", ".cuh", ".h"))))
 def test_no_non_coherent_loads(name):
     assert NON_COHERENT.findall(code(name)) == []
+    # the compiler may load through a const __restrict__ pointer that way
+    assert re.findall(r"const\s+\w+\s*\*\s*__restrict__\s*\w+", code(name)) == []
