@@ -275,18 +275,23 @@ z3_status z3_model_step(const z3_unit *units, int32_t n_units, uint16_t *const *
  * z3_step_layer: first every unit's ReduceScatter, then one norm over all
  * of them, then every unit's update.  With g all the elements of all the
  * tensors given,
- *   norm = sqrt(sum of g^2), rounded once to binary32;
+ *   norm = sqrt(sum of g^2), in binary32;
  *   coef = max_norm / norm where norm > max_norm, else 1 (binary32), and NaN
  *          where norm is not finite: +Inf or NaN among the gradients, or a
  *          norm beyond binary32.
  * Both are left in device memory, clip[0] = norm and clip[1] = coef, and the
  * calls that clip read coef there: no host synchronisation.  A NaN coef
  * means that there is no step to take: those calls then write nothing, and
- * the caller sees it in clip.  Sums of squares are held in binary64 and
- * added in an order that the sizes, and the addresses modulo 16, fix: the
- * same call gives the same bits.  Values whose squares leave binary32's range are
- * summed without loss: the norm is right over the whole range of bf16 and
- * fp32, subnormals included. */
+ * the caller sees it in clip.
+ * Squares are added in binary32 over what a thread, or in the reduce-scatter
+ * a warp, takes at a time: at most 13 roundings lie between a square and that
+ * sum.  From there on sums are pairs of binary32 or binary64.  The norm's
+ * relative error is then below 2^-21 for lists of up to 32 GB, and below 2^-19
+ * for any that fits the device's memory.  The order of the additions is fixed
+ * by the sizes and the addresses modulo 16: the same call gives the same
+ * bits.  Squares that leave binary32's range are summed scaled, so this holds
+ * over the whole range of bf16 and fp32, subnormals included (a norm that is
+ * itself subnormal is rounded to its spacing). */
 
 typedef enum z3_dtype {
     Z3_BF16 = 0,  /* gradients */
