@@ -780,16 +780,18 @@ void clip_launches(const std::vector<TAB> &tabs, const float *clip, cudaStream_t
 cudaError_t launch_grad_norm(const z3_tensor_list *list, float max_norm, float *clip,
                              NormWorkspace *ws, cudaStream_t stream) {
     const NormOut o{clip, ws, max_norm, 0, 0};
-    norm_launches(list->small, o, stream);
-    norm_launches(list->medium, o, stream);
-    norm_launches(list->large, o, stream);
+    norm_launches(list->tabs4, o, stream);
+    norm_launches(list->tabs8, o, stream);
+    norm_launches(list->tabs16, o, stream);
+    norm_launches(list->tabs32, o, stream);
     return cudaGetLastError();
 }
 
 cudaError_t launch_clip(const z3_tensor_list *list, const float *clip, cudaStream_t stream) {
-    clip_launches(list->small, clip, stream);
-    clip_launches(list->medium, clip, stream);
-    clip_launches(list->large, clip, stream);
+    clip_launches(list->tabs4, clip, stream);
+    clip_launches(list->tabs8, clip, stream);
+    clip_launches(list->tabs16, clip, stream);
+    clip_launches(list->tabs32, clip, stream);
     return cudaGetLastError();
 }
 

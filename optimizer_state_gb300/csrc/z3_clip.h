@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 #include <vector>
 
@@ -40,13 +41,22 @@ struct ListTab {
     ListEntry e[CAP + 1];
 };
 
-// The first size stays within the classic 4 KB of kernel parameters, the
-// last within the 32,764 bytes that sm_103 takes.  A table travels with its
-// launch: 2.3 us of host time with the first size, 3.5 with the second, 9
-// with the last.
-using ListSmall = ListTab<180>;
-using ListMedium = ListTab<700>;
-using ListLarge = ListTab<1900>;
+// The tensors of a table that fills `bytes` of kernel parameters together with
+// the kernel's other argument (32 bytes at most).
+constexpr int list_cap(int bytes) {
+    return (bytes - (int)offsetof(ListTab<0>, e) - 32) / (int)sizeof(ListEntry) - 1;
+}
+
+// A table travels with its launch, so its size is host time.  Each size is
+// twice the one before, from the classic 4 KB of kernel parameters to the
+// 32,764 bytes that sm_103 takes.  A norm of tensors of 5,000 fp32 takes the
+// host 4.1 us with 187 of them, 4.2 with 188, 5.4 | 6.2 with 443 | 444, 9.0 | 9.7
+// with 955 | 956 and 15.0 with 1,979: always less than the GPU takes (5.2,
+// 6.8, 10.0 and 15.7).
+using ListTab4 = ListTab<list_cap(4096)>;    //   187 tensors
+using ListTab8 = ListTab<list_cap(8192)>;    //   443
+using ListTab16 = ListTab<list_cap(16384)>;  //   955
+using ListTab32 = ListTab<list_cap(32764)>;  // 1,979
 
 // Device workspace of z3_grad_norm.
 constexpr int kNormCtas = 6;                     // resident on an SM
@@ -66,9 +76,10 @@ struct z3_tensor_list {
     uintptr_t lo = UINTPTR_MAX, hi = 0; // the addresses they span
     int32_t sums = -1;                  // a tensor that holds sums of squares, if any
     int32_t clash[2] = {-1, -1};        // two tensors that overlap, if any do
-    std::vector<z3::ListSmall> small;
-    std::vector<z3::ListMedium> medium;
-    std::vector<z3::ListLarge> large;
+    std::vector<z3::ListTab4> tabs4;
+    std::vector<z3::ListTab8> tabs8;
+    std::vector<z3::ListTab16> tabs16;
+    std::vector<z3::ListTab32> tabs32;
 };
 
 namespace z3 {
@@ -80,6 +91,11 @@ struct NormOut {
     int32_t first;  // this launch is the call's first: no carry
     int32_t last;   // its last: write clip
 };
+
+static_assert(sizeof(NormOut) <= 32 && sizeof(ListTab4) + 32 <= 4096 &&
+                  sizeof(ListTab8) + 32 <= 8192 && sizeof(ListTab16) + 32 <= 16384 &&
+                  sizeof(ListTab32) + 32 <= 32764,
+              "a table and the other argument are one launch's parameters");
 
 struct ReduceNormArgs {
     const uint16_t *grads;  // [N][stride] bf16

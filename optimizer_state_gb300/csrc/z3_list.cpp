@@ -101,9 +101,10 @@ z3_status build_list(const char *fn, const z3_tensor *tensors, int32_t n, z3_ten
     }
     find_clash(list);
     const size_t count = list->tensors.size();
-    if (count <= (size_t)ListSmall::kCap) fill_all(list->small, list->tensors);
-    else if (count <= (size_t)ListMedium::kCap) fill_all(list->medium, list->tensors);
-    else fill_all(list->large, list->tensors);
+    if (count <= (size_t)ListTab4::kCap) fill_all(list->tabs4, list->tensors);
+    else if (count <= (size_t)ListTab8::kCap) fill_all(list->tabs8, list->tensors);
+    else if (count <= (size_t)ListTab16::kCap) fill_all(list->tabs16, list->tensors);
+    else fill_all(list->tabs32, list->tensors);
     return Z3_OK;
 }
 
