@@ -34,16 +34,6 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// pdl_enter() the other way round: the next kernel may start before this
-// one's primary has completed, so that it is resident by the time this short
-// kernel ends (reduce-scatter with norm of a d = 1024 layer, one after the
-// other: 45 us, against 49).  The next kernel still waits for this one,
-// which completes after its primary; it must not be one that reads early.
-__device__ __forceinline__ void pdl_enter_early() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // --------------------------------------------------------------------------
 // sums of squares
 // --------------------------------------------------------------------------
@@ -452,9 +442,12 @@ k_grad_norm(const __grid_constant__ TAB tab, const NormOut o) {
 // the call's earlier launches.  As a launch of its own it starts while the
 // partials are computed, and its wait for them is shorter than a ticket
 // taken by every CTA and a last one's sum: 912 tickets at one address took
-// 1 us more.
+// 1 us more.  Letting the next kernel start before this wait, too, gains nothing
+// (norms one after the other: 700 tensors, 10 MB, 7.0 us against 7.2, 300
+// tensors, 17 MB, 7.7 against 7.0, 707 MB the same), and the early variants of
+// other kernels rest on its not being done.
 __global__ void __launch_bounds__(kFinishThreads) k_norm_finish(const NormOut o, int n) {
-    pdl_enter_early();
+    pdl_enter();
     constexpr int PER = (kNormMaxGrid + kFinishThreads - 1) / kFinishThreads;
     double x[PER];  // all loads in flight at once
 #pragma unroll

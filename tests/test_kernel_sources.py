@@ -28,3 +28,12 @@ def test_no_non_coherent_loads(name):
     assert NON_COHERENT.findall(code(name)) == []
     # the compiler may load through a const __restrict__ pointer that way
     assert re.findall(r"const\s+\w+\s*\*\s*__restrict__\s*\w+", code(name)) == []
+
+
+def test_every_kernel_waits_before_it_releases_the_next():
+    """The early variants of kernels read before they wait for their primary.
+    They may, as long as no kernel lets the next one start before it has
+    itself waited: then all that came before the primary is complete."""
+    order = [x for name in sorted(os.listdir(build.CSRC)) if name.endswith((".cu", ".cuh", ".h"))
+             for x in re.findall(r"griddepcontrol\.(\w+)", code(name))]
+    assert order and order == ["wait", "launch_dependents"] * (len(order) // 2)
