@@ -49,7 +49,7 @@ __device__ __forceinline__ void cluster_wait() {
 // binary64 addition.  With one for every element the reduce-scatter of a
 // d = 1024 layer with its norm took 98 us instead of 45, and with one for
 // every batch and for every step of the CTAs' trees the norm of 700 tensors
-// (10 MB) took 11.5 us instead of 9.8 (7.3 now).  A CTA's sum is stored as
+// (10 MB) took 11.5 us instead of 9.8 (6.9 now).  A CTA's sum is stored as
 // binary64.
 //
 // A batch whose sum leaves [kSafeLo, kSafeHi] may have lost squares to
@@ -319,21 +319,21 @@ __device__ __forceinline__ void add_sums(Sum &sum, const uint4 &w) {
 
 // With the CTAs resident on an SM (kNormCtas) this sets how much is in flight.
 // 3 and 6 were taken over 4 and 6, which reads 1.41 GB in 197 us instead of
-// 201 after reads, but takes 654 us instead of 610 for norm and clipping one
+// 202 after reads, but takes 631 us instead of 611 for norm and clipping one
 // after the other: its reads crowd out the write-back of what the clipping
 // before left in L2.  Lists of small tensors are near their best with 3 and 6
-// too (700 of them, 10 MB, measured together: 7.7 us; 2 and 8: 7.6; 4 and 6:
-// 7.9; 3 and 7: 8.5).
+// too (700 of them, 10 MB, one norm after the other: 6.9 us; 2 and 8: 7.1; 4
+// and 6: 6.8; 3 and 7: 7.2).
 constexpr int kNormU = 3;
 
 // Lists of few tiles (12 KB each) take one launch: a cluster of at most the
 // portable 8 CTAs, whose sums meet in shared memory.  Longer ones spread over
-// the SMs, and a second launch adds the CTAs' sums.  4,000 fp32: 2.5 us with
-// a cluster, 3.9 with two launches; 96,000 (32 tiles): 4.3 and 3.8.  The
+// the SMs, and a second launch adds the CTAs' sums.  4,000 fp32: 2.3 us with
+// a cluster, 3.2 with two launches; 96,000 (32 tiles): 4.0 and 3.4.  The
 // 12,304 sums of a d = 1024 layer take one cluster (9 tiles): its
-// reduce-scatter and norm, one after the other, 41.9 us instead of 45.8.
-// Tiles of many tensors take longer each: 1,900 of 17 fp32 (13 tiles) 10.1 us
-// two tiles to a CTA, 7.0 spread out; so they get one tile per CTA or spread.
+// reduce-scatter and norm, one after the other, 42.3 us instead of 45.1.
+// Tiles of many tensors take longer each: 1,900 of 17 fp32 (13 tiles) 9.3 us
+// two tiles to a CTA, 6.6 spread out; so they get one tile per CTA or spread.
 constexpr int kNormCluster = 8;
 
 template <typename TAB>
@@ -344,7 +344,9 @@ bool fits_cluster(const TAB &tab, int64_t tiles) {
 // The run's last vectors, 64 MB, are left in L2 for the clipping that
 // follows from the end; those before are read with the streaming hint, so
 // that they make no room for themselves.  Norm and clipping of 1.41 GB: 612
-// us, against 628 without the hint; 617 with 32 MB, 614 with 160 MB.
+// us, against 628 without the hint; 617 with 32 MB, 614 with 160 MB.  This
+// holds for lists of one table: of several, the clipping takes the tables
+// first to last (1.52 GB in 4,000 tensors, three tables: 682 us; in 1,900: 660).
 constexpr int64_t kNormKeep = (64ll << 20) / 16;
 constexpr int kFinishThreads = 256;
 
@@ -357,7 +359,7 @@ __device__ __forceinline__ void write_clip(const NormOut &o, double sum) {
 
 // One pass over the run: 2 or 4 bytes read per element and nothing written.
 // Tiles go round the CTAs of a grid that is resident at once, so that at any
-// time they read one window of the run; 1.41 GB of fp32 take 201 us (7.0
+// time they read one window of the run; 1.41 GB of fp32 take 202 us (7.0
 // TB/s), 707 MB of bf16 104 us.  With a contiguous share of the run for each
 // CTA the same read was 5% slower.
 //
@@ -489,6 +491,8 @@ constexpr int kClipU = 2;
 // read last is still in L2 (1.41 GB of fp32, norm and clipping: 628 us in the
 // other order).  Alone, that clipping takes 398 us, 7.1 TB/s; 415 with one
 // vector per thread, 399 with four, 476 with one contiguous share per CTA.
+// Where coef is 1 the CTAs still start, look their tile up and leave: 175 us for
+// those 172,609, 3.7 us for a d = 1024 layer in bf16 (8.9 with a coef).
 template <typename TAB>
 __global__ void __launch_bounds__(kListThreads, 8)
 k_clip(const __grid_constant__ TAB tab, const float *clip) {
@@ -536,8 +540,9 @@ k_clip(const __grid_constant__ TAB tab, const float *clip) {
 // z3_reduce_scatter's fold, tiles and stores; the squares are taken of the
 // registers that are stored, so the norm costs no second read of the
 // gradient (4 bytes per element) but the one barrier that joins a CTA's
-// warps: 38.6 us instead of 37.3 for the d = 1024 layer over 8 ranks, 259
-// instead of 256 for a [50257, 1024] embedding over 16.
+// warps: 37.9 us instead of 36.6 for the d = 1024 layer over 8 ranks, 259
+// instead of 256 for a [50257, 1024] embedding over 16.  At the 64 registers
+// that keep eight CTAs on an SM the aligned form spills 16 bytes per thread.
 // --------------------------------------------------------------------------
 
 // A thread's share of its tile's sum of squares: s * 2^e, in binary32 where

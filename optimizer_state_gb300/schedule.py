@@ -90,9 +90,12 @@ class Model:
 
     @property
     def step_bytes(self) -> int:
+        """HBM bytes of a step that is not clipped; a clipped one moves 8 more
+        per padded element (the fp32 gradient, stored and read back)."""
         return sum(u.step_bytes for u in self.units)
 
     def launches_per_step(self) -> int:
+        """Kernel launches of a step that is not clipped."""
         n = 0
         for u in self.units:
             tabs = -(-sum(1 for x in u.L.numel if x > 0) // 40)
@@ -161,7 +164,9 @@ class Model:
                                       stream=stream)
 
     def _finish(self, hp: dict, t: int, max_norm, stream):
-        """The rest of a clipped step, once every unit is reduced."""
+        """The rest of a clipped step, once every unit is reduced: the calls of
+        z3_model_step_clipped, but for its one launch of all updates (24
+        layers and an embedding: 3.90 ms issued from here, 3.73 there)."""
         if max_norm is None:
             return
         z3.z3_grad_norm(self._sums, max_norm, self.clip, self._workspace, stream=stream)
