@@ -392,6 +392,115 @@ z3_status z3_model_step_clipped(const z3_unit *units, const z3_clip_unit *clips,
                                 int64_t step, float max_norm, float *clip, void *workspace,
                                 z3_stream stream, z3_stream gather_stream);
 
+/* ---- losses over a vocabulary ------------------------------------------- */
+
+/* Where a step's gradients begin: the loss of a head, hidden states [tokens]
+ * [dim] times a weight [vocab][dim] (bf16 both; the weight is a parameter of a
+ * gathered unit, an embedding's where the head is tied to it), and the
+ * gradients of both, that of the weight being the parameter's part of a
+ * rank's row of `grads`.  The logits
+ *   z[t][j] = sum_c hidden[t][c] * weight[j][c]   (summed in binary32)
+ * are never stored whole: the forward calls keep each token's lse, and the
+ * gradient calls compute them again, a piece of the vocabulary at a time.
+ *
+ * A token may be left out: then its loss and lse are 0, nothing of its row of
+ * hidden, whatever it holds, reaches any result but its own, and its row of
+ * d_hidden is 0 (where the weight is finite).  Over the tokens that count
+ *   total[0] = sum_t w_t loss[t],  total[1] = sum_t w_t   (summed in binary64)
+ * with w the token's weight, 1 where weights is NULL.  A weight of 0 keeps the
+ * token's loss, and takes it out of total and of the gradients.  The gradients
+ * are those of scale * total[0] / total[1] where total is given (0 where
+ * total[1] is 0: no token counts), else of scale * total[0].  A total of several
+ * calls added up, such as every rank's, makes them those of the mean over all.
+ *
+ * Sums and softmax statistics are held in binary32.  dz, the gradient of the
+ * logits, is rounded to bf16 (the operand type of the two products that
+ * follow, whose sums are binary32), each result once more at its end.  Results
+ * depend on the sizes only: the same call gives the same bits.  A head whose
+ * logits are not finite has a NaN loss and gradient.
+ *
+ * dim is a multiple of 8, at most 2^31 - 1024 as are tokens and vocab (a call
+ * of 0 tokens writes total = {0, 0}, and zeros to d_weight); strides are in
+ * elements, >= dim and multiples of 8.  hidden, weight, d_hidden, d_weight and
+ * the workspace start on a 16-byte boundary, the other buffers on one of their
+ * elements.  Errors: sizes out of these ranges, a NULL buffer, a workspace
+ * that is too small, an output or the workspace overlapping another buffer of
+ * the call, scale not finite (INVALID_ARG); strides, boundaries (ALIGNMENT);
+ * sizes whose workspace no memory holds (OVERFLOW). */
+typedef struct z3_head {
+    const uint16_t *hidden; /* bf16 [tokens][hidden_stride] */
+    int64_t hidden_stride;
+    const uint16_t *weight; /* bf16 [vocab][weight_stride] */
+    int64_t weight_stride;
+    int64_t tokens;
+    int64_t vocab;
+    int64_t dim;
+    const float *weights; /* [tokens], or NULL */
+} z3_head;
+
+/* Bytes of the workspace of the calls below, for at most these sizes' call:
+ * k the length of the teacher's lists (0: cross entropy), grads != 0 with the
+ * gradient calls.  What it holds before a call does not matter and nothing is
+ * kept in it between calls; calls that may overlap on the GPU, captured ones
+ * among them, need one each. */
+z3_status z3_head_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, int32_t k,
+                                  int32_t grads, int64_t *bytes);
+
+/* Softmax cross entropy with a target word for each token:
+ *   lse[t] = log sum_j exp(z[t][j]);  loss[t] = lse[t] - z[t][targets[t]].
+ * targets: int32 or int64 [tokens] (index_bytes 4 or 8).  A negative target
+ * leaves the token out; one >= vocab reads nothing, and makes the token's loss
+ * NaN and all gradients with it.  loss, lse (float [tokens]) and total (float
+ * [2]) are written. */
+z3_status z3_xent(const z3_head *head, const void *targets, int32_t index_bytes, float *loss,
+                  float *lse, float *total, void *workspace, int64_t workspace_bytes,
+                  z3_stream stream);
+
+/* Its gradients, with a_t = scale * w_t / total[1] (scale * w_t where total is NULL):
+ *   dz[t][j] = a_t * (exp(z[t][j] - lse[t]) - (j == targets[t]));
+ *   d_hidden[t][c] = sum_j dz[t][j] * weight[j][c];
+ *   d_weight[j][c] = sum_t dz[t][j] * hidden[t][c].
+ * lse and total: what z3_xent wrote (total: or the sum of several calls').
+ * d_hidden (bf16 [tokens][d_hidden_stride]) and d_weight (bf16 [vocab]
+ * [d_weight_stride]) are written, each unless NULL; the gap between dim and a
+ * stride stays as it is. */
+z3_status z3_xent_grad(const z3_head *head, const void *targets, int32_t index_bytes,
+                       const float *lse, const float *total_or_NULL, float scale,
+                       uint16_t *d_hidden_or_NULL, int64_t d_hidden_stride,
+                       uint16_t *d_weight_or_NULL, int64_t d_weight_stride, void *workspace,
+                       int64_t workspace_bytes, z3_stream stream);
+
+/* A teacher's k highest logits for each token, in any order: [tokens][k] of
+ * dtype Z3_BF16 or Z3_F32, and the words that they belong to, int32 or int64
+ * [tokens][k] (index_bytes 4 or 8).  1 <= k <= 1024.  An entry with a negative
+ * index or a logit of -Inf is left out, and a token without any other; an
+ * index >= vocab reads nothing and makes the token's loss and all gradients NaN.
+ * A word may stand in a list more than once: its shares add up. */
+typedef struct z3_teacher {
+    const void *logits;
+    const void *index;
+    int32_t dtype; /* z3_dtype */
+    int32_t index_bytes;
+    int32_t k;
+    float temperature; /* tau > 0; tau^2 and 2 / tau finite in binary32 */
+} z3_teacher;
+
+/* Divergence of the head's softmax from the teacher's, over the whole vocabulary
+ * and over the list, both at the temperature tau:
+ *   q[t] = softmax(logits[t] / tau);  lse[t] = log sum_j exp(z[t][j] / tau);
+ *   loss[t] = tau^2 * sum_i q[t][i] * (log q[t][i] - z[t][index[t][i]] / tau + lse[t]).
+ * Outputs as z3_xent. */
+z3_status z3_distill(const z3_head *head, const z3_teacher *teacher, float *loss, float *lse,
+                     float *total, void *workspace, int64_t workspace_bytes, z3_stream stream);
+
+/* Its gradients, as z3_xent_grad, with
+ *   dz[t][j] = a_t * tau * (exp(z[t][j] / tau - lse[t]) - sum of q[t][i] over index[t][i] == j). */
+z3_status z3_distill_grad(const z3_head *head, const z3_teacher *teacher, const float *lse,
+                          const float *total_or_NULL, float scale, uint16_t *d_hidden_or_NULL,
+                          int64_t d_hidden_stride, uint16_t *d_weight_or_NULL,
+                          int64_t d_weight_stride, void *workspace, int64_t workspace_bytes,
+                          z3_stream stream);
+
 /* ---- the layer step fed from host memory ------------------------------- */
 
 /* A pipeline that runs z3_step_layer on gradients held in host memory and

@@ -26,8 +26,10 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-f
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", f"-I{INCLUDE}"]
 
 SOURCES = [("z3_layout.cpp", "cxx"), ("z3_list.cpp", "cxx"), ("z3_api.cpp", "cxx"),
-           ("z3_kernels.cu", "nvcc"), ("z3_clip.cu", "nvcc"), ("z3_noalloc.cu", "nvcc")]
-HEADERS = ["z3_internal.h", "z3_launch.h", "z3_device.cuh", "z3_clip.h"]
+           ("z3_kernels.cu", "nvcc"), ("z3_clip.cu", "nvcc"), ("z3_noalloc.cu", "nvcc"),
+           ("z3_head_api.cpp", "cxx"), ("z3_head.cu", "nvcc")]
+HEADERS = ["z3_internal.h", "z3_launch.h", "z3_device.cuh", "z3_clip.h", "z3_check.h", "z3_head.h",
+           "z3_mma.cuh"]
 
 
 def _nvcc() -> str:

@@ -4,7 +4,6 @@
 // (z3_model_step, z3_model_step_clipped) orders its launches on two streams
 // with CUDA events.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
 #include <cmath>
@@ -13,6 +12,7 @@
 #include <string>
 #include <vector>
 
+#include "z3_check.h"
 #include "z3_clip.h"
 #include "z3_launch.h"
 
@@ -22,34 +22,6 @@ namespace {
 // --------------------------------------------------------------------------
 // argument validation and launch-error reporting
 // --------------------------------------------------------------------------
-
-struct Buf {
-    const void *ptr;
-    int64_t bytes;
-    const char *name;
-};
-
-z3_status check_bufs(const char *fn, const Buf *bufs, int n) {
-    for (int i = 0; i < n; ++i) {
-        if (bufs[i].bytes == 0) continue;
-        if (bufs[i].ptr == nullptr)
-            return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": " + bufs[i].name + " is NULL");
-        if (reinterpret_cast<uintptr_t>(bufs[i].ptr) % 16 != 0)
-            return fail(Z3_ERR_ALIGNMENT,
-                        std::string(fn) + ": " + bufs[i].name + " is not 16-byte aligned");
-    }
-    for (int i = 0; i < n; ++i) {
-        for (int j = i + 1; j < n; ++j) {
-            if (bufs[i].bytes == 0 || bufs[j].bytes == 0) continue;
-            const uintptr_t a0 = reinterpret_cast<uintptr_t>(bufs[i].ptr);
-            const uintptr_t b0 = reinterpret_cast<uintptr_t>(bufs[j].ptr);
-            if (a0 < b0 + (uintptr_t)bufs[j].bytes && b0 < a0 + (uintptr_t)bufs[i].bytes)
-                return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": " + bufs[i].name +
-                                                    " overlaps " + bufs[j].name);
-        }
-    }
-    return Z3_OK;
-}
 
 z3_status check_grads(const char *fn, const z3_layout *L, int64_t grad_stride, int64_t *bytes) {
     if (grad_stride < L->psi)
@@ -99,22 +71,6 @@ z3_status adam_constants(const char *fn, const z3_adam_hp *hp, int64_t step, Ada
         return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": eps rounds to 0 in binary32");
     return Z3_OK;
 }
-
-z3_status launched(const char *fn, cudaError_t err) {
-    if (err != cudaSuccess)
-        return fail(Z3_ERR_CUDA, std::string(fn) + ": " + cudaGetErrorString(err));
-    return Z3_OK;
-}
-
-// Host-side NVTX range around the launches of one call, named after the
-// collective it enqueues, so a trace shows the AllGather / ReduceScatter /
-// update pattern of "The ZeRO-3 Diagram Most People Remember Is Wrong", s.6.
-struct Range {
-    explicit Range(const char *name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-    Range(const Range &) = delete;
-    Range &operator=(const Range &) = delete;
-};
 
 // early: see launch_allgather / launch_reduce.  Only the calls that enqueue
 // several dependent launches pass true, for a launch whose stream

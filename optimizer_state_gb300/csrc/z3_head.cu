@@ -1,0 +1,1001 @@
+// z3_head.cu -- softmax cross entropy and distillation over a large
+// vocabulary, whose logits are never stored.
+//
+// With z = hidden weight^T, a forward call is one product whose epilogue keeps
+// of each tile only every row's maximum and sum of exponentials (and the few
+// logits that the row's target or list names); k_head_join joins the tiles.
+// A gradient call walks the vocabulary in pieces: the piece's logits are
+// computed once more, their epilogue turns them into dz (bf16, in the
+// workspace), and two products of dz give this piece's rows of d_weight and
+// its share of d_hidden.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "z3_device.cuh"
+#include "z3_head.h"
+#include "z3_mma.cuh"
+
+namespace z3 {
+namespace {
+
+constexpr int kBK = 64;           // values of K in a stage: one swizzled row of 128 bytes
+constexpr int kMmaThreads = 256;  // warps: TMA, products, tensor memory, -, 4 x epilogue
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// --------------------------------------------------------------------------
+// the tiled product
+// --------------------------------------------------------------------------
+
+enum Epilogue { kStats, kDz, kOut };
+
+struct MmaArgs {
+    CUtensorMap a, b;
+    Cut cut;
+    int32_t n_fast;        // walk a row of tiles before the next row
+    int32_t b_n, b_k;      // where in b's map this call's columns and depth begin
+    int64_t rows, cols;    // valid extent of the result
+    // kStats, kDz
+    float beta;            // log2(e) / temperature: exponents are powers of two
+    int32_t col0;          // the word of column 0
+    int32_t k;             // list length
+    int32_t first_pitch;   // of `first`
+    const int32_t *index;  // lists by ascending word, where each tile's entries begin
+    const float *q;
+    const uint16_t *first;
+    // kStats
+    float2 *part;
+    float *z;
+    const void *targets;
+    int32_t target_bytes;
+    // kDz
+    const float2 *row;
+    const int32_t *words;
+    uint16_t *dz;
+    int64_t dz_pitch;
+    // kOut
+    float *slab;           // null: nothing to add up
+    int64_t slab_stride;
+    int32_t add;           // the slab holds the sums so far
+    int32_t store_slab;
+    uint16_t *out;
+    int64_t out_pitch;
+};
+
+__device__ __forceinline__ int64_t load_index(const void *p, int bytes, int64_t i) {
+    return bytes == 8 ? static_cast<const int64_t *>(p)[i]
+                      : (int64_t)static_cast<const int32_t *>(p)[i];
+}
+
+template <int BN, int CG>
+__host__ __device__ constexpr int stage_bytes() {
+    return 128 * kBK * 2 + BN / CG * kBK * 2;
+}
+template <int BN, int CG>
+__host__ __device__ constexpr int stages() {
+    return 196608 / stage_bytes<BN, CG>();
+}
+template <int BN, int CG>
+__host__ __device__ constexpr int smem_bytes() {  // beyond half an SM's: one CTA's tensor memory to an SM
+    return stages<BN, CG>() * stage_bytes<BN, CG>() + 1024 + 512;
+}
+
+struct Tile {
+    int m, n, split;
+};
+
+__device__ __forceinline__ Tile tile_of(const MmaArgs &p, int item) {
+    const int tiles = p.cut.m_tiles * p.cut.n_tiles;
+    Tile t;
+    t.split = item / tiles;
+    int i = item - t.split * tiles;
+    if (p.n_fast) {
+        t.m = i / p.cut.n_tiles;
+        t.n = i - t.m * p.cut.n_tiles;
+    } else {
+        constexpr int kGroup = 32;  // row tiles whose operand stays in L2
+        const int per = kGroup * p.cut.n_tiles;
+        const int g = i / per;
+        const int rows = min(kGroup, p.cut.m_tiles - g * kGroup);
+        i -= g * per;
+        t.n = i / rows;
+        t.m = g * kGroup + i - t.n * rows;
+    }
+    return t;
+}
+
+// value of register `j` of a thread's own choice
+__device__ __forceinline__ float pick(const float (&v)[32], uint32_t j) {
+    float x = v[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) x = j == (uint32_t)i ? v[i] : x;
+    return x;
+}
+
+// D[m][n] = sum_k A(m, k) B(n, k), tile by tile; AMN, BMN: the operand's rows run
+// along M or N rather than K.  One thread feeds TMA, one issues the products
+// of 128 x CG rows by BN columns, four warps take a finished tile out of
+// tensor memory while the next one is computed beside it.
+// Every wait ends (mbar_wait); an epilogue whose tile did not come takes NaN
+// for its values.
+template <int CG, int BN, bool AMN, bool BMN, Epilogue EPI, bool LIST>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+k_head_mma(const __grid_constant__ MmaArgs p) {
+    constexpr int S = stages<BN, CG>();
+    constexpr int kA = 128 * kBK * 2;
+    constexpr int kStage = stage_bytes<BN, CG>();
+    constexpr int kBRows = BN / CG;  // of b that this CTA loads
+    constexpr int kCols = 2 * BN;    // of tensor memory: two tiles
+    extern __shared__ uint8_t raw[];
+    const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
+    const uint32_t bars = base + S * kStage;
+    auto full = [&](int i) { return bars + 8 * i; };
+    auto empty = [&](int i) { return bars + 8 * (S + i); };
+    auto tfull = [&](int i) { return bars + 8 * (2 * S + i); };
+    auto tempty = [&](int i) { return bars + 8 * (2 * S + 2 + i); };
+    const uint32_t tmem_at = bars + 8 * (2 * S + 4);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = CG == 1 ? 0 : cluster_rank();
+    const int group = blockIdx.x / CG, groups = gridDim.x / CG;
+    const int items = p.cut.m_tiles * p.cut.n_tiles * p.cut.splits;
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_map(&p.a);
+        tma_prefetch_map(&p.b);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull(i), 1);
+            mbar_init(tempty(i), 4 * CG);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc<CG>(tmem_at, kCols);
+    __syncwarp();
+    tmem_fence_before();
+    group_sync<CG>();
+    if constexpr (CG > 1) __syncthreads();
+    tmem_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at) : "memory");
+
+    if (warp == 0 && lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int item = group; ok && item < items; item += groups) {
+            const Tile t = tile_of(p, item);
+            const int m0 = t.m * (128 * CG) + (int)rank * 128;
+            const int n0 = p.b_n + t.n * BN + (int)rank * kBRows;
+            const int k0 = t.split * p.cut.k_chunk;
+            const int k1 = min(p.cut.k_tiles, k0 + p.cut.k_chunk);
+            for (int kt = k0; kt < k1; ++kt) {
+                ok = mbar_wait(empty(stage), phase ^ 1);
+                if (!ok) break;
+                const uint32_t a = base + stage * kStage, b = a + kA;
+                if (rank == 0) mbar_expect(full(stage), CG * kStage);
+                const uint32_t bar = CG == 1 ? full(stage) : in_leader(full(stage));
+                const int ka = kt * kBK, kb = p.b_k + kt * kBK;
+                if constexpr (AMN) {
+                    for (int i = 0; i < 2; ++i)
+                        tma_load<CG>(a + i * (64 * kBK * 2), &p.a, bar, m0 + 64 * i, ka);
+                } else {
+                    tma_load<CG>(a, &p.a, bar, ka, m0);
+                }
+                if constexpr (BMN) {
+                    for (int i = 0; i < kBRows / 64; ++i)
+                        tma_load<CG>(b + i * (64 * kBK * 2), &p.b, bar, n0 + 64 * i, kb);
+                } else {
+                    tma_load<CG>(b, &p.b, bar, kb, n0);
+                }
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        // until the last products have read their stages: the peer's barriers and
+        // memory are in use up to then
+        for (int i = 0; ok && i < S; ++i) {
+            ok = mbar_wait(empty(stage), phase ^ 1);
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = mma_desc(128 * CG, BN, AMN, BMN);
+        constexpr uint32_t kStepA = AMN ? 16 * 128 / 16 : 32 / 16;  // 16 values of K on
+        constexpr uint32_t kStepB = BMN ? 16 * 128 / 16 : 32 / 16;
+        int stage = 0, done = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int item = group; ok && item < items; item += groups, ++done) {
+            const Tile t = tile_of(p, item);
+            const int k0 = t.split * p.cut.k_chunk;
+            const int k1 = min(p.cut.k_tiles, k0 + p.cut.k_chunk);
+            const int buf = done & 1;
+            const uint32_t d = tmem + buf * BN;
+            ok = mbar_wait(tempty(buf), ((done >> 1) & 1) ^ 1);
+            tmem_fence_after();
+            for (int kt = k0; ok && kt < k1; ++kt) {
+                ok = mbar_wait(full(stage), phase);
+                if (!ok) break;
+                tmem_fence_after();
+                const uint32_t a = base + stage * kStage;
+                const uint64_t da = operand_desc<AMN>(a, 64 * kBK * 2);
+                const uint64_t db = operand_desc<BMN>(a + kA, 64 * kBK * 2);
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma<CG>(d, da + k * kStepA, db + k * kStepB, idesc, kt > k0 || k > 0);
+                mma_commit<CG>(empty(stage));
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok) mma_commit<CG>(tfull(buf));
+        }
+    } else if (warp >= 4) {
+        const int quad = warp - 4;  // its 32 lanes of tensor memory
+        int done = 0;
+        bool ok = true;
+        for (int item = group; item < items; item += groups, ++done) {
+            const Tile t = tile_of(p, item);
+            const int64_t row = (int64_t)t.m * (128 * CG) + rank * 128 + quad * 32 + lane;
+            const bool live = row < p.rows;
+            const int n0 = t.n * BN;
+            const int cols = (int)min((int64_t)BN, p.cols - n0);  // valid ones of this tile
+            // what the row asks of this tile's words
+            [[maybe_unused]] int next = 0x7fffffff;   // column of the next one asked for
+            [[maybe_unused]] int at = 0, end = 0;     // list entries of this tile
+            [[maybe_unused]] float2 rw = make_float2(0.0f, 0.0f);
+            if constexpr (EPI != kOut) {
+                if (live) {
+                    if constexpr (LIST) {
+                        const int w0 = (p.col0 + n0) / BN;
+                        const uint16_t *f = p.first + row * p.first_pitch + w0;
+                        at = f[0];
+                        end = f[1];
+                        if (at < end) next = p.index[row * p.k + at] - p.col0 - n0;
+                    } else {
+                        const int64_t w = EPI == kStats
+                                              ? load_index(p.targets, p.target_bytes, row)
+                                              : (int64_t)p.words[row];
+                        const int64_t c = w - p.col0 - n0;
+                        if (w >= 0 && c >= 0 && c < cols) next = (int)c;
+                    }
+                    if constexpr (EPI == kDz) rw = p.row[row];
+                }
+            }
+            [[maybe_unused]] auto advance = [&] {
+                next = 0x7fffffff;
+                if constexpr (LIST)
+                    if (++at < end) next = p.index[row * p.k + at] - p.col0 - n0;
+            };
+            const int buf = done & 1;
+            if (ok) ok = mbar_wait(tfull(buf), (done >> 1) & 1);
+            tmem_fence_after();
+            const uint32_t d = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
+            [[maybe_unused]] float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) {
+                uint32_t bits[32];
+                tmem_load32(d + c, bits);
+                tmem_wait_load();
+                if (c + 32 == BN) {
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_leader(tempty(buf)));
+                }
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = ok ? __uint_as_float(bits[j]) : NAN;
+                if constexpr (EPI == kStats) {
+                    while (next < c + 32) {
+                        const float x = pick(v, (uint32_t)(next - c));
+                        p.z[LIST ? row * p.k + at : row] = x;
+                        advance();
+                    }
+                    // powers of two: exp(z / temperature) = 2^(beta z)
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        v[j] = c + j < cols ? __fmul_rn(v[j], p.beta) : -INFINITY;
+                        m = fmaxf(m, v[j]);
+                    }
+                    const float new_top = fmaxf(top, m);
+                    const float shift = new_top == -INFINITY ? 0.0f : new_top;
+                    float s = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        s = __fadd_rn(s, exp2_fast(__fsub_rn(v[j], shift)));
+                    sum = __fmaf_rn(sum, exp2_fast(__fsub_rn(top, shift)), s);
+                    top = new_top;
+                } else if constexpr (EPI == kDz) {
+                    const bool none = rw.x == 0.0f;  // also where the logits are not finite
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float e = exp2_fast(__fmaf_rn(v[j], p.beta, -rw.y));
+                        v[j] = none || c + j >= cols ? 0.0f : __fmul_rn(e, rw.x);
+                    }
+                    while (next < c + 32) {
+                        float q = rw.x;
+                        if constexpr (LIST) q = __fmul_rn(q, p.q[row * p.k + at]);
+                        const int hit = next - c;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j == hit) v[j] = __fsub_rn(v[j], q);
+                        advance();
+                    }
+                    if (live) {
+                        uint16_t *o = p.dz + row * p.dz_pitch + n0 + c;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            // rounded once to bf16, the type of the products' operands
+                            const uint4 w = make_uint4(
+                                pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+                            *reinterpret_cast<uint4 *>(o + j) = w;
+                        }
+                    }
+                } else {
+                    if (live) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            if (c + j >= cols) break;  // cols is a multiple of 8
+                            float *f = p.slab + t.split * p.slab_stride + row * p.cols + n0 + c + j;
+                            float4 *f4 = reinterpret_cast<float4 *>(f);
+                            if (p.add) {
+                                const float4 x = f4[0], y = f4[1];
+                                v[j] += x.x; v[j + 1] += x.y; v[j + 2] += x.z; v[j + 3] += x.w;
+                                v[j + 4] += y.x; v[j + 5] += y.y; v[j + 6] += y.z; v[j + 7] += y.w;
+                            }
+                            if (p.store_slab) {
+                                f4[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                                f4[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+                            } else {
+                                *reinterpret_cast<uint4 *>(p.out + row * p.out_pitch + n0 + c + j) =
+                                    make_uint4(pack_bf16x2(v[j], v[j + 1]),
+                                               pack_bf16x2(v[j + 2], v[j + 3]),
+                                               pack_bf16x2(v[j + 4], v[j + 5]),
+                                               pack_bf16x2(v[j + 6], v[j + 7]));
+                            }
+                        }
+                    }
+                }
+            }
+            if constexpr (EPI == kStats)
+                if (live) p.part[t.n * p.rows + row] = make_float2(top, sum);
+        }
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    group_sync<CG>();
+    tmem_fence_after();
+    if (warp == 2) tmem_free<CG>(tmem, kCols);
+}
+
+// --------------------------------------------------------------------------
+// the small kernels around it
+// --------------------------------------------------------------------------
+
+// Everything the forward's join and the gradient's factors need of a token.
+struct RowArgs {
+    int64_t tokens, vocab, dim;
+    int32_t k;             // 0: cross entropy
+    int32_t n_tiles;
+    int32_t index_bytes, teacher_bytes;
+    const void *index;
+    const void *teacher;
+    const float *weights;
+    float temperature;
+    int8_t *state;
+    int32_t *list;
+    float *q;
+    uint16_t *first;
+    int32_t first_pitch;
+    int32_t tile;          // words of a column tile
+};
+
+__device__ __forceinline__ Row state_of(const RowArgs &a, int64_t t, int64_t *word) {
+    if (a.k > 0) return (Row)a.state[t];
+    *word = load_index(a.index, a.index_bytes, t);
+    return *word < 0 ? kLeftOut : *word < a.vocab ? kCounts : kBad;
+}
+
+constexpr int kListSort = 128;  // threads
+
+// A token's list by ascending word, with q = softmax(teacher / temperature), and
+// where each column tile's entries begin.  Entries of a negative word or a
+// logit of -Inf are left out (at the end, q = 0); a word beyond the vocabulary
+// spoils the row.  One CTA to a token: a bitonic sort of (word, place), so that
+// equal words keep their order.
+__global__ void __launch_bounds__(kListSort) k_head_lists(const RowArgs a, int pow2) {
+    extern __shared__ uint64_t key[];
+    __shared__ float red[kListSort / 32];
+    __shared__ int bad;
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x;
+    // the maximum; a NaN stays
+    auto larger = [](float x, float y) { return isnan(x) ? x : isnan(y) || y > x ? y : x; };
+    auto logit = [&](int i) {
+        return a.teacher_bytes == 2
+                   ? bf16_to_f32(static_cast<const uint16_t *>(a.teacher)[t * a.k + i])
+                   : static_cast<const float *>(a.teacher)[t * a.k + i];
+    };
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    float top = -INFINITY;
+    for (int i = tid; i < pow2; i += kListSort) {
+        uint32_t word = 0x7fffffffu;
+        if (i < a.k) {
+            const int64_t w = load_index(a.index, a.index_bytes, t * a.k + i);
+            const float x = logit(i);
+            if (w >= a.vocab) {
+                bad = 1;
+            } else if (w >= 0 && x != -INFINITY) {
+                word = (uint32_t)w;
+                top = larger(top, x);
+            }
+        }
+        key[i] = (uint64_t)word << 32 | (uint32_t)i;
+    }
+    for (int o = 16; o > 0; o /= 2) top = larger(top, __shfl_xor_sync(~0u, top, o));
+    if (tid % 32 == 0) red[tid / 32] = top;
+    __syncthreads();
+    for (int i = 0; i < kListSort / 32; ++i) top = larger(top, red[i]);
+    for (int size = 2; size <= pow2; size *= 2) {
+        for (int stride = size / 2; stride > 0; stride /= 2) {
+            __syncthreads();
+            for (int i = tid; i < pow2 / 2; i += kListSort) {
+                const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
+                const uint64_t x = key[lo], y = key[hi];
+                if ((x > y) == ((lo & size) == 0)) {
+                    key[lo] = y;
+                    key[hi] = x;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    auto begin = [&](uint32_t word) {  // the first entry of this word or a later one
+        int lo = 0, hi = a.k;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if ((uint32_t)(key[mid] >> 32) < word) lo = mid + 1; else hi = mid;
+        }
+        return lo;
+    };
+    const int count = begin(0x7fffffffu);
+    const float inv = __fdiv_rn(1.0f, a.temperature);
+    float sum = 0.0f;
+    for (int i = tid; i < count; i += kListSort)
+        sum += exp2f((logit((int)(uint32_t)key[i]) - top) * inv * kLog2e);
+    for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
+    if (tid % 32 == 0) red[tid / 32] = sum;  // `top` has been read: a barrier lies between
+    __syncthreads();
+    sum = 0.0f;
+    for (int i = 0; i < kListSort / 32; ++i) sum += red[i];
+    const float norm = __fdiv_rn(1.0f, sum);
+    for (int i = tid; i < a.k; i += kListSort) {
+        a.list[t * a.k + i] = (int32_t)(key[i] >> 32);
+        a.q[t * a.k + i] =
+            i < count ? exp2f((logit((int)(uint32_t)key[i]) - top) * inv * kLog2e) * norm : 0.0f;
+    }
+    for (int n = tid; n < a.first_pitch; n += kListSort)
+        a.first[t * a.first_pitch + n] =
+            (uint16_t)min(count, begin((uint32_t)min((int64_t)n * a.tile, (int64_t)0x7fffffff)));
+    if (tid == 0) a.state[t] = bad ? kBad : count > 0 ? kCounts : kLeftOut;
+}
+
+struct JoinArgs {
+    RowArgs row;
+    const float2 *part;
+    const float *z;
+    double2 *sums;         // of each block
+    unsigned *done;        // 0 at the start
+    float *loss, *lse, *total;
+};
+
+constexpr int kJoinThreads = 256;
+
+// Joins the column tiles' maxima and sums, TOK tokens to a block, and finishes
+// each token's loss; the last block adds up the blocks' sums in their order.
+// Bound by latency: with 8192 tokens it reads 13 MB.  Few tokens take a block
+// each.
+template <int TOK>
+__global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
+    constexpr int kSlices = kJoinThreads / TOK;
+    __shared__ float2 joined[kSlices][TOK];
+    __shared__ float lists[kSlices][TOK];
+    __shared__ float lse2s[TOK];
+    __shared__ double2 pair[kJoinThreads];
+    __shared__ bool last;
+    const int tok = threadIdx.x % TOK, slice = threadIdx.x / TOK;
+    const int64_t t = (int64_t)blockIdx.x * TOK + tok;
+    const bool live = t < a.row.tokens;
+    auto join = [](float2 x, float2 y) {
+        const float m = fmaxf(x.x, y.x);
+        const float s = m == -INFINITY ? 0.0f : m;
+        return make_float2(m, __fmaf_rn(x.y, exp2_fast(x.x - s), y.y * exp2_fast(y.x - s)));
+    };
+    float2 acc = make_float2(-INFINITY, 0.0f);
+    if (live) {
+#pragma unroll 4
+        for (int n = slice; n < a.row.n_tiles; n += kSlices)
+            acc = join(acc, a.part[(int64_t)n * a.row.tokens + t]);
+    }
+    joined[slice][tok] = acc;
+    __syncthreads();
+    for (int w = kSlices / 2; w > 0; w /= 2) {
+        if (slice < w) joined[slice][tok] = join(joined[slice][tok], joined[slice + w][tok]);
+        __syncthreads();
+    }
+    if (slice == 0)  // a sum that is not a number stays one through the logarithm
+        lse2s[tok] = joined[0][tok].x + log2f(joined[0][tok].y);
+    __syncthreads();
+    const float lse = lse2s[tok] * kLn2;
+    int64_t word = 0;
+    const Row state = live ? state_of(a.row, t, &word) : kLeftOut;
+    if (a.row.k > 0) {
+        float part = 0.0f;
+        const float inv = __fdiv_rn(1.0f, a.row.temperature);
+        if (state == kCounts) {
+            for (int i = slice; i < a.row.k; i += kSlices) {
+                const float q = a.row.q[t * a.row.k + i];
+                // 0 log 0 = 0: an entry left out, or one whose q is below binary32
+                if (q != 0.0f)
+                    part += q * (logf(q) - a.z[t * a.row.k + i] * inv + lse);
+            }
+        }
+        lists[slice][tok] = part;
+        __syncthreads();
+        for (int w = kSlices / 2; w > 0; w /= 2) {
+            if (slice < w) lists[slice][tok] += lists[slice + w][tok];
+            __syncthreads();
+        }
+    }
+    double2 mine = make_double2(0.0, 0.0);
+    if (slice == 0 && live) {
+        float loss = 0.0f;
+        if (state == kBad)
+            loss = NAN;
+        else if (state == kCounts)
+            loss = a.row.k > 0 ? a.row.temperature * a.row.temperature * lists[0][tok]
+                               : lse - a.z[t];
+        a.loss[t] = loss;
+        a.lse[t] = state == kLeftOut ? 0.0f : lse;
+        const float w = state == kLeftOut ? 0.0f : a.row.weights ? a.row.weights[t] : 1.0f;
+        if (w != 0.0f) mine = make_double2((double)w * (double)loss, (double)w);
+    }
+    auto total = [&] {  // over the block, in a fixed order
+        __syncthreads();
+        pair[threadIdx.x] = mine;
+        __syncthreads();
+        for (int w = kJoinThreads / 2; w > 0; w /= 2) {
+            if (threadIdx.x < w) {
+                pair[threadIdx.x].x += pair[threadIdx.x + w].x;
+                pair[threadIdx.x].y += pair[threadIdx.x + w].y;
+            }
+            __syncthreads();
+        }
+    };
+    total();
+    if (threadIdx.x == 0) {
+        a.sums[blockIdx.x] = pair[0];
+        __threadfence();
+        last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    mine = make_double2(0.0, 0.0);
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) {
+        const double2 x = __ldcg(a.sums + i);  // from L2, where the other blocks left them
+        mine.x += x.x;
+        mine.y += x.y;
+    }
+    total();
+    if (threadIdx.x == 0) {
+        a.total[0] = (float)pair[0].x;
+        a.total[1] = (float)pair[0].y;
+    }
+}
+
+struct FactorArgs {
+    RowArgs row;
+    const float *lse;
+    const float *total;    // or null
+    float scale;
+    float2 *factor;
+    int32_t *words;
+    const uint16_t *hidden;
+    int64_t stride;
+    uint16_t *copy;        // null: not needed
+};
+
+// Each token's factor a = scale w / total[1] (times the temperature) and its
+// lse in powers of two; and the hidden states with zeros in the rows left out:
+// what stands there may be anything, and 0 * NaN would reach d_weight.  The
+// copy costs 4 bytes a value, 5 us of the 1.9 ms at 8192 x 1024.
+__global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
+    const int64_t t = blockIdx.x;
+    int64_t word = -1;
+    const Row state = state_of(a.row, t, &word);
+    float f = a.scale;
+    if (a.total) f = a.total[1] == 0.0f ? 0.0f : __fdiv_rn(f, a.total[1]);
+    if (a.row.weights && state != kLeftOut) f = __fmul_rn(f, a.row.weights[t]);
+    if (a.row.k > 0) f = __fmul_rn(f, a.row.temperature);
+    if (state == kLeftOut) f = 0.0f;
+    if (state == kBad) f = NAN;
+    if (threadIdx.x == 0) {
+        a.factor[t] = make_float2(f, __fmul_rn(a.lse[t], kLog2e));
+        if (a.row.k == 0) a.words[t] = state == kCounts ? (int32_t)word : -1;
+    }
+    if (a.copy == nullptr) return;
+    const bool keep = f != 0.0f;
+    for (int64_t i = threadIdx.x * 8; i < a.row.dim; i += 128 * 8) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (keep) x = ld8b(a.hidden + t * a.stride + i);
+        *reinterpret_cast<uint4 *>(a.copy + t * a.row.dim + i) = x;
+    }
+}
+
+// The splits' sums, in their order, rounded once to bf16.
+__global__ void __launch_bounds__(256) k_head_slabs(const float *slab, int splits, int64_t stride,
+                                                    int64_t rows, int64_t cols, uint16_t *out,
+                                                    int64_t pitch) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= rows * cols) return;
+    const int64_t r = i / cols, c = i - r * cols;
+    float v[8] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float4 *f = reinterpret_cast<const float4 *>(slab + s * stride + i);
+        const float4 x = f[0], y = f[1];
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+    }
+    *reinterpret_cast<uint4 *>(out + r * pitch + c) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+}
+
+// --------------------------------------------------------------------------
+// host side: cutting, tensor maps, launches
+// --------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled f = [] {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                             cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return (EncodeTiled)fn;
+    }();
+    return f;
+}
+
+// Rows of `inner` bf16 values, `pitch` apart, in boxes of 64 values by box_rows;
+// zeros outside.
+bool make_map(CUtensorMap *m, const void *p, int64_t inner, int64_t outer, int64_t pitch,
+              int box_rows) {
+    const EncodeTiled encode = encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t ones[2] = {1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG, int BN, bool AMN, bool BMN, Epilogue EPI, bool LIST>
+cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
+    auto *kernel = k_head_mma<CG, BN, AMN, BMN, EPI, LIST>;
+    constexpr int smem = smem_bytes<BN, CG>();
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)p.cut.m_tiles * p.cut.n_tiles * p.cut.splits;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, kHeadSMs / CG)));
+    cfg.blockDim = dim3(kMmaThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    (void)cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaGetLastError();
+}
+
+template <bool AMN, bool BMN, Epilogue EPI, bool LIST>
+cudaError_t launch_cut(const MmaArgs &p, cudaStream_t s) {
+    if (p.cut.bn == 256) return launch_mma<1, 256, AMN, BMN, EPI, LIST>(p, s);
+    return launch_mma<1, 64, AMN, BMN, EPI, LIST>(p, s);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A product's tiles.  Splits: where the tiles are fewer than half the SMs, the
+// depth is cut until they are all at work, 4 k tiles (256 values) at least to a
+// split.
+Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split) {
+    Cut c{};
+    c.cg = 1;
+    c.bn = m <= 128 || n <= 128 ? 64 : 256;
+    c.m_tiles = (int32_t)ceil_div(m, 128 * c.cg);
+    c.n_tiles = (int32_t)ceil_div(n, c.bn);
+    c.k_tiles = (int32_t)ceil_div(k, kBK);
+    int64_t splits = 1;
+    const int64_t tiles = (int64_t)c.m_tiles * c.n_tiles, room = kHeadSMs / c.cg;
+    if (may_split && tiles * 2 <= room)
+        splits = std::max<int64_t>(1, std::min<int64_t>(room / tiles, c.k_tiles / 4));
+    c.k_chunk = (int32_t)ceil_div(c.k_tiles, splits);
+    c.splits = (int32_t)ceil_div(c.k_tiles, c.k_chunk);
+    return c;
+}
+
+constexpr int64_t kPieceBytes = 256ll << 20;  // of dz
+
+// Where each column tile's list entries begin, up to the end of the last piece,
+// whose width is rounded up to 256.
+int64_t first_pitch(const HeadPlan &p) {
+    return ceil_div(p.vocab, 256) * (256 / p.logits.bn) + 1;
+}
+
+int join_tokens(int64_t tokens) { return tokens <= 1024 ? 1 : 32; }
+
+RowArgs row_args(const HeadArgs &a) {
+    const HeadPlan &p = a.plan;
+    RowArgs r{};
+    r.tokens = p.tokens;
+    r.vocab = p.vocab;
+    r.dim = p.dim;
+    r.k = a.teacher ? (int32_t)p.k : 0;
+    r.n_tiles = p.n_tiles;
+    r.index_bytes = a.index_bytes;
+    r.teacher_bytes = a.teacher_bytes;
+    r.index = a.index;
+    r.teacher = a.teacher;
+    r.weights = a.weights;
+    r.temperature = a.temperature;
+    r.state = reinterpret_cast<int8_t *>(a.ws + p.state);
+    r.list = reinterpret_cast<int32_t *>(a.ws + p.index);
+    r.q = reinterpret_cast<float *>(a.ws + p.q);
+    r.first = reinterpret_cast<uint16_t *>(a.ws + p.first);
+    r.first_pitch = (int32_t)first_pitch(p);
+    r.tile = p.logits.bn;
+    return r;
+}
+
+cudaError_t launch_lists(const RowArgs &r, cudaStream_t s) {
+    int pow2 = 2;
+    while (pow2 < r.k) pow2 *= 2;
+    k_head_lists<<<(unsigned)r.tokens, kListSort, pow2 * sizeof(uint64_t), s>>>(r, pow2);
+    return cudaGetLastError();
+}
+
+void fill_lists(MmaArgs *m, const RowArgs &r) {
+    m->k = r.k;
+    m->index = r.list;
+    m->q = r.q;
+    m->first = r.first;
+    m->first_pitch = r.first_pitch;
+}
+
+}  // namespace
+
+bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads, HeadPlan *p) {
+    *p = HeadPlan{};
+    p->tokens = tokens;
+    p->vocab = vocab;
+    p->dim = dim;
+    p->k = k;
+    // tiles and rows are counted in 32 bits, bytes in 64
+    constexpr int64_t kMost = (1ll << 31) - 1024;
+    if (tokens > kMost || vocab > kMost || dim > kMost) return false;
+    int64_t probe;
+    if (__builtin_mul_overflow(tokens, vocab, &probe) ||
+        __builtin_mul_overflow(std::max(tokens, vocab), dim, &probe) || probe > (1ll << 56) ||
+        ceil_div(std::max(tokens, dim), 64) * ceil_div(std::max(vocab, tokens), 64) > kMost)
+        return false;
+    p->logits = cut_product(tokens, vocab, dim, false);
+    p->n_tiles = p->logits.n_tiles;
+    int64_t at = 0;
+    bool fits = true;
+    auto take = [&](int64_t n, int64_t size) {
+        const int64_t here = at;
+        int64_t bytes;
+        if (__builtin_mul_overflow(n, size, &bytes) || bytes > (1ll << 60) - at)
+            fits = false;
+        else
+            at += ceil_div(bytes, 256) * 256;
+        return here;
+    };
+    p->part = take((int64_t)p->n_tiles * tokens, 8);
+    p->z = take(tokens * std::max<int64_t>(k, 1), 4);
+    p->sums = take(ceil_div(tokens, join_tokens(tokens)), 16);
+    p->done = take(1, 4);
+    p->state = take(k ? tokens : 0, 1);
+    p->index = take(tokens * k, 4);
+    p->q = take(tokens * k, 4);
+    p->first = take(k ? tokens * first_pitch(*p) : 0, 2);
+    if (grads && tokens > 0) {
+        const int64_t most = std::max<int64_t>(1, kPieceBytes / 512 / tokens) * 256;
+        p->pieces = ceil_div(vocab, most);
+        p->piece = ceil_div(ceil_div(vocab, p->pieces), 256) * 256;
+        p->pieces = ceil_div(vocab, p->piece);
+        p->rows = take(tokens, 8);
+        p->words = take(tokens, 4);
+        p->hidden = take(tokens * dim, 2);
+        p->dz = take(tokens * p->piece, 2);
+        const Cut h = cut_product(tokens, dim, p->piece, true);
+        const Cut w = cut_product(p->piece, dim, tokens, true);
+        p->slab_h = take(h.splits > 1 || p->pieces > 1 ? h.splits * tokens * dim : 0, 4);
+        p->slab_w = take(w.splits > 1 ? w.splits * p->piece * dim : 0, 4);
+    }
+    p->bytes = std::max<int64_t>(at, 256);
+    return fits;
+}
+
+cudaError_t launch_head_forward(const HeadArgs &a, cudaStream_t s) {
+    const HeadPlan &p = a.plan;
+    if (p.tokens == 0) return cudaMemsetAsync(a.total, 0, 8, s);
+    const RowArgs r = row_args(a);
+    cudaError_t e = cudaMemsetAsync(a.ws + p.done, 0, 4, s);
+    if (e != cudaSuccess) return e;
+    if (r.k > 0 && (e = launch_lists(r, s)) != cudaSuccess) return e;
+    MmaArgs m{};
+    m.cut = p.logits;
+    if (!make_map(&m.a, a.hidden, p.dim, p.tokens, a.hidden_stride, 128) ||
+        !make_map(&m.b, a.weight, p.dim, p.vocab, a.weight_stride, m.cut.bn / m.cut.cg))
+        return cudaErrorInvalidValue;
+    m.rows = p.tokens;
+    m.cols = p.vocab;
+    m.beta = kLog2e / a.temperature;
+    m.part = reinterpret_cast<float2 *>(a.ws + p.part);
+    m.z = reinterpret_cast<float *>(a.ws + p.z);
+    m.targets = a.index;
+    m.target_bytes = a.index_bytes;
+    fill_lists(&m, r);
+    e = r.k > 0 ? launch_cut<false, false, kStats, true>(m, s)
+                : launch_cut<false, false, kStats, false>(m, s);
+    if (e != cudaSuccess) return e;
+    JoinArgs j{};
+    j.row = r;
+    j.part = m.part;
+    j.z = m.z;
+    j.sums = reinterpret_cast<double2 *>(a.ws + p.sums);
+    j.done = reinterpret_cast<unsigned *>(a.ws + p.done);
+    j.loss = a.loss;
+    j.lse = a.lse;
+    j.total = a.total;
+    if (join_tokens(p.tokens) == 1)
+        k_head_join<1><<<(unsigned)p.tokens, kJoinThreads, 0, s>>>(j);
+    else
+        k_head_join<32><<<(unsigned)ceil_div(p.tokens, 32), kJoinThreads, 0, s>>>(j);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
+    const HeadPlan &p = a.plan;
+    if (p.tokens == 0) {
+        if (a.d_weight == nullptr) return cudaSuccess;
+        return cudaMemset2DAsync(a.d_weight, (size_t)a.d_weight_stride * 2, 0, (size_t)p.dim * 2,
+                                 (size_t)p.vocab, s);
+    }
+    const RowArgs r = row_args(a);
+    cudaError_t e;
+    if (r.k > 0 && (e = launch_lists(r, s)) != cudaSuccess) return e;
+    uint16_t *hidden = reinterpret_cast<uint16_t *>(a.ws + p.hidden);
+    FactorArgs f{};
+    f.row = r;
+    f.lse = a.lse;
+    f.total = a.total;
+    f.scale = a.scale;
+    f.factor = reinterpret_cast<float2 *>(a.ws + p.rows);
+    f.words = reinterpret_cast<int32_t *>(a.ws + p.words);
+    f.hidden = a.hidden;
+    f.stride = a.hidden_stride;
+    f.copy = a.d_weight ? hidden : nullptr;
+    k_head_factors<<<(unsigned)p.tokens, 128, 0, s>>>(f);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+    uint16_t *dz = reinterpret_cast<uint16_t *>(a.ws + p.dz);
+    for (int64_t i = 0; i < p.pieces; ++i) {
+        const int64_t w0 = i * p.piece, words = std::min(p.piece, p.vocab - w0);
+        const int64_t width = ceil_div(words, 256) * 256;  // columns of dz written
+        MmaArgs m{};
+        m.cut = cut_product(p.tokens, p.vocab, p.dim, false);  // the forward's tiles
+        m.cut.n_tiles = (int32_t)(width / m.cut.bn);
+        if (!make_map(&m.a, a.hidden, p.dim, p.tokens, a.hidden_stride, 128) ||
+            !make_map(&m.b, a.weight, p.dim, p.vocab, a.weight_stride, m.cut.bn / m.cut.cg))
+            return cudaErrorInvalidValue;
+        m.b_n = (int32_t)w0;
+        m.rows = p.tokens;
+        m.cols = words;
+        m.beta = kLog2e / a.temperature;
+        m.col0 = (int32_t)w0;
+        m.row = f.factor;
+        m.words = f.words;
+        m.dz = dz;
+        m.dz_pitch = p.piece;
+        fill_lists(&m, r);
+        e = r.k > 0 ? launch_cut<false, false, kDz, true>(m, s)
+                    : launch_cut<false, false, kDz, false>(m, s);
+        if (e != cudaSuccess) return e;
+
+        if (a.d_hidden) {
+            MmaArgs h{};
+            h.cut = cut_product(p.tokens, p.dim, p.piece, true);
+            h.cut.k_tiles = (int32_t)ceil_div(words, kBK);
+            h.cut.splits = (int32_t)ceil_div(h.cut.k_tiles, h.cut.k_chunk);
+            if (!make_map(&h.a, dz, width, p.tokens, p.piece, 128) ||
+                !make_map(&h.b, a.weight, p.dim, p.vocab, a.weight_stride, kBK))
+                return cudaErrorInvalidValue;
+            h.n_fast = 1;
+            h.b_k = (int32_t)w0;
+            h.rows = p.tokens;
+            h.cols = p.dim;
+            h.slab = reinterpret_cast<float *>(a.ws + p.slab_h);
+            h.slab_stride = p.tokens * p.dim;
+            h.add = i > 0;
+            const int splits = cut_product(p.tokens, p.dim, p.piece, true).splits;
+            const bool finish = i + 1 == p.pieces;
+            h.store_slab = splits > 1 || !finish;
+            h.out = a.d_hidden;
+            h.out_pitch = a.d_hidden_stride;
+            if ((e = launch_cut<false, true, kOut, false>(h, s)) != cudaSuccess) return e;
+            if (finish && splits > 1) {
+                const int used = p.pieces > 1 ? splits : h.cut.splits;
+                k_head_slabs<<<(unsigned)ceil_div(p.tokens * p.dim, 2048), 256, 0, s>>>(
+                    h.slab, used, h.slab_stride, p.tokens, p.dim, a.d_hidden, a.d_hidden_stride);
+                if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            }
+        }
+        if (a.d_weight) {
+            MmaArgs g{};
+            g.cut = cut_product(p.piece, p.dim, p.tokens, true);
+            g.cut.m_tiles = (int32_t)ceil_div(words, 128 * g.cut.cg);
+            if (!make_map(&g.a, dz, width, p.tokens, p.piece, kBK) ||
+                !make_map(&g.b, hidden, p.dim, p.tokens, p.dim, kBK))
+                return cudaErrorInvalidValue;
+            g.n_fast = 1;
+            g.rows = words;
+            g.cols = p.dim;
+            g.slab = reinterpret_cast<float *>(a.ws + p.slab_w);
+            g.slab_stride = p.piece * p.dim;
+            g.store_slab = g.cut.splits > 1;
+            g.out = a.d_weight + w0 * a.d_weight_stride;
+            g.out_pitch = a.d_weight_stride;
+            if ((e = launch_cut<true, true, kOut, false>(g, s)) != cudaSuccess) return e;
+            if (g.cut.splits > 1) {
+                k_head_slabs<<<(unsigned)ceil_div(words * p.dim, 2048), 256, 0, s>>>(
+                    g.slab, g.cut.splits, g.slab_stride, words, p.dim, g.out, g.out_pitch);
+                if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            }
+        }
+    }
+    return cudaSuccess;
+}
+
+}  // namespace z3

@@ -34,7 +34,8 @@ EXPORTS = ("z3_layout_create", "z3_layout_destroy", "z3_layout_info", "z3_layout
            "z3_step_layer_noalloc", "z3_tensor_list_create", "z3_tensor_list_destroy",
            "z3_grad_norm_workspace_bytes", "z3_grad_norm", "z3_clip",
            "z3_sumsq_len", "z3_reduce_scatter_norm", "z3_adam_shard_step_clipped",
-           "z3_model_step_clipped", "z3_status_string", "z3_last_error")
+           "z3_model_step_clipped", "z3_head_workspace_bytes", "z3_xent", "z3_xent_grad",
+           "z3_distill", "z3_distill_grad", "z3_status_string", "z3_last_error")
 
 # enum z3_dtype
 Z3_BF16, Z3_F32, Z3_SUMSQ = range(3)
@@ -71,6 +72,21 @@ class ClipUnit(ctypes.Structure):
     """struct z3_clip_unit."""
     _fields_ = [("grad_shards", ctypes.c_void_p), ("sumsq", ctypes.c_void_p),
                 ("accumulate", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Head(ctypes.Structure):
+    """struct z3_head."""
+    _fields_ = [("hidden", ctypes.c_void_p), ("hidden_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("weights", ctypes.c_void_p)]
+
+
+class Teacher(ctypes.Structure):
+    """struct z3_teacher."""
+    _fields_ = [("logits", ctypes.c_void_p), ("index", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("index_bytes", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("temperature", ctypes.c_float)]
 
 
 class Traffic(ctypes.Structure):
@@ -135,6 +151,14 @@ def load():
             "z3_adam_shard_step_clipped": (st, [vp, vp, vp, vp, vp, vp, hp, i64, vp, vp]),
             "z3_model_step_clipped": (st, [ctypes.POINTER(Unit), ctypes.POINTER(ClipUnit), i32,
                                            ctypes.POINTER(vp), i32, hp, i64, f32, vp, vp, vp, vp]),
+            "z3_head_workspace_bytes": (st, [i64, i64, i64, i32, i32, ctypes.POINTER(i64)]),
+            "z3_xent": (st, [ctypes.POINTER(Head), vp, i32, vp, vp, vp, vp, i64, vp]),
+            "z3_xent_grad": (st, [ctypes.POINTER(Head), vp, i32, vp, vp, f32, vp, i64, vp, i64, vp,
+                                  i64, vp]),
+            "z3_distill": (st, [ctypes.POINTER(Head), ctypes.POINTER(Teacher), vp, vp, vp, vp, i64,
+                                vp]),
+            "z3_distill_grad": (st, [ctypes.POINTER(Head), ctypes.POINTER(Teacher), vp, vp, f32, vp,
+                                     i64, vp, i64, vp, i64, vp]),
             "z3_status_string": (ctypes.c_char_p, [st]),
             "z3_last_error": (ctypes.c_size_t, [ctypes.c_char_p, ctypes.c_size_t]),
         }
@@ -546,6 +570,129 @@ def z3_model_step_clipped(units, clips, full, hp, step: int, max_norm: float, cl
         arr, carr, len(units), fulls, len(full), ctypes.byref(h), step, max_norm,
         _dev(clip, f32, 2, "clip"), _workspace(workspace), _stream(stream),
         None if gather_stream is None else _stream(gather_stream)))
+
+
+# ---------------------------------------------------------------------------
+# losses over a vocabulary
+# ---------------------------------------------------------------------------
+
+def head_workspace(tokens: int, dim: int, vocab: int, k: int = 0, grads: bool = True,
+                   device=None):
+    """A workspace for the calls below at these sizes: k the length of the
+    teacher's lists (0: cross entropy), grads for the gradient calls too."""
+    import torch
+    n = ctypes.c_int64()
+    _check(load().z3_head_workspace_bytes(tokens, dim, vocab, k, 1 if grads else 0,
+                                          ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device="cuda" if device is None else device)
+
+
+def _matrix(t, rows, cols, name: str):
+    """Address and row stride of a bf16 [rows][cols] CUDA tensor whose rows
+    may lie apart."""
+    if t is None:
+        return None, 0
+    b16, _ = _dtypes()
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: needs shape [{rows}, {cols}], has {list(t.shape)}")
+    apart = t.stride(0) if rows > 1 else cols
+    if cols > 1 and t.stride(1) != 1 or apart < cols:
+        raise ValueError(f"{name}: strides {t.stride()}: rows must be contiguous and apart")
+    _dev(t[:0], b16, 0, name)                       # device and type
+    return t.data_ptr(), apart
+
+
+def _vector(t, dtypes, shape, name: str):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: needs shape {list(shape)}, has {list(t.shape)}")
+    return _dev(t, dtypes, 0, name)
+
+
+def _head(hidden, weight, weights):
+    """struct z3_head of tensors, and its sizes."""
+    for t, name in ((hidden, "hidden"), (weight, "weight")):
+        if t.dim() != 2:
+            raise ValueError(f"{name}: needs two dimensions, has shape {list(t.shape)}")
+    n, d = hidden.shape
+    v = weight.shape[0]
+    _, f32 = _dtypes()
+    h, hs = _matrix(hidden, n, d, "hidden")
+    w, ws = _matrix(weight, v, d, "weight")
+    return Head(h, hs, w, ws, n, v, d, _vector(weights, f32, (n,), "weights")), n, v, d
+
+
+def _index(t, shape, name: str):
+    torch = _torch()
+    return _vector(t, (torch.int32, torch.int64), shape, name), t.element_size()
+
+
+def _teacher(teacher, index, temperature, n):
+    torch = _torch()
+    if teacher.dim() != 2:
+        raise ValueError(f"teacher: needs two dimensions, has shape {list(teacher.shape)}")
+    k = teacher.shape[1]
+    logits = _vector(teacher, (torch.bfloat16, torch.float32), (n, k), "teacher")
+    idx, size = _index(index, (n, k), "index")
+    return Teacher(logits, idx, Z3_BF16 if teacher.dtype == torch.bfloat16 else Z3_F32, size, k,
+                   temperature)
+
+
+def _space(workspace):
+    return _dev(workspace, (_torch().uint8,), 0, "workspace"), workspace.numel()
+
+
+def _losses(loss, lse, total, n):
+    _, f32 = _dtypes()
+    return (_vector(loss, f32, (n,), "loss"), _vector(lse, f32, (n,), "lse"),
+            _vector(total, f32, (2,), "total"))
+
+
+def _head_grads(lse, total, scale, d_hidden, d_weight, n, v, d):
+    _, f32 = _dtypes()
+    return (_vector(lse, f32, (n,), "lse"), _vector(total, f32, (2,), "total"), scale,
+            *_matrix(d_hidden, n, d, "d_hidden"), *_matrix(d_weight, v, d, "d_weight"))
+
+
+def z3_xent(hidden, weight, targets, loss, lse, total, workspace, weights=None, stream=None):
+    """Softmax cross entropy of hidden [tokens, dim] against the vocabulary of
+    weight [vocab, dim] (bf16; rows may lie apart), without its logits.
+    targets: int32 or int64 [tokens], negative ones left out; weights: fp32
+    [tokens] or None; loss and lse: fp32 [tokens], total: fp32 [2], receive the
+    tokens' losses and {sum of weighted losses, sum of weights}."""
+    h, n, _, _ = _head(hidden, weight, weights)
+    _check(load().z3_xent(ctypes.byref(h), *_index(targets, (n,), "targets"),
+                          *_losses(loss, lse, total, n), *_space(workspace), _stream(stream)))
+
+
+def z3_xent_grad(hidden, weight, targets, lse, total, scale: float, d_hidden, d_weight, workspace,
+                 weights=None, stream=None):
+    """The gradients of scale * total[0] / total[1] (total None: of scale times
+    the sum) into d_hidden and d_weight, either of which may be None; lse and
+    total as z3_xent wrote them."""
+    h, n, v, d = _head(hidden, weight, weights)
+    _check(load().z3_xent_grad(ctypes.byref(h), *_index(targets, (n,), "targets"),
+                               *_head_grads(lse, total, scale, d_hidden, d_weight, n, v, d),
+                               *_space(workspace), _stream(stream)))
+
+
+def z3_distill(hidden, weight, teacher, index, temperature: float, loss, lse, total, workspace,
+               weights=None, stream=None):
+    """Divergence of the head's softmax from that of a teacher's k highest
+    logits, teacher [tokens, k] (bf16 or fp32) at the words index [tokens, k]
+    (int32 or int64; negative ones left out).  The rest as z3_xent."""
+    h, n, _, _ = _head(hidden, weight, weights)
+    t = _teacher(teacher, index, temperature, n)
+    _check(load().z3_distill(ctypes.byref(h), ctypes.byref(t), *_losses(loss, lse, total, n),
+                             *_space(workspace), _stream(stream)))
+
+
+def z3_distill_grad(hidden, weight, teacher, index, temperature: float, lse, total, scale: float,
+                    d_hidden, d_weight, workspace, weights=None, stream=None):
+    h, n, v, d = _head(hidden, weight, weights)
+    t = _teacher(teacher, index, temperature, n)
+    _check(load().z3_distill_grad(ctypes.byref(h), ctypes.byref(t),
+                                  *_head_grads(lse, total, scale, d_hidden, d_weight, n, v, d),
+                                  *_space(workspace), _stream(stream)))
 
 
 def _host(t, dtypes, numel: int, name: str):
