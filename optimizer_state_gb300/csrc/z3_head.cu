@@ -729,7 +729,7 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
 
 template <bool AMN, bool BMN, Epilogue EPI, bool LIST>
 cudaError_t launch_cut(const MmaArgs &p, cudaStream_t s) {
-    if (p.cut.bn == 256) return launch_mma<1, 256, AMN, BMN, EPI, LIST>(p, s);
+    if (p.cut.cg == 2) return launch_mma<2, 256, AMN, BMN, EPI, LIST>(p, s);
     return launch_mma<1, 64, AMN, BMN, EPI, LIST>(p, s);
 }
 
@@ -740,8 +740,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // split.
 Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split) {
     Cut c{};
-    c.cg = 1;
-    c.bn = m <= 128 || n <= 128 ? 64 : 256;
+    const bool small = m <= 128 || n <= 128;
+    c.cg = small ? 1 : 2;
+    c.bn = small ? 64 : 256;
     c.m_tiles = (int32_t)ceil_div(m, 128 * c.cg);
     c.n_tiles = (int32_t)ceil_div(n, c.bn);
     c.k_tiles = (int32_t)ceil_div(k, kBK);
