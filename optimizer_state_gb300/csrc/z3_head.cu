@@ -21,7 +21,8 @@ namespace z3 {
 namespace {
 
 constexpr int kBK = 64;           // values of K in a stage: one swizzled row of 128 bytes
-constexpr int kMmaThreads = 256;  // warps: TMA, products, tensor memory, -, 4 x epilogue
+constexpr int kEpilogueWarps = 8;
+constexpr int kMmaThreads = 128 + 32 * kEpilogueWarps;  // TMA, products, tensor memory, -
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -29,25 +30,37 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the tiled product
 // --------------------------------------------------------------------------
 
-enum Epilogue { kStats, kDz, kOut };
+// What becomes of a result's tiles: each row's maximum and sum of exponentials;
+// the gradient of the logits; the values themselves.
+enum Kind : int32_t { kStats, kDz, kOut };
 
-struct MmaArgs {
-    CUtensorMap a, b;
+// One product D[m][n] = sum_k A(m, k) B(n, k).
+struct Job {
+    CUtensorMap a, b, out;
     Cut cut;
     int32_t n_fast;        // walk a row of tiles before the next row
-    int32_t b_n, b_k;      // where in b's map this call's columns and depth begin
-    int64_t rows, cols;    // valid extent of the result
+    int32_t a_m, a_k;      // where in the maps this product begins
+    int32_t b_n, b_k;
+    int32_t out_f32;       // kOut: binary32 results, by split
+    int32_t add;           // kOut: added to what is there
+    int64_t rows, cols;    // tokens x words, or the rows and columns of kOut's result
+};
+
+struct MmaArgs {
+    Job job;
     // kStats, kDz
     float beta;            // log2(e) / temperature: exponents are powers of two
-    int32_t col0;          // the word of column 0
+    int32_t word0;         // the word of column 0
     int32_t k;             // list length
-    int32_t first_pitch;   // of `first`
-    const int32_t *index;  // lists by ascending word, where each tile's entries begin
+    int32_t grain;         // words between entries of `first`
+    int32_t first_pitch;
+    const int32_t *index;  // lists by ascending word, where each grain's entries begin
     const float *q;
     const uint16_t *first;
     // kStats
     float2 *part;
     float *z;
+    unsigned *done;        // zeroed for the join
     const void *targets;
     int32_t target_bytes;
     // kDz
@@ -55,13 +68,6 @@ struct MmaArgs {
     const int32_t *words;
     uint16_t *dz;
     int64_t dz_pitch;
-    // kOut
-    float *slab;           // null: nothing to add up
-    int64_t slab_stride;
-    int32_t add;           // the slab holds the sums so far
-    int32_t store_slab;
-    uint16_t *out;
-    int64_t out_pitch;
 };
 
 __device__ __forceinline__ int64_t load_index(const void *p, int bytes, int64_t i) {
@@ -77,28 +83,28 @@ template <int BN, int CG>
 __host__ __device__ constexpr int stages() {
     return 196608 / stage_bytes<BN, CG>();
 }
-template <int BN, int CG>
-__host__ __device__ constexpr int smem_bytes() {  // beyond half an SM's: one CTA's tensor memory to an SM
-    return stages<BN, CG>() * stage_bytes<BN, CG>() + 1024 + 512;
-}
+constexpr int kStaging = 4096;  // a warp's: 32 rows of 128 bytes
+constexpr int kSmem = 196608 + kEpilogueWarps * kStaging + 1024 + 512;
+static_assert(kSmem <= 232448 && kSmem > 116736,
+              "fits an SM, and no second CTA beside it competes for its tensor memory");
 
 struct Tile {
     int m, n, split;
 };
 
-__device__ __forceinline__ Tile tile_of(const MmaArgs &p, int item) {
-    const int tiles = p.cut.m_tiles * p.cut.n_tiles;
+__device__ __forceinline__ Tile tile_of(const Job &jb, int item) {
+    const int tiles = jb.cut.m_tiles * jb.cut.n_tiles;
     Tile t;
     t.split = item / tiles;
     int i = item - t.split * tiles;
-    if (p.n_fast) {
-        t.m = i / p.cut.n_tiles;
-        t.n = i - t.m * p.cut.n_tiles;
+    if (jb.n_fast) {
+        t.m = i / jb.cut.n_tiles;
+        t.n = i - t.m * jb.cut.n_tiles;
     } else {
         constexpr int kGroup = 32;  // row tiles whose operand stays in L2
-        const int per = kGroup * p.cut.n_tiles;
+        const int per = kGroup * jb.cut.n_tiles;
         const int g = i / per;
-        const int rows = min(kGroup, p.cut.m_tiles - g * kGroup);
+        const int rows = min(kGroup, jb.cut.m_tiles - g * kGroup);
         i -= g * per;
         t.n = i / rows;
         t.m = g * kGroup + i - t.n * rows;
@@ -114,13 +120,68 @@ __device__ __forceinline__ float pick(const float (&v)[32], uint32_t j) {
     return x;
 }
 
-// D[m][n] = sum_k A(m, k) B(n, k), tile by tile; AMN, BMN: the operand's rows run
-// along M or N rather than K.  One thread feeds TMA, one issues the products
-// of 128 x CG rows by BN columns, four warps take a finished tile out of
-// tensor memory while the next one is computed beside it.
-// Every wait ends (mbar_wait); an epilogue whose tile did not come takes NaN
-// for its values.
-template <int CG, int BN, bool AMN, bool BMN, Epilogue EPI, bool LIST>
+// The entries of a token's list (or its target) among some columns of a
+// tile: the column of the next one, and of the one after it, so that no
+// load is waited for where an entry is met.
+template <bool LIST>
+struct Walk {
+    static constexpr int kNone = 0x7fffffff;
+    int next = kNone, after = kNone;
+    int at = 0, end = 0;
+    const int32_t *index = nullptr;
+    int word0 = 0;
+
+    __device__ __forceinline__ void load_after() {
+        after = LIST && at + 1 < end ? index[at + 1] - word0 : kNone;
+    }
+    __device__ __forceinline__ void advance() {
+        next = after;
+        if constexpr (LIST) {
+            ++at;
+            load_after();
+        }
+    }
+};
+
+// A warp's box of 32 rows of 128 bytes goes out, where it meets the result at all.
+__device__ __forceinline__ void store_box(const Job &jb, uint32_t stage, int lane, int col,
+                                          int64_t row, int split) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0 && row < jb.rows && col < jb.cols)
+        tma_store(&jb.out, stage, col, (int)row, split, jb.add != 0);
+}
+
+// The staging rows may be written again.
+__device__ __forceinline__ void await_box(int lane) {
+    if (lane == 0) tma_wait_read();
+    __syncwarp();
+}
+
+// 32 columns of this thread's row as bf16, `i` columns into the warp's: every
+// second time the 64 go out.
+__device__ __forceinline__ void store_bf16(const Job &jb, uint32_t stage, int lane, int i,
+                                           const uint32_t (&w)[16], int col0, int64_t row) {
+    const int first = i / 32 % 2 * 4;  // 16-byte chunk of the row
+    if (first == 0) await_box(lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        st_shared(stage + lane * 128 + (((first + j) ^ (lane & 7)) << 4), w[4 * j], w[4 * j + 1],
+                  w[4 * j + 2], w[4 * j + 3]);
+    if (first == 4) store_box(jb, stage, lane, col0 + i - 32, row, 0);
+}
+
+// D tile by tile: 128 x CG rows by BN columns.  One thread feeds TMA, one issues
+// the products, eight warps take a finished tile out of tensor memory (a
+// quarter of a CTA's rows, half of the columns each) while the next one is
+// computed beside it.
+// SWAP, for few tokens: M runs along words (or, for d_hidden, along its columns)
+// and N along tokens, so that the weight fills the tiles; a warp turns its 32
+// x 32 values over in shared memory, after which thread, row and columns mean
+// what they mean without SWAP.
+// Every wait ends (mbar_wait); an epilogue whose tile did not come takes NaN for
+// its values.
+template <int CG, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 k_head_mma(const __grid_constant__ MmaArgs p) {
     constexpr int S = stages<BN, CG>();
@@ -130,7 +191,8 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     constexpr int kCols = 2 * BN;    // of tensor memory: two tiles
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
-    const uint32_t bars = base + S * kStage;
+    const uint32_t staging = base + S * kStage;
+    const uint32_t bars = staging + kEpilogueWarps * kStaging;
     auto full = [&](int i) { return bars + 8 * i; };
     auto empty = [&](int i) { return bars + 8 * (S + i); };
     auto tfull = [&](int i) { return bars + 8 * (2 * S + i); };
@@ -139,20 +201,22 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = CG == 1 ? 0 : cluster_rank();
     const int group = blockIdx.x / CG, groups = gridDim.x / CG;
-    const int items = p.cut.m_tiles * p.cut.n_tiles * p.cut.splits;
+    const Job &jb = p.job;
+    const int items = jb.cut.m_tiles * jb.cut.n_tiles * jb.cut.splits;
 
     if (warp == 0 && lane == 0) {
-        tma_prefetch_map(&p.a);
-        tma_prefetch_map(&p.b);
+        tma_prefetch_map(&jb.a);
+        tma_prefetch_map(&jb.b);
         for (int i = 0; i < S; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull(i), 1);
-            mbar_init(tempty(i), 4 * CG);
+            mbar_init(tempty(i), kEpilogueWarps * CG);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (KIND == kStats && blockIdx.x == 0) *p.done = 0;
     }
     if (warp == 2) tmem_alloc<CG>(tmem_at, kCols);
     __syncwarp();
@@ -167,30 +231,33 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
+        // SWAP: a tile may have fewer than 128 rows; the others are not loaded, and
+        // what their sums are is not looked at
+        const uint32_t bytes = CG * (uint32_t)(kStage - (128 - jb.cut.tile_m) * 128);
         for (int item = group; ok && item < items; item += groups) {
-            const Tile t = tile_of(p, item);
-            const int m0 = t.m * (128 * CG) + (int)rank * 128;
-            const int n0 = p.b_n + t.n * BN + (int)rank * kBRows;
-            const int k0 = t.split * p.cut.k_chunk;
-            const int k1 = min(p.cut.k_tiles, k0 + p.cut.k_chunk);
+            const Tile t = tile_of(jb, item);
+            const int m0 = jb.a_m + t.m * (jb.cut.tile_m * CG) + (int)rank * 128;
+            const int n0 = jb.b_n + t.n * BN + (int)rank * kBRows;
+            const int k0 = t.split * jb.cut.k_chunk;
+            const int k1 = min(jb.cut.k_tiles, k0 + jb.cut.k_chunk);
             for (int kt = k0; kt < k1; ++kt) {
                 ok = mbar_wait(empty(stage), phase ^ 1);
                 if (!ok) break;
                 const uint32_t a = base + stage * kStage, b = a + kA;
-                if (rank == 0) mbar_expect(full(stage), CG * kStage);
+                if (rank == 0) mbar_expect(full(stage), bytes);
                 const uint32_t bar = CG == 1 ? full(stage) : in_leader(full(stage));
-                const int ka = kt * kBK, kb = p.b_k + kt * kBK;
+                const int ka = jb.a_k + kt * kBK, kb = jb.b_k + kt * kBK;
                 if constexpr (AMN) {
                     for (int i = 0; i < 2; ++i)
-                        tma_load<CG>(a + i * (64 * kBK * 2), &p.a, bar, m0 + 64 * i, ka);
+                        tma_load<CG>(a + i * (64 * kBK * 2), &jb.a, bar, m0 + 64 * i, ka);
                 } else {
-                    tma_load<CG>(a, &p.a, bar, ka, m0);
+                    tma_load<CG>(a, &jb.a, bar, ka, m0);
                 }
                 if constexpr (BMN) {
                     for (int i = 0; i < kBRows / 64; ++i)
-                        tma_load<CG>(b + i * (64 * kBK * 2), &p.b, bar, n0 + 64 * i, kb);
+                        tma_load<CG>(b + i * (64 * kBK * 2), &jb.b, bar, n0 + 64 * i, kb);
                 } else {
-                    tma_load<CG>(b, &p.b, bar, kb, n0);
+                    tma_load<CG>(b, &jb.b, bar, kb, n0);
                 }
                 if (++stage == S) {
                     stage = 0;
@@ -215,9 +282,9 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         uint32_t phase = 0;
         bool ok = true;
         for (int item = group; ok && item < items; item += groups, ++done) {
-            const Tile t = tile_of(p, item);
-            const int k0 = t.split * p.cut.k_chunk;
-            const int k1 = min(p.cut.k_tiles, k0 + p.cut.k_chunk);
+            const Tile t = tile_of(jb, item);
+            const int k0 = t.split * jb.cut.k_chunk;
+            const int k1 = min(jb.cut.k_tiles, k0 + jb.cut.k_chunk);
             const int buf = done & 1;
             const uint32_t d = tmem + buf * BN;
             ok = mbar_wait(tempty(buf), ((done >> 1) & 1) ^ 1);
@@ -241,138 +308,167 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             if (ok) mma_commit<CG>(tfull(buf));
         }
     } else if (warp >= 4) {
-        const int quad = warp - 4;  // its 32 lanes of tensor memory
+        const int quad = warp % 4;  // its 32 lanes of tensor memory
+        const int half = (warp - 4) / 4;
+        constexpr int kPer = BN / 2 < 32 ? 32 : BN / 2;  // columns of a warp
+        const int c0 = half * kPer;
+        const uint32_t stage = staging + (warp - 4) * kStaging;
         int done = 0;
         bool ok = true;
         for (int item = group; item < items; item += groups, ++done) {
-            const Tile t = tile_of(p, item);
-            const int64_t row = (int64_t)t.m * (128 * CG) + rank * 128 + quad * 32 + lane;
-            const bool live = row < p.rows;
-            const int n0 = t.n * BN;
-            const int cols = (int)min((int64_t)BN, p.cols - n0);  // valid ones of this tile
-            // what the row asks of this tile's words
-            [[maybe_unused]] int next = 0x7fffffff;   // column of the next one asked for
-            [[maybe_unused]] int at = 0, end = 0;     // list entries of this tile
-            [[maybe_unused]] float2 rw = make_float2(0.0f, 0.0f);
-            if constexpr (EPI != kOut) {
-                if (live) {
-                    if constexpr (LIST) {
-                        const int w0 = (p.col0 + n0) / BN;
-                        const uint16_t *f = p.first + row * p.first_pitch + w0;
-                        at = f[0];
-                        end = f[1];
-                        if (at < end) next = p.index[row * p.k + at] - p.col0 - n0;
-                    } else {
-                        const int64_t w = EPI == kStats
-                                              ? load_index(p.targets, p.target_bytes, row)
-                                              : (int64_t)p.words[row];
-                        const int64_t c = w - p.col0 - n0;
-                        if (w >= 0 && c >= 0 && c < cols) next = (int)c;
-                    }
-                    if constexpr (EPI == kDz) rw = p.row[row];
-                }
-            }
-            [[maybe_unused]] auto advance = [&] {
-                next = 0x7fffffff;
-                if constexpr (LIST)
-                    if (++at < end) next = p.index[row * p.k + at] - p.col0 - n0;
-            };
+            const Tile t = tile_of(jb, item);
             const int buf = done & 1;
+            // this warp's first row and column; with SWAP its columns are those of the
+            // quarter, and its rows go on with each 32
+            const int64_t row0 = SWAP ? (int64_t)t.n * BN + c0
+                                      : (int64_t)t.m * (128 * CG) + rank * 128 + quad * 32;
+            const int col0 = SWAP ? t.m * jb.cut.tile_m + quad * 32 : t.n * BN + c0;
+            const int cols =  // valid ones among them
+                (int)min((int64_t)(SWAP ? min(32, jb.cut.tile_m - quad * 32) : kPer),
+                         jb.cols - col0);
+            int64_t row = row0 + lane;
+            bool live = row < jb.rows;
+            [[maybe_unused]] Walk<LIST> walk;
+            [[maybe_unused]] float2 rw = make_float2(0.0f, 0.0f);
+            // what the row asks of these words
+            [[maybe_unused]] auto begin_row = [&] {
+                walk = Walk<LIST>{};
+                rw = make_float2(0.0f, 0.0f);
+                if (!live || cols <= 0) return;
+                if constexpr (LIST) {
+                    const uint16_t *f =
+                        p.first + row * p.first_pitch + (p.word0 + col0) / p.grain;
+                    walk.index = p.index + row * p.k;
+                    walk.word0 = p.word0 + col0;
+                    walk.at = f[0];
+                    walk.end = f[((SWAP ? cols : kPer) + p.grain - 1) / p.grain];
+                    if (walk.at < walk.end) walk.next = walk.index[walk.at] - walk.word0;
+                    walk.load_after();
+                } else {
+                    const int64_t w = KIND == kStats ? load_index(p.targets, p.target_bytes, row)
+                                                     : (int64_t)p.words[row];
+                    const int64_t c = w - p.word0 - col0;
+                    if (w >= 0 && c >= 0 && c < cols) walk.next = (int)c;
+                }
+                if constexpr (KIND == kDz) rw = p.row[row];
+            };
+            if constexpr (KIND != kOut && !SWAP) begin_row();
             if (ok) ok = mbar_wait(tfull(buf), (done >> 1) & 1);
             tmem_fence_after();
-            const uint32_t d = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN;
+            const uint32_t d = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + c0;
             [[maybe_unused]] float top = -INFINITY, sum = 0.0f;
+            auto release = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_leader(tempty(buf)));
+            };
+            if (c0 >= BN) release();
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
+            for (int i = 0; i < kPer && c0 + i < BN; i += 32) {
                 uint32_t bits[32];
-                tmem_load32(d + c, bits);
+                tmem_load32(d + i, bits);
                 tmem_wait_load();
-                if (c + 32 == BN) {
-                    tmem_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_leader(tempty(buf)));
-                }
+                if (i + 32 == kPer) release();
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = ok ? __uint_as_float(bits[j]) : NAN;
-                if constexpr (EPI == kStats) {
-                    while (next < c + 32) {
-                        const float x = pick(v, (uint32_t)(next - c));
-                        p.z[LIST ? row * p.k + at : row] = x;
-                        advance();
-                    }
-                    // powers of two: exp(z / temperature) = 2^(beta z)
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        v[j] = c + j < cols ? __fmul_rn(v[j], p.beta) : -INFINITY;
-                        m = fmaxf(m, v[j]);
-                    }
-                    const float new_top = fmaxf(top, m);
-                    const float shift = new_top == -INFINITY ? 0.0f : new_top;
-                    float s = 0.0f;
+                if constexpr (SWAP) {
+                    // [token][word], each row turned by its number: no two lanes meet
+                    // in a bank
+                    await_box(lane);
+                    auto at = [&](int r, int c) { return stage + (r * 32 + ((c + r) & 31)) * 4; };
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        s = __fadd_rn(s, exp2_fast(__fsub_rn(v[j], shift)));
-                    sum = __fmaf_rn(sum, exp2_fast(__fsub_rn(top, shift)), s);
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(j, lane)), "f"(v[j])
+                                     : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(at(lane, j))
+                                     : "memory");
+                    __syncwarp();
+                    row = row0 + i + lane;
+                    live = row < jb.rows;
+                    if constexpr (KIND != kOut) begin_row();
+                    top = -INFINITY;
+                    sum = 0.0f;
+                }
+                const int c = SWAP ? 0 : i;  // column of v[0] from col0 on
+                if constexpr (KIND == kStats) {
+                    while (walk.next < c + 32) {
+                        p.z[LIST ? row * p.k + walk.at : row] = pick(v, (uint32_t)(walk.next - c));
+                        walk.advance();
+                    }
+                    if (c + 32 > cols) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : -INFINITY;
+                    }
+                    // four chains of each; exp(z / temperature) = 2^(beta z)
+                    float m[4], s[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m[j] = v[j];
+#pragma unroll
+                    for (int j = 4; j < 32; ++j) m[j % 4] = fmaxf(m[j % 4], v[j]);
+                    const float new_top =
+                        fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * p.beta);
+                    const float shift = new_top == -INFINITY ? 0.0f : -new_top;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] = exp2_fast(__fmaf_rn(v[j], p.beta, shift));
+#pragma unroll
+                    for (int j = 4; j < 32; ++j)
+                        s[j % 4] += exp2_fast(__fmaf_rn(v[j], p.beta, shift));
+                    sum = __fmaf_rn(sum, exp2_fast(top + shift), (s[0] + s[1]) + (s[2] + s[3]));
                     top = new_top;
-                } else if constexpr (EPI == kDz) {
+                    if constexpr (SWAP)
+                        if (live) p.part[(t.m * 4 + quad) * jb.rows + row] = make_float2(top, sum);
+                } else if constexpr (KIND == kDz) {
                     const bool none = rw.x == 0.0f;  // also where the logits are not finite
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float e = exp2_fast(__fmaf_rn(v[j], p.beta, -rw.y));
-                        v[j] = none || c + j >= cols ? 0.0f : __fmul_rn(e, rw.x);
-                    }
-                    while (next < c + 32) {
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = exp2_fast(__fmaf_rn(v[j], p.beta, -rw.y)) * rw.x;
+                    while (walk.next < c + 32) {
                         float q = rw.x;
-                        if constexpr (LIST) q = __fmul_rn(q, p.q[row * p.k + at]);
-                        const int hit = next - c;
+                        if constexpr (LIST) q = q * p.q[row * p.k + walk.at];
+                        const int hit = walk.next - c;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j == hit) v[j] = __fsub_rn(v[j], q);
-                        advance();
+                            if (j == hit) v[j] -= q;
+                        walk.advance();
                     }
-                    if (live) {
-                        uint16_t *o = p.dz + row * p.dz_pitch + n0 + c;
+                    // rounded once to bf16, the type of the products' operands
+                    uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            // rounded once to bf16, the type of the products' operands
-                            const uint4 w = make_uint4(
-                                pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                                pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
-                            *reinterpret_cast<uint4 *>(o + j) = w;
-                        }
+                    for (int j = 0; j < 16; ++j)
+                        w[j] = none ? 0u : pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    if constexpr (SWAP) {
+                        uint16_t *o = p.dz + row * p.dz_pitch + col0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)  // a pitch of 8s: room beyond the last word
+                            if (live && 8 * j < cols)
+                                *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
+                                    w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    } else {
+                        store_bf16(jb, stage, lane, i, w, col0, row0);
                     }
+                } else if (SWAP || jb.out_f32) {
+                    if constexpr (!SWAP) await_box(lane);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
+                                  __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                  __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+                    store_box(jb, stage, lane, col0 + c, SWAP ? row0 + i : row0, t.split);
                 } else {
-                    if (live) {
+                    uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            if (c + j >= cols) break;  // cols is a multiple of 8
-                            float *f = p.slab + t.split * p.slab_stride + row * p.cols + n0 + c + j;
-                            float4 *f4 = reinterpret_cast<float4 *>(f);
-                            if (p.add) {
-                                const float4 x = f4[0], y = f4[1];
-                                v[j] += x.x; v[j + 1] += x.y; v[j + 2] += x.z; v[j + 3] += x.w;
-                                v[j + 4] += y.x; v[j + 5] += y.y; v[j + 6] += y.z; v[j + 7] += y.w;
-                            }
-                            if (p.store_slab) {
-                                f4[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                                f4[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
-                            } else {
-                                *reinterpret_cast<uint4 *>(p.out + row * p.out_pitch + n0 + c + j) =
-                                    make_uint4(pack_bf16x2(v[j], v[j + 1]),
-                                               pack_bf16x2(v[j + 2], v[j + 3]),
-                                               pack_bf16x2(v[j + 4], v[j + 5]),
-                                               pack_bf16x2(v[j + 6], v[j + 7]));
-                            }
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    store_bf16(jb, stage, lane, i, w, col0, row0);
                 }
             }
-            if constexpr (EPI == kStats)
-                if (live) p.part[t.n * p.rows + row] = make_float2(top, sum);
+            if constexpr (KIND == kStats && !SWAP)
+                if (live) p.part[(t.n * 2 + half) * jb.rows + row] = make_float2(top, sum);
         }
+        if (lane == 0) tma_wait_all();
     }
     __syncwarp();
     tmem_fence_before();
@@ -390,7 +486,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 struct RowArgs {
     int64_t tokens, vocab, dim;
     int32_t k;             // 0: cross entropy
-    int32_t n_tiles;
+    int32_t parts;         // maxima and sums of a token
     int32_t index_bytes, teacher_bytes;
     const void *index;
     const void *teacher;
@@ -401,7 +497,7 @@ struct RowArgs {
     float *q;
     uint16_t *first;
     int32_t first_pitch;
-    int32_t tile;          // words of a column tile
+    int32_t grain;         // words between its entries
 };
 
 __device__ __forceinline__ Row state_of(const RowArgs &a, int64_t t, int64_t *word) {
@@ -413,7 +509,7 @@ __device__ __forceinline__ Row state_of(const RowArgs &a, int64_t t, int64_t *wo
 constexpr int kListSort = 128;  // threads
 
 // A token's list by ascending word, with q = softmax(teacher / temperature), and
-// where each column tile's entries begin.  Entries of a negative word or a
+// where the entries of every `grain` words begin.  Entries of a negative word or a
 // logit of -Inf are left out (at the end, q = 0); a word beyond the vocabulary
 // spoils the row.  One CTA to a token: a bitonic sort of (word, place), so that
 // equal words keep their order.
@@ -491,7 +587,7 @@ __global__ void __launch_bounds__(kListSort) k_head_lists(const RowArgs a, int p
     }
     for (int n = tid; n < a.first_pitch; n += kListSort)
         a.first[t * a.first_pitch + n] =
-            (uint16_t)min(count, begin((uint32_t)min((int64_t)n * a.tile, (int64_t)0x7fffffff)));
+            (uint16_t)min(count, begin((uint32_t)min((int64_t)n * a.grain, (int64_t)0x7fffffff)));
     if (tid == 0) a.state[t] = bad ? kBad : count > 0 ? kCounts : kLeftOut;
 }
 
@@ -504,9 +600,9 @@ struct JoinArgs {
     float *loss, *lse, *total;
 };
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 
-// Joins the column tiles' maxima and sums, TOK tokens to a block, and finishes
+// Joins the tiles' maxima and sums, TOK tokens to a block, and finishes
 // each token's loss; the last block adds up the blocks' sums in their order.
 // Bound by latency: with 8192 tokens it reads 13 MB.  Few tokens take a block
 // each.
@@ -528,9 +624,16 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
     };
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (live) {
-#pragma unroll 4
-        for (int n = slice; n < a.row.n_tiles; n += kSlices)
-            acc = join(acc, a.part[(int64_t)n * a.row.tokens + t]);
+        for (int n = slice; n < a.row.parts; n += 8 * kSlices) {  // eight loads in flight
+            float2 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = n + i * kSlices < a.row.parts
+                           ? a.part[(int64_t)(n + i * kSlices) * a.row.tokens + t]
+                           : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc = join(acc, x[i]);
+        }
     }
     joined[slice][tok] = acc;
     __syncthreads();
@@ -705,17 +808,36 @@ bool make_map(CUtensorMap *m, const void *p, int64_t inner, int64_t outer, int64
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, int BN, bool AMN, bool BMN, Epilogue EPI, bool LIST>
+// A result in boxes of 32 rows of 128 bytes: bf16 [rows][pitch], or binary32
+// [splits][rows][pitch].
+bool make_out(CUtensorMap *m, void *p, bool f32, int64_t cols, int64_t rows, int64_t pitch,
+              int64_t splits) {
+    const EncodeTiled encode = encoder();
+    if (encode == nullptr) return false;
+    const int size = f32 ? 4 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)splits};
+    const cuuint64_t strides[2] = {(cuuint64_t)(pitch * size),
+                                   (cuuint64_t)((splits > 1 ? rows : 1) * pitch * size)};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / size), 32, 1};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p,
+                  dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int CG, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
 cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
-    auto *kernel = k_head_mma<CG, BN, AMN, BMN, EPI, LIST>;
-    constexpr int smem = smem_bytes<BN, CG>();
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto *kernel = k_head_mma<CG, BN, SWAP, AMN, BMN, KIND, LIST>;
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)p.cut.m_tiles * p.cut.n_tiles * p.cut.splits;
+    const Cut &c = p.job.cut;
+    const int64_t items = (int64_t)c.m_tiles * c.n_tiles * c.splits;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, kHeadSMs / CG)));
     cfg.blockDim = dim3(kMmaThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -727,41 +849,94 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <bool AMN, bool BMN, Epilogue EPI, bool LIST>
-cudaError_t launch_cut(const MmaArgs &p, cudaStream_t s) {
-    if (p.cut.cg == 2) return launch_mma<2, 256, AMN, BMN, EPI, LIST>(p, s);
-    return launch_mma<1, 64, AMN, BMN, EPI, LIST>(p, s);
+// tokens x words
+template <Kind KIND, bool LIST>
+cudaError_t launch_logits(const MmaArgs &p, cudaStream_t s) {
+    const Cut &c = p.job.cut;
+    if (!c.swap) return launch_mma<2, 256, false, false, false, KIND, LIST>(p, s);
+    if (c.bn == 32) return launch_mma<1, 32, true, false, false, KIND, LIST>(p, s);
+    return launch_mma<1, 128, true, false, false, KIND, LIST>(p, s);
+}
+
+cudaError_t launch_d_hidden(const MmaArgs &p, cudaStream_t s) {
+    const Cut &c = p.job.cut;
+    if (c.swap)
+        return c.bn == 32 ? launch_mma<1, 32, true, true, false, kOut, false>(p, s)
+                          : launch_mma<1, 128, true, true, false, kOut, false>(p, s);
+    return c.bn == 256 ? launch_mma<2, 256, false, false, true, kOut, false>(p, s)
+                       : launch_mma<2, 128, false, false, true, kOut, false>(p, s);
+}
+
+cudaError_t launch_d_weight(const MmaArgs &p, cudaStream_t s) {
+    return p.job.cut.bn == 256 ? launch_mma<2, 256, false, true, true, kOut, false>(p, s)
+                               : launch_mma<2, 128, false, true, true, kOut, false>(p, s);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A product's tiles.  Splits: where the tiles are fewer than half the SMs, the
-// depth is cut until they are all at work, 4 k tiles (256 values) at least to a
-// split.
-Cut cut_product(int64_t m, int64_t n, int64_t k, bool may_split) {
+constexpr int64_t kFew = 128;  // tokens that SWAP takes
+
+// The logits' tiles.  Few tokens: the weight's rows are cut so that every SM has
+// the same number of tiles, none more than 128 rows.
+Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
     Cut c{};
-    const bool small = m <= 128 || n <= 128;
-    c.cg = small ? 1 : 2;
-    c.bn = small ? 64 : 256;
+    c.k_tiles = c.k_chunk = (int32_t)ceil_div(dim, kBK);
+    c.splits = 1;
+    c.swap = tokens <= kFew;
+    if (c.swap) {
+        c.cg = 1;
+        c.bn = tokens <= 32 ? 32 : 128;
+        const int64_t waves = ceil_div(words, kHeadSMs * 128);
+        c.tile_m = (int32_t)(ceil_div(ceil_div(words, kHeadSMs * waves), 8) * 8);
+        c.m_tiles = (int32_t)ceil_div(words, c.tile_m);
+        c.n_tiles = 1;
+    } else {
+        c.cg = 2;
+        c.bn = 256;
+        c.tile_m = 128;
+        c.m_tiles = (int32_t)ceil_div(tokens, 256);
+        c.n_tiles = (int32_t)ceil_div(words, 256);
+    }
+    return c;
+}
+
+// The tiles of a product of dz: [m][n] of depth k.  Where they are fewer than
+// half of what the GPU holds at a time, the depth is cut until it is full, 4 k
+// tiles (256 values) at least to a split.
+Cut cut_out(int64_t m, int64_t n, int64_t k, bool swap, int64_t tokens) {
+    Cut c{};
+    c.swap = swap;
+    c.cg = swap ? 1 : 2;
+    c.bn = swap ? (tokens <= 32 ? 32 : 128) : n <= 128 ? 128 : 256;
+    c.tile_m = 128;
     c.m_tiles = (int32_t)ceil_div(m, 128 * c.cg);
     c.n_tiles = (int32_t)ceil_div(n, c.bn);
     c.k_tiles = (int32_t)ceil_div(k, kBK);
     int64_t splits = 1;
     const int64_t tiles = (int64_t)c.m_tiles * c.n_tiles, room = kHeadSMs / c.cg;
-    if (may_split && tiles * 2 <= room)
+    if (tiles * 2 <= room)
         splits = std::max<int64_t>(1, std::min<int64_t>(room / tiles, c.k_tiles / 4));
     c.k_chunk = (int32_t)ceil_div(c.k_tiles, splits);
     c.splits = (int32_t)ceil_div(c.k_tiles, c.k_chunk);
     return c;
 }
 
+Cut cut_d_hidden(int64_t tokens, int64_t dim, int64_t words) {
+    return tokens <= kFew ? cut_out(dim, tokens, words, true, tokens)
+                          : cut_out(tokens, dim, words, false, tokens);
+}
+
+Cut cut_d_weight(int64_t tokens, int64_t dim, int64_t words) {
+    return cut_out(words, dim, tokens, false, tokens);
+}
+
 constexpr int64_t kPieceBytes = 256ll << 20;  // of dz
 
-// Where each column tile's list entries begin, up to the end of the last piece,
-// whose width is rounded up to 256.
-int64_t first_pitch(const HeadPlan &p) {
-    return ceil_div(p.vocab, 256) * (256 / p.logits.bn) + 1;
-}
+// Words between the entries of `first`: what a warp of the logits' epilogue takes,
+// or what a quarter of a SWAP tile begins on.
+int grain(const HeadPlan &p) { return p.logits.swap ? 8 : 128; }
+// ... which goes up to the end of the last tile of the last piece.
+int64_t first_pitch(const HeadPlan &p) { return ceil_div(p.vocab, 256) * (256 / grain(p)) + 1; }
 
 int join_tokens(int64_t tokens) { return tokens <= 1024 ? 1 : 32; }
 
@@ -772,7 +947,7 @@ RowArgs row_args(const HeadArgs &a) {
     r.vocab = p.vocab;
     r.dim = p.dim;
     r.k = a.teacher ? (int32_t)p.k : 0;
-    r.n_tiles = p.n_tiles;
+    r.parts = p.parts;
     r.index_bytes = a.index_bytes;
     r.teacher_bytes = a.teacher_bytes;
     r.index = a.index;
@@ -784,7 +959,7 @@ RowArgs row_args(const HeadArgs &a) {
     r.q = reinterpret_cast<float *>(a.ws + p.q);
     r.first = reinterpret_cast<uint16_t *>(a.ws + p.first);
     r.first_pitch = (int32_t)first_pitch(p);
-    r.tile = p.logits.bn;
+    r.grain = grain(p);
     return r;
 }
 
@@ -801,6 +976,22 @@ void fill_lists(MmaArgs *m, const RowArgs &r) {
     m->q = r.q;
     m->first = r.first;
     m->first_pitch = r.first_pitch;
+    m->grain = r.grain;
+}
+
+// The product of the hidden states with the words from w0 on.
+bool logits_job(MmaArgs *m, const HeadArgs &a, const Cut &cut, int64_t w0, int64_t words) {
+    const HeadPlan &p = a.plan;
+    Job &jb = m->job;
+    jb.cut = cut;
+    jb.rows = p.tokens;
+    jb.cols = words;
+    m->word0 = (int32_t)w0;
+    m->beta = kLog2e / a.temperature;
+    CUtensorMap *hidden = cut.swap ? &jb.b : &jb.a, *weight = cut.swap ? &jb.a : &jb.b;
+    (cut.swap ? jb.a_m : jb.b_n) = (int32_t)w0;
+    return make_map(hidden, a.hidden, p.dim, p.tokens, a.hidden_stride, cut.swap ? cut.bn : 128) &&
+           make_map(weight, a.weight, p.dim, p.vocab, a.weight_stride, cut.tile_m);
 }
 
 }  // namespace
@@ -819,8 +1010,8 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
         __builtin_mul_overflow(std::max(tokens, vocab), dim, &probe) || probe > (1ll << 56) ||
         ceil_div(std::max(tokens, dim), 64) * ceil_div(std::max(vocab, tokens), 64) > kMost)
         return false;
-    p->logits = cut_product(tokens, vocab, dim, false);
-    p->n_tiles = p->logits.n_tiles;
+    p->logits = cut_logits(tokens, vocab, dim);
+    p->parts = p->logits.swap ? p->logits.m_tiles * 4 : p->logits.n_tiles * 2;
     int64_t at = 0;
     bool fits = true;
     auto take = [&](int64_t n, int64_t size) {
@@ -832,7 +1023,7 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
             at += ceil_div(bytes, 256) * 256;
         return here;
     };
-    p->part = take((int64_t)p->n_tiles * tokens, 8);
+    p->part = take((int64_t)p->parts * tokens, 8);
     p->z = take(tokens * std::max<int64_t>(k, 1), 4);
     p->sums = take(ceil_div(tokens, join_tokens(tokens)), 16);
     p->done = take(1, 4);
@@ -849,9 +1040,10 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
         p->words = take(tokens, 4);
         p->hidden = take(tokens * dim, 2);
         p->dz = take(tokens * p->piece, 2);
-        const Cut h = cut_product(tokens, dim, p->piece, true);
-        const Cut w = cut_product(p->piece, dim, tokens, true);
-        p->slab_h = take(h.splits > 1 || p->pieces > 1 ? h.splits * tokens * dim : 0, 4);
+        const Cut h = cut_d_hidden(tokens, dim, p->piece);
+        const Cut w = cut_d_weight(tokens, dim, p->piece);
+        p->slab_h =
+            take(h.swap || h.splits > 1 || p->pieces > 1 ? h.splits * tokens * dim : 0, 4);
         p->slab_w = take(w.splits > 1 ? w.splits * p->piece * dim : 0, 4);
     }
     p->bytes = std::max<int64_t>(at, 256);
@@ -862,31 +1054,24 @@ cudaError_t launch_head_forward(const HeadArgs &a, cudaStream_t s) {
     const HeadPlan &p = a.plan;
     if (p.tokens == 0) return cudaMemsetAsync(a.total, 0, 8, s);
     const RowArgs r = row_args(a);
-    cudaError_t e = cudaMemsetAsync(a.ws + p.done, 0, 4, s);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     if (r.k > 0 && (e = launch_lists(r, s)) != cudaSuccess) return e;
     MmaArgs m{};
-    m.cut = p.logits;
-    if (!make_map(&m.a, a.hidden, p.dim, p.tokens, a.hidden_stride, 128) ||
-        !make_map(&m.b, a.weight, p.dim, p.vocab, a.weight_stride, m.cut.bn / m.cut.cg))
-        return cudaErrorInvalidValue;
-    m.rows = p.tokens;
-    m.cols = p.vocab;
-    m.beta = kLog2e / a.temperature;
+    if (!logits_job(&m, a, p.logits, 0, p.vocab)) return cudaErrorInvalidValue;
     m.part = reinterpret_cast<float2 *>(a.ws + p.part);
     m.z = reinterpret_cast<float *>(a.ws + p.z);
+    m.done = reinterpret_cast<unsigned *>(a.ws + p.done);
     m.targets = a.index;
     m.target_bytes = a.index_bytes;
     fill_lists(&m, r);
-    e = r.k > 0 ? launch_cut<false, false, kStats, true>(m, s)
-                : launch_cut<false, false, kStats, false>(m, s);
+    e = r.k > 0 ? launch_logits<kStats, true>(m, s) : launch_logits<kStats, false>(m, s);
     if (e != cudaSuccess) return e;
     JoinArgs j{};
     j.row = r;
     j.part = m.part;
     j.z = m.z;
     j.sums = reinterpret_cast<double2 *>(a.ws + p.sums);
-    j.done = reinterpret_cast<unsigned *>(a.ws + p.done);
+    j.done = m.done;
     j.loss = a.loss;
     j.lse = a.lse;
     j.total = a.total;
@@ -924,74 +1109,80 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
     uint16_t *dz = reinterpret_cast<uint16_t *>(a.ws + p.dz);
     for (int64_t i = 0; i < p.pieces; ++i) {
         const int64_t w0 = i * p.piece, words = std::min(p.piece, p.vocab - w0);
-        const int64_t width = ceil_div(words, 256) * 256;  // columns of dz written
+        const bool last = i + 1 == p.pieces;
         MmaArgs m{};
-        m.cut = cut_product(p.tokens, p.vocab, p.dim, false);  // the forward's tiles
-        m.cut.n_tiles = (int32_t)(width / m.cut.bn);
-        if (!make_map(&m.a, a.hidden, p.dim, p.tokens, a.hidden_stride, 128) ||
-            !make_map(&m.b, a.weight, p.dim, p.vocab, a.weight_stride, m.cut.bn / m.cut.cg))
+        Cut cut = p.logits;
+        if (cut.swap)
+            cut.m_tiles = (int32_t)ceil_div(words, cut.tile_m);
+        else
+            cut.n_tiles = (int32_t)ceil_div(words, cut.bn);
+        if (!logits_job(&m, a, cut, w0, words) ||
+            !make_out(&m.job.out, dz, false, words, p.tokens, p.piece, 1))
             return cudaErrorInvalidValue;
-        m.b_n = (int32_t)w0;
-        m.rows = p.tokens;
-        m.cols = words;
-        m.beta = kLog2e / a.temperature;
-        m.col0 = (int32_t)w0;
         m.row = f.factor;
         m.words = f.words;
         m.dz = dz;
         m.dz_pitch = p.piece;
         fill_lists(&m, r);
-        e = r.k > 0 ? launch_cut<false, false, kDz, true>(m, s)
-                    : launch_cut<false, false, kDz, false>(m, s);
+        e = r.k > 0 ? launch_logits<kDz, true>(m, s) : launch_logits<kDz, false>(m, s);
         if (e != cudaSuccess) return e;
 
         if (a.d_hidden) {
             MmaArgs h{};
-            h.cut = cut_product(p.tokens, p.dim, p.piece, true);
-            h.cut.k_tiles = (int32_t)ceil_div(words, kBK);
-            h.cut.splits = (int32_t)ceil_div(h.cut.k_tiles, h.cut.k_chunk);
-            if (!make_map(&h.a, dz, width, p.tokens, p.piece, 128) ||
-                !make_map(&h.b, a.weight, p.dim, p.vocab, a.weight_stride, kBK))
-                return cudaErrorInvalidValue;
-            h.n_fast = 1;
-            h.b_k = (int32_t)w0;
-            h.rows = p.tokens;
-            h.cols = p.dim;
-            h.slab = reinterpret_cast<float *>(a.ws + p.slab_h);
-            h.slab_stride = p.tokens * p.dim;
-            h.add = i > 0;
-            const int splits = cut_product(p.tokens, p.dim, p.piece, true).splits;
-            const bool finish = i + 1 == p.pieces;
-            h.store_slab = splits > 1 || !finish;
-            h.out = a.d_hidden;
-            h.out_pitch = a.d_hidden_stride;
-            if ((e = launch_cut<false, true, kOut, false>(h, s)) != cudaSuccess) return e;
-            if (finish && splits > 1) {
-                const int used = p.pieces > 1 ? splits : h.cut.splits;
+            Job &jb = h.job;
+            jb.cut = cut_d_hidden(p.tokens, p.dim, p.piece);
+            const int splits = jb.cut.splits;
+            jb.cut.k_tiles = (int32_t)ceil_div(words, kBK);
+            jb.cut.splits = (int32_t)ceil_div(jb.cut.k_tiles, jb.cut.k_chunk);
+            jb.n_fast = 1;
+            jb.rows = p.tokens;
+            jb.cols = p.dim;
+            jb.out_f32 = jb.cut.swap || splits > 1 || p.pieces > 1;
+            jb.add = i > 0;
+            float *slab = reinterpret_cast<float *>(a.ws + p.slab_h);
+            bool ok;
+            if (jb.cut.swap) {
+                jb.a_k = (int32_t)w0;
+                ok = make_map(&jb.a, a.weight, p.dim, p.vocab, a.weight_stride, kBK) &&
+                     make_map(&jb.b, dz, words, p.tokens, p.piece, jb.cut.bn);
+            } else {
+                jb.b_k = (int32_t)w0;
+                ok = make_map(&jb.a, dz, words, p.tokens, p.piece, 128) &&
+                     make_map(&jb.b, a.weight, p.dim, p.vocab, a.weight_stride, kBK);
+            }
+            ok = ok && (jb.out_f32 ? make_out(&jb.out, slab, true, p.dim, p.tokens, p.dim, splits)
+                                   : make_out(&jb.out, a.d_hidden, false, p.dim, p.tokens,
+                                              a.d_hidden_stride, 1));
+            if (!ok) return cudaErrorInvalidValue;
+            if ((e = launch_d_hidden(h, s)) != cudaSuccess) return e;
+            if (last && jb.out_f32) {
                 k_head_slabs<<<(unsigned)ceil_div(p.tokens * p.dim, 2048), 256, 0, s>>>(
-                    h.slab, used, h.slab_stride, p.tokens, p.dim, a.d_hidden, a.d_hidden_stride);
+                    slab, p.pieces > 1 ? splits : jb.cut.splits, p.tokens * p.dim, p.tokens, p.dim,
+                    a.d_hidden, a.d_hidden_stride);
                 if ((e = cudaGetLastError()) != cudaSuccess) return e;
             }
         }
         if (a.d_weight) {
             MmaArgs g{};
-            g.cut = cut_product(p.piece, p.dim, p.tokens, true);
-            g.cut.m_tiles = (int32_t)ceil_div(words, 128 * g.cut.cg);
-            if (!make_map(&g.a, dz, width, p.tokens, p.piece, kBK) ||
-                !make_map(&g.b, hidden, p.dim, p.tokens, p.dim, kBK))
+            Job &jb = g.job;
+            jb.cut = cut_d_weight(p.tokens, p.dim, p.piece);
+            jb.cut.m_tiles = (int32_t)ceil_div(words, 128 * jb.cut.cg);
+            jb.n_fast = 1;
+            jb.rows = words;
+            jb.cols = p.dim;
+            jb.out_f32 = jb.cut.splits > 1;
+            float *slab = reinterpret_cast<float *>(a.ws + p.slab_w);
+            uint16_t *out = a.d_weight + w0 * a.d_weight_stride;
+            if (!make_map(&jb.a, dz, words, p.tokens, p.piece, kBK) ||
+                !make_map(&jb.b, hidden, p.dim, p.tokens, p.dim, kBK) ||
+                !(jb.out_f32
+                      ? make_out(&jb.out, slab, true, p.dim, words, p.dim, jb.cut.splits)
+                      : make_out(&jb.out, out, false, p.dim, words, a.d_weight_stride, 1)))
                 return cudaErrorInvalidValue;
-            g.n_fast = 1;
-            g.rows = words;
-            g.cols = p.dim;
-            g.slab = reinterpret_cast<float *>(a.ws + p.slab_w);
-            g.slab_stride = p.piece * p.dim;
-            g.store_slab = g.cut.splits > 1;
-            g.out = a.d_weight + w0 * a.d_weight_stride;
-            g.out_pitch = a.d_weight_stride;
-            if ((e = launch_cut<true, true, kOut, false>(g, s)) != cudaSuccess) return e;
-            if (g.cut.splits > 1) {
+            if ((e = launch_d_weight(g, s)) != cudaSuccess) return e;
+            if (jb.out_f32) {
                 k_head_slabs<<<(unsigned)ceil_div(words * p.dim, 2048), 256, 0, s>>>(
-                    g.slab, g.cut.splits, g.slab_stride, words, p.dim, g.out, g.out_pitch);
+                    slab, jb.cut.splits, words * p.dim, words, p.dim, out, a.d_weight_stride);
                 if ((e = cudaGetLastError()) != cudaSuccess) return e;
             }
         }

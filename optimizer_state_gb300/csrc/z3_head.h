@@ -18,7 +18,9 @@ constexpr int kHeadMaxList = 1024; // a token's teacher logits
 // A grid of products: how a [M][N] result of depth K is cut into tiles, and the
 // depth of a tile into splits.
 struct Cut {
-    int32_t cg;        // CTAs to a tile: 128 rows each
+    int32_t cg;        // CTAs to a tile
+    int32_t swap;      // rows and columns are exchanged (few tokens)
+    int32_t tile_m;    // rows of a CTA's: 128, or with swap fewer
     int32_t bn;        // columns of a tile
     int32_t m_tiles, n_tiles;
     int32_t k_tiles;   // of 64
@@ -30,17 +32,17 @@ struct Cut {
 struct HeadPlan {
     int64_t tokens, vocab, dim, k;
     Cut logits;          // [tokens][vocab] of depth dim, in the forward calls
-    int32_t n_tiles;     // its column tiles
+    int32_t parts;       // maxima and sums that its tiles leave of a token
     int64_t piece;       // words of a piece (a multiple of 256)
     int64_t pieces;
     // byte offsets into the workspace
-    int64_t part;        // float2 [n_tiles][tokens]: each tile's maximum and sum
+    int64_t part;        // float2 [parts][tokens]: maximum, sum of exponentials
     int64_t z;           // float [tokens][max(k, 1)]: logits of the target or the list
     int64_t sums;        // double2 [blocks]: the join's
     int64_t done;        // int: joined blocks
     int64_t state;       // int8 [tokens]: Row
     int64_t index, q;    // int32, float [tokens][k]: the list by ascending word
-    int64_t first;       // uint16 [tokens][tiles + 1]: a tile's first entry
+    int64_t first;       // uint16 [tokens][..]: where the entries of some words begin
     int64_t rows;        // float2 [tokens]: factor, lse * log2 e
     int64_t words;       // int32 [tokens]: the target
     int64_t hidden;      // bf16 [tokens][dim]: zero where the row is left out
