@@ -23,6 +23,7 @@ namespace {
 constexpr int kBK = 64;           // values of K in a stage: one swizzled row of 128 bytes
 constexpr int kEpilogueWarps = 8;
 constexpr int kMmaThreads = 128 + 32 * kEpilogueWarps;  // TMA, products, tensor memory, -
+constexpr int kGrain = 128;       // words: a list's entries are found by these
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -38,10 +39,13 @@ enum Kind : int32_t { kStats, kDz, kOut };
 struct Job {
     CUtensorMap a, b, out;
     Cut cut;
+    int32_t steps;         // of 16 values in the last k tile
     int32_t n_fast;        // walk a row of tiles before the next row
     int32_t a_m, a_k;      // where in the maps this product begins
     int32_t b_n, b_k;
-    int32_t out_f32;       // kOut: binary32 results, by split
+    uint16_t *out_at;      // kOut: the bf16 result
+    int64_t out_pitch;
+    int32_t out_f32;       // binary32 results instead, by split
     int32_t add;           // kOut: added to what is there
     int64_t rows, cols;    // tokens x words, or the rows and columns of kOut's result
 };
@@ -52,7 +56,6 @@ struct MmaArgs {
     float beta;            // log2(e) / temperature: exponents are powers of two
     int32_t word0;         // the word of column 0
     int32_t k;             // list length
-    int32_t grain;         // words between entries of `first`
     int32_t first_pitch;
     const int32_t *index;  // lists by ascending word, where each grain's entries begin
     const float *q;
@@ -189,6 +192,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     constexpr int kStage = stage_bytes<BN, CG>();
     constexpr int kBRows = BN / CG;  // of b that this CTA loads
     constexpr int kCols = 2 * BN;    // of tensor memory: two tiles
+    const int bn = KIND == kOut && !SWAP ? p.job.cut.bn : BN;  // columns of a tile
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
     const uint32_t staging = base + S * kStage;
@@ -216,7 +220,6 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             mbar_init(tempty(i), kEpilogueWarps * CG);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (KIND == kStats && blockIdx.x == 0) *p.done = 0;
     }
     if (warp == 2) tmem_alloc<CG>(tmem_at, kCols);
     __syncwarp();
@@ -226,6 +229,8 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     tmem_fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at) : "memory");
+    pdl_enter();  // barriers and tensor memory are set up beside the kernel before
+    if (KIND == kStats && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
 
     if (warp == 0 && lane == 0) {
         int stage = 0;
@@ -233,11 +238,13 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         bool ok = true;
         // SWAP: a tile may have fewer than 128 rows; the others are not loaded, and
         // what their sums are is not looked at
-        const uint32_t bytes = CG * (uint32_t)(kStage - (128 - jb.cut.tile_m) * 128);
+        const int b_boxes = BMN ? (bn / CG + 63) / 64 : 0;  // of 64 columns
+        const uint32_t bytes = CG * (uint32_t)(jb.cut.tile_m * 128 +
+                                               (BMN ? b_boxes * 64 : kBRows) * kBK * 2);
         for (int item = group; ok && item < items; item += groups) {
             const Tile t = tile_of(jb, item);
             const int m0 = jb.a_m + t.m * (jb.cut.tile_m * CG) + (int)rank * 128;
-            const int n0 = jb.b_n + t.n * BN + (int)rank * kBRows;
+            const int n0 = jb.b_n + t.n * bn + (int)rank * (bn / CG);
             const int k0 = t.split * jb.cut.k_chunk;
             const int k1 = min(jb.cut.k_tiles, k0 + jb.cut.k_chunk);
             for (int kt = k0; kt < k1; ++kt) {
@@ -254,7 +261,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                     tma_load<CG>(a, &jb.a, bar, ka, m0);
                 }
                 if constexpr (BMN) {
-                    for (int i = 0; i < kBRows / 64; ++i)
+                    for (int i = 0; i < b_boxes; ++i)
                         tma_load<CG>(b + i * (64 * kBK * 2), &jb.b, bar, n0 + 64 * i, kb);
                 } else {
                     tma_load<CG>(b, &jb.b, bar, kb, n0);
@@ -275,7 +282,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             }
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        constexpr uint32_t idesc = mma_desc(128 * CG, BN, AMN, BMN);
+        const uint32_t idesc = mma_desc(128 * CG, bn, AMN, BMN);
         constexpr uint32_t kStepA = AMN ? 16 * 128 / 16 : 32 / 16;  // 16 values of K on
         constexpr uint32_t kStepB = BMN ? 16 * 128 / 16 : 32 / 16;
         int stage = 0, done = 0;
@@ -296,9 +303,11 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 const uint32_t a = base + stage * kStage;
                 const uint64_t da = operand_desc<AMN>(a, 64 * kBK * 2);
                 const uint64_t db = operand_desc<BMN>(a + kA, 64 * kBK * 2);
+                const int steps = kt + 1 == jb.cut.k_tiles ? jb.steps : kBK / 16;
+                mma<CG>(d, da, db, idesc, kt > k0);
 #pragma unroll
-                for (int k = 0; k < kBK / 16; ++k)
-                    mma<CG>(d, da + k * kStepA, db + k * kStepB, idesc, kt > k0 || k > 0);
+                for (int k = 1; k < kBK / 16; ++k)
+                    if (k < steps) mma<CG>(d, da + k * kStepA, db + k * kStepB, idesc, true);
                 mma_commit<CG>(empty(stage));
                 if (++stage == S) {
                     stage = 0;
@@ -322,10 +331,11 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             // quarter, and its rows go on with each 32
             const int64_t row0 = SWAP ? (int64_t)t.n * BN + c0
                                       : (int64_t)t.m * (128 * CG) + rank * 128 + quad * 32;
-            const int col0 = SWAP ? t.m * jb.cut.tile_m + quad * 32 : t.n * BN + c0;
+            const int col0 = SWAP ? t.m * jb.cut.tile_m + quad * 32 : t.n * bn + c0;
             const int cols =  // valid ones among them
-                (int)min((int64_t)(SWAP ? min(32, jb.cut.tile_m - quad * 32) : kPer),
+                (int)min((int64_t)(SWAP ? min(32, jb.cut.tile_m - quad * 32) : min(kPer, bn - c0)),
                          jb.cols - col0);
+            const int per = KIND == kOut && !SWAP ? max(0, min(kPer, (cols + 31) / 32 * 32)) : kPer;
             int64_t row = row0 + lane;
             bool live = row < jb.rows;
             [[maybe_unused]] Walk<LIST> walk;
@@ -336,14 +346,15 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 rw = make_float2(0.0f, 0.0f);
                 if (!live || cols <= 0) return;
                 if constexpr (LIST) {
-                    const uint16_t *f =
-                        p.first + row * p.first_pitch + (p.word0 + col0) / p.grain;
+                    const uint16_t *f = p.first + row * p.first_pitch;
                     walk.index = p.index + row * p.k;
                     walk.word0 = p.word0 + col0;
-                    walk.at = f[0];
-                    walk.end = f[((SWAP ? cols : kPer) + p.grain - 1) / p.grain];
+                    walk.at = f[walk.word0 / kGrain];
+                    walk.end = f[(walk.word0 + cols - 1) / kGrain + 1];
                     if (walk.at < walk.end) walk.next = walk.index[walk.at] - walk.word0;
                     walk.load_after();
+                    if constexpr (SWAP)  // a quarter may begin within a grain
+                        while (walk.next < 0) walk.advance();
                 } else {
                     const int64_t w = KIND == kStats ? load_index(p.targets, p.target_bytes, row)
                                                      : (int64_t)p.words[row];
@@ -362,13 +373,13 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_leader(tempty(buf)));
             };
-            if (c0 >= BN) release();
+            if (c0 >= BN || per == 0) release();
 #pragma unroll 1
-            for (int i = 0; i < kPer && c0 + i < BN; i += 32) {
+            for (int i = 0; i < per && c0 + i < BN; i += 32) {
                 uint32_t bits[32];
                 tmem_load32(d + i, bits);
                 tmem_wait_load();
-                if (i + 32 == kPer) release();
+                if (i + 32 == per) release();
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = ok ? __uint_as_float(bits[j]) : NAN;
@@ -395,7 +406,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 }
                 const int c = SWAP ? 0 : i;  // column of v[0] from col0 on
                 if constexpr (KIND == kStats) {
-                    while (walk.next < c + 32) {
+                    while (walk.next < c + (SWAP ? min(32, cols) : 32)) {
                         p.z[LIST ? row * p.k + walk.at : row] = pick(v, (uint32_t)(walk.next - c));
                         walk.advance();
                     }
@@ -426,7 +437,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         v[j] = exp2_fast(__fmaf_rn(v[j], p.beta, -rw.y)) * rw.x;
-                    while (walk.next < c + 32) {
+                    while (walk.next < c + (SWAP ? min(32, cols) : 32)) {
                         float q = rw.x;
                         if constexpr (LIST) q = q * p.q[row * p.k + walk.at];
                         const int hit = walk.next - c;
@@ -462,7 +473,19 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-                    store_bf16(jb, stage, lane, i, w, col0, row0);
+                    if (i % 64 == 0 && i + 64 > bn - c0 && col0 + i + 32 < jb.cols) {
+                        // half a box at the tile's end, the next tile's columns behind it
+                        uint16_t *o = jb.out_at + row * jb.out_pitch + col0 + i;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (live)
+                                *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
+                                    w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    } else {
+                        store_bf16(jb, stage, lane, i, w, col0, row0);
+                        if (i % 64 == 0 && i + 32 == per)  // the box's other half is clipped
+                            store_box(jb, stage, lane, col0 + i, row0, 0);
+                    }
                 }
             }
             if constexpr (KIND == kStats && !SWAP)
@@ -497,7 +520,6 @@ struct RowArgs {
     float *q;
     uint16_t *first;
     int32_t first_pitch;
-    int32_t grain;         // words between its entries
 };
 
 __device__ __forceinline__ Row state_of(const RowArgs &a, int64_t t, int64_t *word) {
@@ -506,36 +528,46 @@ __device__ __forceinline__ Row state_of(const RowArgs &a, int64_t t, int64_t *wo
     return *word < 0 ? kLeftOut : *word < a.vocab ? kCounts : kBad;
 }
 
-constexpr int kListSort = 128;  // threads
+constexpr int kSortThreads = 128;
+
+// The larger one; a NaN stays.
+__device__ __forceinline__ float larger(float x, float y) {
+    return isnan(x) ? x : isnan(y) || y > x ? y : x;
+}
 
 // A token's list by ascending word, with q = softmax(teacher / temperature), and
-// where the entries of every `grain` words begin.  Entries of a negative word or a
-// logit of -Inf are left out (at the end, q = 0); a word beyond the vocabulary
-// spoils the row.  One CTA to a token: a bitonic sort of (word, place), so that
-// equal words keep their order.
-__global__ void __launch_bounds__(kListSort) k_head_lists(const RowArgs a, int pow2) {
-    extern __shared__ uint64_t key[];
-    __shared__ float red[kListSort / 32];
-    __shared__ int bad;
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x;
-    // the maximum; a NaN stays
-    auto larger = [](float x, float y) { return isnan(x) ? x : isnan(y) || y > x ? y : x; };
+// where the entries of every kGrain words begin.  Entries of a negative word
+// or a logit of -Inf are left out (at the end, q = 0); a word beyond the
+// vocabulary spoils the row.  N threads to a token: a warp for lists of up to
+// 64, whose bitonic sort of (word, place) then needs no barrier of the CTA
+// (4096 lists of 64: 9 us, 16 with 128 threads), 128 for longer ones (501
+// lists of 200: 10 us, 30 with a warp).  Equal words keep their order.
+template <int N>
+__global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, int pow2) {
+    extern __shared__ uint64_t keys[];
+    __shared__ float red[2][kSortThreads / 32];
+    pdl_enter();
+    const int tid = threadIdx.x % N;
+    const int64_t t = (int64_t)blockIdx.x * (kSortThreads / N) + threadIdx.x / N;
+    uint64_t *key = keys + threadIdx.x / N * pow2;
+    if (t >= a.tokens) return;  // all threads of the token
+    auto sync = [] {
+        if constexpr (N == 32) __syncwarp(); else __syncthreads();
+    };
     auto logit = [&](int i) {
         return a.teacher_bytes == 2
                    ? bf16_to_f32(static_cast<const uint16_t *>(a.teacher)[t * a.k + i])
                    : static_cast<const float *>(a.teacher)[t * a.k + i];
     };
-    if (tid == 0) bad = 0;
-    __syncthreads();
+    bool bad = false;
     float top = -INFINITY;
-    for (int i = tid; i < pow2; i += kListSort) {
+    for (int i = tid; i < pow2; i += N) {
         uint32_t word = 0x7fffffffu;
         if (i < a.k) {
             const int64_t w = load_index(a.index, a.index_bytes, t * a.k + i);
             const float x = logit(i);
             if (w >= a.vocab) {
-                bad = 1;
+                bad = true;
             } else if (w >= 0 && x != -INFINITY) {
                 word = (uint32_t)w;
                 top = larger(top, x);
@@ -544,13 +576,17 @@ __global__ void __launch_bounds__(kListSort) k_head_lists(const RowArgs a, int p
         key[i] = (uint64_t)word << 32 | (uint32_t)i;
     }
     for (int o = 16; o > 0; o /= 2) top = larger(top, __shfl_xor_sync(~0u, top, o));
-    if (tid % 32 == 0) red[tid / 32] = top;
-    __syncthreads();
-    for (int i = 0; i < kListSort / 32; ++i) top = larger(top, red[i]);
+    if constexpr (N == 32) {
+        bad = __any_sync(~0u, bad);
+    } else {
+        if (tid % 32 == 0) red[0][tid / 32] = top;
+        bad = __syncthreads_or(bad);
+        for (int i = 0; i < N / 32; ++i) top = larger(top, red[0][i]);
+    }
     for (int size = 2; size <= pow2; size *= 2) {
         for (int stride = size / 2; stride > 0; stride /= 2) {
-            __syncthreads();
-            for (int i = tid; i < pow2 / 2; i += kListSort) {
+            sync();
+            for (int i = tid; i < pow2 / 2; i += N) {
                 const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
                 const uint64_t x = key[lo], y = key[hi];
                 if ((x > y) == ((lo & size) == 0)) {
@@ -560,7 +596,7 @@ __global__ void __launch_bounds__(kListSort) k_head_lists(const RowArgs a, int p
             }
         }
     }
-    __syncthreads();
+    sync();
     auto begin = [&](uint32_t word) {  // the first entry of this word or a later one
         int lo = 0, hi = a.k;
         while (lo < hi) {
@@ -572,22 +608,24 @@ __global__ void __launch_bounds__(kListSort) k_head_lists(const RowArgs a, int p
     const int count = begin(0x7fffffffu);
     const float inv = __fdiv_rn(1.0f, a.temperature);
     float sum = 0.0f;
-    for (int i = tid; i < count; i += kListSort)
+    for (int i = tid; i < count; i += N)
         sum += exp2f((logit((int)(uint32_t)key[i]) - top) * inv * kLog2e);
     for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
-    if (tid % 32 == 0) red[tid / 32] = sum;  // `top` has been read: a barrier lies between
-    __syncthreads();
-    sum = 0.0f;
-    for (int i = 0; i < kListSort / 32; ++i) sum += red[i];
+    if constexpr (N > 32) {
+        if (tid % 32 == 0) red[1][tid / 32] = sum;
+        __syncthreads();
+        sum = 0.0f;
+        for (int i = 0; i < N / 32; ++i) sum += red[1][i];
+    }
     const float norm = __fdiv_rn(1.0f, sum);
-    for (int i = tid; i < a.k; i += kListSort) {
+    for (int i = tid; i < a.k; i += N) {
         a.list[t * a.k + i] = (int32_t)(key[i] >> 32);
         a.q[t * a.k + i] =
             i < count ? exp2f((logit((int)(uint32_t)key[i]) - top) * inv * kLog2e) * norm : 0.0f;
     }
-    for (int n = tid; n < a.first_pitch; n += kListSort)
+    for (int n = tid; n < a.first_pitch; n += N)
         a.first[t * a.first_pitch + n] =
-            (uint16_t)min(count, begin((uint32_t)min((int64_t)n * a.grain, (int64_t)0x7fffffff)));
+            (uint16_t)min(count, begin((uint32_t)min((int64_t)n * kGrain, (int64_t)0x7fffffff)));
     if (tid == 0) a.state[t] = bad ? kBad : count > 0 ? kCounts : kLeftOut;
 }
 
@@ -600,31 +638,49 @@ struct JoinArgs {
     float *loss, *lse, *total;
 };
 
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 
-// Joins the tiles' maxima and sums, TOK tokens to a block, and finishes
-// each token's loss; the last block adds up the blocks' sums in their order.
-// Bound by latency: with 8192 tokens it reads 13 MB.  Few tokens take a block
-// each.
+__device__ __forceinline__ float2 join2(float2 x, float2 y) {
+    const float m = fmaxf(x.x, y.x);
+    const float s = m == -INFINITY ? 0.0f : m;
+    return make_float2(m, __fmaf_rn(x.y, exp2_fast(x.x - s), y.y * exp2_fast(y.x - s)));
+}
+
+// The sum of the block's values, in a fixed order; in thread 0.
+__device__ __forceinline__ double2 block_sum(double2 v, double2 *warps) {
+    for (int o = 16; o > 0; o /= 2) {
+        v.x += __shfl_down_sync(~0u, v.x, o);
+        v.y += __shfl_down_sync(~0u, v.y, o);
+    }
+    if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = v;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int w = 1; w < kJoinThreads / 32; ++w) {
+            v.x += warps[w].x;
+            v.y += warps[w].y;
+        }
+    return v;
+}
+
+// Joins the tiles' maxima and sums, TOK tokens to a block, and finishes each
+// token's loss; the last block adds up the blocks' sums in their order.
+// Bound by latency: with 8192 tokens it reads 26 MB, eight loads of a thread in
+// flight.  Few tokens take a block each.
 template <int TOK>
 __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
     constexpr int kSlices = kJoinThreads / TOK;
-    __shared__ float2 joined[kSlices][TOK];
-    __shared__ float lists[kSlices][TOK];
-    __shared__ float lse2s[TOK];
-    __shared__ double2 pair[kJoinThreads];
+    constexpr int kWarps = kJoinThreads / 32;
+    __shared__ float2 joined[kWarps][TOK];
+    __shared__ float lists[kWarps][TOK];
+    __shared__ double2 warps[2][kWarps];
     __shared__ bool last;
-    const int tok = threadIdx.x % TOK, slice = threadIdx.x / TOK;
+    pdl_enter();
+    const int tok = threadIdx.x % TOK, slice = threadIdx.x / TOK, warp = threadIdx.x / 32;
     const int64_t t = (int64_t)blockIdx.x * TOK + tok;
     const bool live = t < a.row.tokens;
-    auto join = [](float2 x, float2 y) {
-        const float m = fmaxf(x.x, y.x);
-        const float s = m == -INFINITY ? 0.0f : m;
-        return make_float2(m, __fmaf_rn(x.y, exp2_fast(x.x - s), y.y * exp2_fast(y.x - s)));
-    };
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (live) {
-        for (int n = slice; n < a.row.parts; n += 8 * kSlices) {  // eight loads in flight
+        for (int n = slice; n < a.row.parts; n += 8 * kSlices) {
             float2 x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -632,19 +688,22 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
                            ? a.part[(int64_t)(n + i * kSlices) * a.row.tokens + t]
                            : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc = join(acc, x[i]);
+            for (int i = 4; i > 0; i /= 2)
+#pragma unroll
+                for (int j = 0; j < i; ++j) x[j] = join2(x[j], x[j + i]);
+            acc = join2(acc, x[0]);
         }
     }
-    joined[slice][tok] = acc;
+#pragma unroll
+    for (int o = 16; o >= TOK; o /= 2)
+        acc = join2(acc, make_float2(__shfl_xor_sync(~0u, acc.x, o),
+                                     __shfl_xor_sync(~0u, acc.y, o)));
+    if (threadIdx.x % 32 < TOK) joined[warp][tok] = acc;
     __syncthreads();
-    for (int w = kSlices / 2; w > 0; w /= 2) {
-        if (slice < w) joined[slice][tok] = join(joined[slice][tok], joined[slice + w][tok]);
-        __syncthreads();
-    }
-    if (slice == 0)  // a sum that is not a number stays one through the logarithm
-        lse2s[tok] = joined[0][tok].x + log2f(joined[0][tok].y);
-    __syncthreads();
-    const float lse = lse2s[tok] * kLn2;
+    acc = joined[0][tok];
+    for (int w = 1; w < kWarps; ++w) acc = join2(acc, joined[w][tok]);
+    // a sum that is not a number stays one through the logarithm
+    const float lse = (acc.x + log2f(acc.y)) * kLn2;
     int64_t word = 0;
     const Row state = live ? state_of(a.row, t, &word) : kLeftOut;
     if (a.row.k > 0) {
@@ -658,57 +717,48 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
                     part += q * (logf(q) - a.z[t * a.row.k + i] * inv + lse);
             }
         }
-        lists[slice][tok] = part;
+#pragma unroll
+        for (int o = 16; o >= TOK; o /= 2) part += __shfl_xor_sync(~0u, part, o);
+        if (threadIdx.x % 32 < TOK) lists[warp][tok] = part;
         __syncthreads();
-        for (int w = kSlices / 2; w > 0; w /= 2) {
-            if (slice < w) lists[slice][tok] += lists[slice + w][tok];
-            __syncthreads();
-        }
     }
     double2 mine = make_double2(0.0, 0.0);
     if (slice == 0 && live) {
         float loss = 0.0f;
-        if (state == kBad)
+        if (state == kBad) {
             loss = NAN;
-        else if (state == kCounts)
-            loss = a.row.k > 0 ? a.row.temperature * a.row.temperature * lists[0][tok]
-                               : lse - a.z[t];
+        } else if (state == kCounts && a.row.k > 0) {
+            for (int w = 0; w < kWarps; ++w) loss += lists[w][tok];
+            loss *= a.row.temperature * a.row.temperature;
+        } else if (state == kCounts) {
+            loss = lse - a.z[t];
+        }
         a.loss[t] = loss;
         a.lse[t] = state == kLeftOut ? 0.0f : lse;
         const float w = state == kLeftOut ? 0.0f : a.row.weights ? a.row.weights[t] : 1.0f;
         if (w != 0.0f) mine = make_double2((double)w * (double)loss, (double)w);
     }
-    auto total = [&] {  // over the block, in a fixed order
-        __syncthreads();
-        pair[threadIdx.x] = mine;
-        __syncthreads();
-        for (int w = kJoinThreads / 2; w > 0; w /= 2) {
-            if (threadIdx.x < w) {
-                pair[threadIdx.x].x += pair[threadIdx.x + w].x;
-                pair[threadIdx.x].y += pair[threadIdx.x + w].y;
-            }
-            __syncthreads();
+    mine = block_sum(mine, warps[0]);
+    if (gridDim.x > 1) {
+        if (threadIdx.x == 0) {
+            a.sums[blockIdx.x] = mine;
+            __threadfence();
+            last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+            __threadfence();
         }
-    };
-    total();
-    if (threadIdx.x == 0) {
-        a.sums[blockIdx.x] = pair[0];
-        __threadfence();
-        last = atomicAdd(a.done, 1u) == gridDim.x - 1;
-        __threadfence();
+        __syncthreads();
+        if (!last) return;
+        mine = make_double2(0.0, 0.0);
+        for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) {
+            const double2 x = __ldcg(a.sums + i);  // from L2, where the other blocks left them
+            mine.x += x.x;
+            mine.y += x.y;
+        }
+        mine = block_sum(mine, warps[1]);
     }
-    __syncthreads();
-    if (!last) return;
-    mine = make_double2(0.0, 0.0);
-    for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) {
-        const double2 x = __ldcg(a.sums + i);  // from L2, where the other blocks left them
-        mine.x += x.x;
-        mine.y += x.y;
-    }
-    total();
     if (threadIdx.x == 0) {
-        a.total[0] = (float)pair[0].x;
-        a.total[1] = (float)pair[0].y;
+        a.total[0] = (float)mine.x;
+        a.total[1] = (float)mine.y;
     }
 }
 
@@ -729,6 +779,7 @@ struct FactorArgs {
 // what stands there may be anything, and 0 * NaN would reach d_weight.  The
 // copy costs 4 bytes a value, 5 us of the 1.9 ms at 8192 x 1024.
 __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
+    pdl_enter();
     const int64_t t = blockIdx.x;
     int64_t word = -1;
     const Row state = state_of(a.row, t, &word);
@@ -755,6 +806,7 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
 __global__ void __launch_bounds__(256) k_head_slabs(const float *slab, int splits, int64_t stride,
                                                     int64_t rows, int64_t cols, uint16_t *out,
                                                     int64_t pitch) {
+    pdl_enter();
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
     if (i >= rows * cols) return;
     const int64_t r = i / cols, c = i - r * cols;
@@ -773,6 +825,25 @@ __global__ void __launch_bounds__(256) k_head_slabs(const float *slab, int split
 // --------------------------------------------------------------------------
 // host side: cutting, tensor maps, launches
 // --------------------------------------------------------------------------
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A kernel that begins with pdl_enter.
+template <typename... KArgs, typename... Args>
+void launch_small(void (*kernel)(KArgs...), int64_t grid, int block, size_t smem, cudaStream_t s,
+                  Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    (void)cudaLaunchKernelEx(&cfg, kernel, args...);  // errors: cudaGetLastError
+}
 
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -839,12 +910,14 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
     cfg.blockDim = dim3(kMmaThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = CG;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = CG > 1 ? 1 : 0;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG > 1 ? 2 : 1;
     (void)cudaLaunchKernelEx(&cfg, kernel, p);
     return cudaGetLastError();
 }
@@ -863,16 +936,15 @@ cudaError_t launch_d_hidden(const MmaArgs &p, cudaStream_t s) {
     if (c.swap)
         return c.bn == 32 ? launch_mma<1, 32, true, true, false, kOut, false>(p, s)
                           : launch_mma<1, 128, true, true, false, kOut, false>(p, s);
-    return c.bn == 256 ? launch_mma<2, 256, false, false, true, kOut, false>(p, s)
-                       : launch_mma<2, 128, false, false, true, kOut, false>(p, s);
+    return c.bn > 128 ? launch_mma<2, 256, false, false, true, kOut, false>(p, s)
+                      : launch_mma<2, 128, false, false, true, kOut, false>(p, s);
 }
 
 cudaError_t launch_d_weight(const MmaArgs &p, cudaStream_t s) {
-    return p.job.cut.bn == 256 ? launch_mma<2, 256, false, true, true, kOut, false>(p, s)
-                               : launch_mma<2, 128, false, true, true, kOut, false>(p, s);
+    return p.job.cut.bn > 128 ? launch_mma<2, 256, false, true, true, kOut, false>(p, s)
+                              : launch_mma<2, 128, false, true, true, kOut, false>(p, s);
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kFew = 128;  // tokens that SWAP takes
 
@@ -907,7 +979,9 @@ Cut cut_out(int64_t m, int64_t n, int64_t k, bool swap, int64_t tokens) {
     Cut c{};
     c.swap = swap;
     c.cg = swap ? 1 : 2;
-    c.bn = swap ? (tokens <= 32 ? 32 : 128) : n <= 128 ? 128 : 256;
+    // the columns in equal tiles of up to 256, in steps of 32
+    c.bn = swap ? (tokens <= 32 ? 32 : 128)
+                : (int32_t)(ceil_div(ceil_div(n, ceil_div(n, 256)), 32) * 32);
     c.tile_m = 128;
     c.m_tiles = (int32_t)ceil_div(m, 128 * c.cg);
     c.n_tiles = (int32_t)ceil_div(n, c.bn);
@@ -932,13 +1006,10 @@ Cut cut_d_weight(int64_t tokens, int64_t dim, int64_t words) {
 
 constexpr int64_t kPieceBytes = 256ll << 20;  // of dz
 
-// Words between the entries of `first`: what a warp of the logits' epilogue takes,
-// or what a quarter of a SWAP tile begins on.
-int grain(const HeadPlan &p) { return p.logits.swap ? 8 : 128; }
-// ... which goes up to the end of the last tile of the last piece.
-int64_t first_pitch(const HeadPlan &p) { return ceil_div(p.vocab, 256) * (256 / grain(p)) + 1; }
+// Up to the end of the last tile.
+int64_t first_pitch(const HeadPlan &p) { return ceil_div(p.vocab, 256) * (256 / kGrain) + 1; }
 
-int join_tokens(int64_t tokens) { return tokens <= 1024 ? 1 : 32; }
+int join_tokens(int64_t tokens) { return tokens <= kFew ? 1 : 8; }
 
 RowArgs row_args(const HeadArgs &a) {
     const HeadPlan &p = a.plan;
@@ -959,14 +1030,18 @@ RowArgs row_args(const HeadArgs &a) {
     r.q = reinterpret_cast<float *>(a.ws + p.q);
     r.first = reinterpret_cast<uint16_t *>(a.ws + p.first);
     r.first_pitch = (int32_t)first_pitch(p);
-    r.grain = grain(p);
     return r;
 }
 
 cudaError_t launch_lists(const RowArgs &r, cudaStream_t s) {
     int pow2 = 2;
     while (pow2 < r.k) pow2 *= 2;
-    k_head_lists<<<(unsigned)r.tokens, kListSort, pow2 * sizeof(uint64_t), s>>>(r, pow2);
+    if (pow2 <= 64)
+        launch_small(k_head_lists<32>, ceil_div(r.tokens, kSortThreads / 32), kSortThreads,
+                     kSortThreads / 32 * pow2 * sizeof(uint64_t), s, r, pow2);
+    else
+        launch_small(k_head_lists<kSortThreads>, r.tokens, kSortThreads, pow2 * sizeof(uint64_t),
+                     s, r, pow2);
     return cudaGetLastError();
 }
 
@@ -976,14 +1051,16 @@ void fill_lists(MmaArgs *m, const RowArgs &r) {
     m->q = r.q;
     m->first = r.first;
     m->first_pitch = r.first_pitch;
-    m->grain = r.grain;
 }
+
+int last_steps(int64_t k) { return (int)ceil_div(k - (ceil_div(k, kBK) - 1) * kBK, 16); }
 
 // The product of the hidden states with the words from w0 on.
 bool logits_job(MmaArgs *m, const HeadArgs &a, const Cut &cut, int64_t w0, int64_t words) {
     const HeadPlan &p = a.plan;
     Job &jb = m->job;
     jb.cut = cut;
+    jb.steps = last_steps(p.dim);
     jb.rows = p.tokens;
     jb.cols = words;
     m->word0 = (int32_t)w0;
@@ -1076,9 +1153,9 @@ cudaError_t launch_head_forward(const HeadArgs &a, cudaStream_t s) {
     j.lse = a.lse;
     j.total = a.total;
     if (join_tokens(p.tokens) == 1)
-        k_head_join<1><<<(unsigned)p.tokens, kJoinThreads, 0, s>>>(j);
+        launch_small(k_head_join<1>, p.tokens, kJoinThreads, 0, s, j);
     else
-        k_head_join<32><<<(unsigned)ceil_div(p.tokens, 32), kJoinThreads, 0, s>>>(j);
+        launch_small(k_head_join<8>, ceil_div(p.tokens, 8), kJoinThreads, 0, s, j);
     return cudaGetLastError();
 }
 
@@ -1103,7 +1180,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
     f.hidden = a.hidden;
     f.stride = a.hidden_stride;
     f.copy = a.d_weight ? hidden : nullptr;
-    k_head_factors<<<(unsigned)p.tokens, 128, 0, s>>>(f);
+    launch_small(k_head_factors, p.tokens, 128, 0, s, f);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
     uint16_t *dz = reinterpret_cast<uint16_t *>(a.ws + p.dz);
@@ -1134,6 +1211,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
             const int splits = jb.cut.splits;
             jb.cut.k_tiles = (int32_t)ceil_div(words, kBK);
             jb.cut.splits = (int32_t)ceil_div(jb.cut.k_tiles, jb.cut.k_chunk);
+            jb.steps = last_steps(words);
             jb.n_fast = 1;
             jb.rows = p.tokens;
             jb.cols = p.dim;
@@ -1153,12 +1231,14 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
             ok = ok && (jb.out_f32 ? make_out(&jb.out, slab, true, p.dim, p.tokens, p.dim, splits)
                                    : make_out(&jb.out, a.d_hidden, false, p.dim, p.tokens,
                                               a.d_hidden_stride, 1));
+            jb.out_at = a.d_hidden;
+            jb.out_pitch = a.d_hidden_stride;
             if (!ok) return cudaErrorInvalidValue;
             if ((e = launch_d_hidden(h, s)) != cudaSuccess) return e;
             if (last && jb.out_f32) {
-                k_head_slabs<<<(unsigned)ceil_div(p.tokens * p.dim, 2048), 256, 0, s>>>(
-                    slab, p.pieces > 1 ? splits : jb.cut.splits, p.tokens * p.dim, p.tokens, p.dim,
-                    a.d_hidden, a.d_hidden_stride);
+                launch_small(k_head_slabs, ceil_div(p.tokens * p.dim, 2048), 256, 0, s, slab,
+                             p.pieces > 1 ? splits : jb.cut.splits, p.tokens * p.dim, p.tokens,
+                             p.dim, a.d_hidden, a.d_hidden_stride);
                 if ((e = cudaGetLastError()) != cudaSuccess) return e;
             }
         }
@@ -1167,12 +1247,15 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
             Job &jb = g.job;
             jb.cut = cut_d_weight(p.tokens, p.dim, p.piece);
             jb.cut.m_tiles = (int32_t)ceil_div(words, 128 * jb.cut.cg);
+            jb.steps = last_steps(p.tokens);
             jb.n_fast = 1;
             jb.rows = words;
             jb.cols = p.dim;
             jb.out_f32 = jb.cut.splits > 1;
             float *slab = reinterpret_cast<float *>(a.ws + p.slab_w);
             uint16_t *out = a.d_weight + w0 * a.d_weight_stride;
+            jb.out_at = out;
+            jb.out_pitch = a.d_weight_stride;
             if (!make_map(&jb.a, dz, words, p.tokens, p.piece, kBK) ||
                 !make_map(&jb.b, hidden, p.dim, p.tokens, p.dim, kBK) ||
                 !(jb.out_f32
@@ -1181,8 +1264,8 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
                 return cudaErrorInvalidValue;
             if ((e = launch_d_weight(g, s)) != cudaSuccess) return e;
             if (jb.out_f32) {
-                k_head_slabs<<<(unsigned)ceil_div(words * p.dim, 2048), 256, 0, s>>>(
-                    slab, jb.cut.splits, words * p.dim, words, p.dim, out, a.d_weight_stride);
+                launch_small(k_head_slabs, ceil_div(words * p.dim, 2048), 256, 0, s, slab,
+                             jb.cut.splits, words * p.dim, words, p.dim, out, a.d_weight_stride);
                 if ((e = cudaGetLastError()) != cudaSuccess) return e;
             }
         }
