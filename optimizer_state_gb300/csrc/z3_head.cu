@@ -91,6 +91,11 @@ constexpr int kSmem = 196608 + kEpilogueWarps * kStaging + 1024 + 512;
 static_assert(kSmem <= 232448 && kSmem > 116736,
               "fits an SM, and no second CTA beside it competes for its tensor memory");
 
+template <int N>
+struct Steps {
+    static constexpr int value = N;
+};
+
 struct Tile {
     int m, n, split;
 };
@@ -296,23 +301,31 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             const uint32_t d = tmem + buf * BN;
             ok = mbar_wait(tempty(buf), ((done >> 1) & 1) ^ 1);
             tmem_fence_after();
-            for (int kt = k0; ok && kt < k1; ++kt) {
+            // one k tile; the four products stand without a branch between them
+            // (with one, 8192 x 50257 x 1024 took 537 us instead of 511)
+            auto product = [&](int kt, auto steps) {
                 ok = mbar_wait(full(stage), phase);
-                if (!ok) break;
+                if (!ok) return;
                 tmem_fence_after();
                 const uint32_t a = base + stage * kStage;
                 const uint64_t da = operand_desc<AMN>(a, 64 * kBK * 2);
                 const uint64_t db = operand_desc<BMN>(a + kA, 64 * kBK * 2);
-                const int steps = kt + 1 == jb.cut.k_tiles ? jb.steps : kBK / 16;
-                mma<CG>(d, da, db, idesc, kt > k0);
 #pragma unroll
-                for (int k = 1; k < kBK / 16; ++k)
-                    if (k < steps) mma<CG>(d, da + k * kStepA, db + k * kStepB, idesc, true);
+                for (int k = 0; k < decltype(steps)::value; ++k)
+                    mma<CG>(d, da + k * kStepA, db + k * kStepB, idesc, kt > k0 || k > 0);
                 mma_commit<CG>(empty(stage));
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1;
                 }
+            };
+            // the depth's last tile may hold fewer than four times 16 values
+            const int whole = k1 == jb.cut.k_tiles && jb.steps < 4 ? k1 - 1 : k1;
+            for (int kt = k0; ok && kt < whole; ++kt) product(kt, Steps<4>{});
+            if (ok && whole < k1) {
+                if (jb.steps == 1) product(whole, Steps<1>{});
+                if (jb.steps == 2) product(whole, Steps<2>{});
+                if (jb.steps == 3) product(whole, Steps<3>{});
             }
             if (ok) mma_commit<CG>(tfull(buf));
         }

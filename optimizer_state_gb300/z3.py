@@ -587,70 +587,81 @@ def head_workspace(tokens: int, dim: int, vocab: int, k: int = 0, grads: bool = 
     return torch.empty(n.value, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
-def _matrix(t, rows, cols, name: str):
+@functools.cache
+def _head_types():
+    torch = _torch()
+    b16, f32 = _dtypes()
+    return b16, f32, (torch.int32, torch.int64), (torch.bfloat16, torch.float32), (torch.uint8,)
+
+
+def _matrix(t, rows, cols, here, name: str):
     """Address and row stride of a bf16 [rows][cols] CUDA tensor whose rows
     may lie apart."""
     if t is None:
         return None, 0
-    b16, _ = _dtypes()
-    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+    if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name}: needs shape [{rows}, {cols}], has {list(t.shape)}")
-    apart = t.stride(0) if rows > 1 else cols
-    if cols > 1 and t.stride(1) != 1 or apart < cols:
+    apart, step = t.stride()
+    if rows <= 1:
+        apart = cols
+    if cols > 1 and step != 1 or apart < cols:
         raise ValueError(f"{name}: strides {t.stride()}: rows must be contiguous and apart")
-    _dev(t[:0], b16, 0, name)                       # device and type
+    b16 = _head_types()[0]
+    if not t.is_cuda or t.get_device() != here or t.dtype not in b16:
+        _dev(t[:0], b16, 0, name)                   # says what is wrong
     return t.data_ptr(), apart
 
 
-def _vector(t, dtypes, shape, name: str):
-    if t is not None and tuple(t.shape) != shape:
+def _vector(t, dtypes, shape, here, name: str):
+    if t is None:
+        return None
+    if tuple(t.shape) != shape:
         raise ValueError(f"{name}: needs shape {list(shape)}, has {list(t.shape)}")
-    return _dev(t, dtypes, 0, name)
+    if not t.is_cuda or t.get_device() != here or t.dtype not in dtypes or not t.is_contiguous():
+        _dev(t, dtypes, 0, name)                    # says what is wrong
+    return t.data_ptr()
 
 
-def _head(hidden, weight, weights):
-    """struct z3_head of tensors, and its sizes."""
-    for t, name in ((hidden, "hidden"), (weight, "weight")):
+class _HeadCall:
+    """The arguments that the calls below share, from tensors."""
+
+    def __init__(self, hidden, weight, weights, workspace, stream):
+        for t, name in ((hidden, "hidden"), (weight, "weight")):
+            if t.dim() != 2:
+                raise ValueError(f"{name}: needs two dimensions, has shape {list(t.shape)}")
+        self.n, self.d = n, d = hidden.shape
+        self.v = v = weight.shape[0]
+        self.here = here = _current_device()() if hidden.is_cuda else None
+        h, hs = _matrix(hidden, n, d, here, "hidden")
+        w, ws = _matrix(weight, v, d, here, "weight")
+        self.head = ctypes.byref(Head(h, hs, w, ws, n, v, d, self.vector(weights, 1, (n,),
+                                                                         "weights")))
+        self.end = (_vector(workspace, _head_types()[4], workspace.shape[:1], here, "workspace"),
+                    workspace.shape[0], _stream(stream))
+
+    def vector(self, t, kind, shape, name):
+        return _vector(t, _head_types()[kind], shape, self.here, name)
+
+    def targets(self, t):
+        return self.vector(t, 2, (self.n,), "targets"), t.element_size()
+
+    def teacher(self, t, index, temperature):
         if t.dim() != 2:
-            raise ValueError(f"{name}: needs two dimensions, has shape {list(t.shape)}")
-    n, d = hidden.shape
-    v = weight.shape[0]
-    _, f32 = _dtypes()
-    h, hs = _matrix(hidden, n, d, "hidden")
-    w, ws = _matrix(weight, v, d, "weight")
-    return Head(h, hs, w, ws, n, v, d, _vector(weights, f32, (n,), "weights")), n, v, d
+            raise ValueError(f"teacher: needs two dimensions, has shape {list(t.shape)}")
+        k = t.shape[1]
+        return ctypes.byref(Teacher(
+            self.vector(t, 3, (self.n, k), "teacher"), self.vector(index, 2, (self.n, k), "index"),
+            Z3_F32 if t.element_size() == 4 else Z3_BF16, index.element_size(), k, temperature))
 
+    def losses(self, loss, lse, total):
+        n = (self.n,)
+        return (self.vector(loss, 1, n, "loss"), self.vector(lse, 1, n, "lse"),
+                self.vector(total, 1, (2,), "total"))
 
-def _index(t, shape, name: str):
-    torch = _torch()
-    return _vector(t, (torch.int32, torch.int64), shape, name), t.element_size()
-
-
-def _teacher(teacher, index, temperature, n):
-    torch = _torch()
-    if teacher.dim() != 2:
-        raise ValueError(f"teacher: needs two dimensions, has shape {list(teacher.shape)}")
-    k = teacher.shape[1]
-    logits = _vector(teacher, (torch.bfloat16, torch.float32), (n, k), "teacher")
-    idx, size = _index(index, (n, k), "index")
-    return Teacher(logits, idx, Z3_BF16 if teacher.dtype == torch.bfloat16 else Z3_F32, size, k,
-                   temperature)
-
-
-def _space(workspace):
-    return _dev(workspace, (_torch().uint8,), 0, "workspace"), workspace.numel()
-
-
-def _losses(loss, lse, total, n):
-    _, f32 = _dtypes()
-    return (_vector(loss, f32, (n,), "loss"), _vector(lse, f32, (n,), "lse"),
-            _vector(total, f32, (2,), "total"))
-
-
-def _head_grads(lse, total, scale, d_hidden, d_weight, n, v, d):
-    _, f32 = _dtypes()
-    return (_vector(lse, f32, (n,), "lse"), _vector(total, f32, (2,), "total"), scale,
-            *_matrix(d_hidden, n, d, "d_hidden"), *_matrix(d_weight, v, d, "d_weight"))
+    def grads(self, lse, total, scale, d_hidden, d_weight):
+        return (self.vector(lse, 1, (self.n,), "lse"), self.vector(total, 1, (2,), "total"), scale,
+                *_matrix(d_hidden, self.n, self.d, self.here, "d_hidden"),
+                *_matrix(d_weight, self.v, self.d, self.here, "d_weight"))
 
 
 def z3_xent(hidden, weight, targets, loss, lse, total, workspace, weights=None, stream=None):
@@ -659,9 +670,8 @@ def z3_xent(hidden, weight, targets, loss, lse, total, workspace, weights=None, 
     targets: int32 or int64 [tokens], negative ones left out; weights: fp32
     [tokens] or None; loss and lse: fp32 [tokens], total: fp32 [2], receive the
     tokens' losses and {sum of weighted losses, sum of weights}."""
-    h, n, _, _ = _head(hidden, weight, weights)
-    _check(load().z3_xent(ctypes.byref(h), *_index(targets, (n,), "targets"),
-                          *_losses(loss, lse, total, n), *_space(workspace), _stream(stream)))
+    c = _HeadCall(hidden, weight, weights, workspace, stream)
+    _check(load().z3_xent(c.head, *c.targets(targets), *c.losses(loss, lse, total), *c.end))
 
 
 def z3_xent_grad(hidden, weight, targets, lse, total, scale: float, d_hidden, d_weight, workspace,
@@ -669,10 +679,9 @@ def z3_xent_grad(hidden, weight, targets, lse, total, scale: float, d_hidden, d_
     """The gradients of scale * total[0] / total[1] (total None: of scale times
     the sum) into d_hidden and d_weight, either of which may be None; lse and
     total as z3_xent wrote them."""
-    h, n, v, d = _head(hidden, weight, weights)
-    _check(load().z3_xent_grad(ctypes.byref(h), *_index(targets, (n,), "targets"),
-                               *_head_grads(lse, total, scale, d_hidden, d_weight, n, v, d),
-                               *_space(workspace), _stream(stream)))
+    c = _HeadCall(hidden, weight, weights, workspace, stream)
+    _check(load().z3_xent_grad(c.head, *c.targets(targets),
+                               *c.grads(lse, total, scale, d_hidden, d_weight), *c.end))
 
 
 def z3_distill(hidden, weight, teacher, index, temperature: float, loss, lse, total, workspace,
@@ -680,19 +689,16 @@ def z3_distill(hidden, weight, teacher, index, temperature: float, loss, lse, to
     """Divergence of the head's softmax from that of a teacher's k highest
     logits, teacher [tokens, k] (bf16 or fp32) at the words index [tokens, k]
     (int32 or int64; negative ones left out).  The rest as z3_xent."""
-    h, n, _, _ = _head(hidden, weight, weights)
-    t = _teacher(teacher, index, temperature, n)
-    _check(load().z3_distill(ctypes.byref(h), ctypes.byref(t), *_losses(loss, lse, total, n),
-                             *_space(workspace), _stream(stream)))
+    c = _HeadCall(hidden, weight, weights, workspace, stream)
+    _check(load().z3_distill(c.head, c.teacher(teacher, index, temperature),
+                             *c.losses(loss, lse, total), *c.end))
 
 
 def z3_distill_grad(hidden, weight, teacher, index, temperature: float, lse, total, scale: float,
                     d_hidden, d_weight, workspace, weights=None, stream=None):
-    h, n, v, d = _head(hidden, weight, weights)
-    t = _teacher(teacher, index, temperature, n)
-    _check(load().z3_distill_grad(ctypes.byref(h), ctypes.byref(t),
-                                  *_head_grads(lse, total, scale, d_hidden, d_weight, n, v, d),
-                                  *_space(workspace), _stream(stream)))
+    c = _HeadCall(hidden, weight, weights, workspace, stream)
+    _check(load().z3_distill_grad(c.head, c.teacher(teacher, index, temperature),
+                                  *c.grads(lse, total, scale, d_hidden, d_weight), *c.end))
 
 
 def _host(t, dtypes, numel: int, name: str):
