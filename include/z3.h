@@ -406,7 +406,7 @@ z3_status z3_model_step_clipped(const z3_unit *units, const z3_clip_unit *clips,
  * A token may be left out: then its loss and lse are 0, nothing of its row of
  * hidden, whatever it holds, reaches any result but its own, and its row of
  * d_hidden is 0 (where the weight is finite).  Over the tokens that count
- *   total[0] = sum_t w_t loss[t],  total[1] = sum_t w_t   (summed in binary64)
+ *   total[0] = sum_t w_t loss[t],  total[1] = sum_t w_t  (as pairs of binary32)
  * with w the token's weight, 1 where weights is NULL.  A weight of 0 keeps the
  * token's loss, and takes it out of total and of the gradients.  The gradients
  * are those of scale * total[0] / total[1] where total is given (0 where

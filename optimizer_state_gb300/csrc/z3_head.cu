@@ -129,24 +129,44 @@ __device__ __forceinline__ float pick(const float (&v)[32], uint32_t j) {
 }
 
 // The entries of a token's list (or its target) among some columns of a
-// tile: the column of the next one, and of the one after it, so that no
-// load is waited for where an entry is met.
-template <bool LIST>
+// tile, in turn.  The next four are held, so that hardly any load is waited for
+// where an entry is met (with one, 501 lists of 200 over 32003 words took 59
+// us to turn into dz, 44 with four).
+template <bool LIST, bool Q>
 struct Walk {
     static constexpr int kNone = 0x7fffffff;
-    int next = kNone, after = kNone;
-    int at = 0, end = 0;
-    const int32_t *index = nullptr;
-    int word0 = 0;
+    static constexpr int kHeld = LIST ? 4 : 1;
+    int column[kHeld];
+    float share[kHeld];  // q
+    int at, end, word0;
+    const int32_t *index;
+    const float *q;
 
-    __device__ __forceinline__ void load_after() {
-        after = LIST && at + 1 < end ? index[at + 1] - word0 : kNone;
+    __device__ __forceinline__ Walk() : at(0), end(0), word0(0), index(nullptr), q(nullptr) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            column[i] = kNone;
+            share[i] = 1.0f;
+        }
+    }
+    __device__ __forceinline__ int next() const { return column[0]; }
+    __device__ __forceinline__ void load(int i) {
+        const bool there = at + i < end;
+        column[i] = there ? index[at + i] - word0 : kNone;
+        if constexpr (Q)
+            if (there) share[i] = q[at + i];
     }
     __device__ __forceinline__ void advance() {
-        next = after;
+#pragma unroll
+        for (int i = 0; i + 1 < kHeld; ++i) {
+            column[i] = column[i + 1];
+            share[i] = share[i + 1];
+        }
         if constexpr (LIST) {
             ++at;
-            load_after();
+            load(kHeld - 1);
+        } else {
+            column[0] = kNone;
         }
     }
 };
@@ -164,19 +184,6 @@ __device__ __forceinline__ void store_box(const Job &jb, uint32_t stage, int lan
 __device__ __forceinline__ void await_box(int lane) {
     if (lane == 0) tma_wait_read();
     __syncwarp();
-}
-
-// 32 columns of this thread's row as bf16, `i` columns into the warp's: every
-// second time the 64 go out.
-__device__ __forceinline__ void store_bf16(const Job &jb, uint32_t stage, int lane, int i,
-                                           const uint32_t (&w)[16], int col0, int64_t row) {
-    const int first = i / 32 % 2 * 4;  // 16-byte chunk of the row
-    if (first == 0) await_box(lane);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        st_shared(stage + lane * 128 + (((first + j) ^ (lane & 7)) << 4), w[4 * j], w[4 * j + 1],
-                  w[4 * j + 2], w[4 * j + 3]);
-    if (first == 4) store_box(jb, stage, lane, col0 + i - 32, row, 0);
 }
 
 // D tile by tile: 128 x CG rows by BN columns.  One thread feeds TMA, one issues
@@ -333,8 +340,27 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         const int quad = warp % 4;  // its 32 lanes of tensor memory
         const int half = (warp - 4) / 4;
         constexpr int kPer = BN / 2 < 32 ? 32 : BN / 2;  // columns of a warp
+        constexpr int kW = SWAP ? 32 : 64;               // ... which it takes at a time
         const int c0 = half * kPer;
         const uint32_t stage = staging + (warp - 4) * kStaging;
+        // what a token asks for: its target, its factor and lse
+        struct Ask {
+            int64_t word;
+            float2 rw;
+        };
+        [[maybe_unused]] auto ask = [&](int64_t row) {
+            Ask x{-1, make_float2(0.0f, 0.0f)};
+            if (row >= jb.rows) return x;
+            if constexpr (!LIST)
+                x.word = KIND == kStats ? load_index(p.targets, p.target_bytes, row)
+                                        : (int64_t)p.words[row];
+            if constexpr (KIND == kDz) x.rw = p.row[row];
+            return x;
+        };
+        [[maybe_unused]] Ask mine[2];
+        if constexpr (SWAP && KIND != kOut)  // the same tokens in every tile
+            for (int i = 0; i < 2; ++i)
+                if (32 * i < kPer) mine[i] = ask(c0 + 32 * i + lane);
         int done = 0;
         bool ok = true;
         for (int item = group; item < items; item += groups, ++done) {
@@ -351,32 +377,29 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             const int per = KIND == kOut && !SWAP ? max(0, min(kPer, (cols + 31) / 32 * 32)) : kPer;
             int64_t row = row0 + lane;
             bool live = row < jb.rows;
-            [[maybe_unused]] Walk<LIST> walk;
-            [[maybe_unused]] float2 rw = make_float2(0.0f, 0.0f);
-            // what the row asks of these words
-            [[maybe_unused]] auto begin_row = [&] {
-                walk = Walk<LIST>{};
-                rw = make_float2(0.0f, 0.0f);
+            [[maybe_unused]] Walk<LIST, LIST && KIND == kDz> walk;
+            [[maybe_unused]] float2 rw;
+            [[maybe_unused]] auto begin_row = [&](const Ask &x) {
+                walk = {};
+                rw = x.rw;
                 if (!live || cols <= 0) return;
                 if constexpr (LIST) {
                     const uint16_t *f = p.first + row * p.first_pitch;
                     walk.index = p.index + row * p.k;
+                    walk.q = p.q + row * p.k;
                     walk.word0 = p.word0 + col0;
                     walk.at = f[walk.word0 / kGrain];
                     walk.end = f[(walk.word0 + cols - 1) / kGrain + 1];
-                    if (walk.at < walk.end) walk.next = walk.index[walk.at] - walk.word0;
-                    walk.load_after();
+#pragma unroll
+                    for (int i = 0; i < walk.kHeld; ++i) walk.load(i);
                     if constexpr (SWAP)  // a quarter may begin within a grain
-                        while (walk.next < 0) walk.advance();
+                        while (walk.next() < 0) walk.advance();
                 } else {
-                    const int64_t w = KIND == kStats ? load_index(p.targets, p.target_bytes, row)
-                                                     : (int64_t)p.words[row];
-                    const int64_t c = w - p.word0 - col0;
-                    if (w >= 0 && c >= 0 && c < cols) walk.next = (int)c;
+                    const int64_t c = x.word - p.word0 - col0;
+                    if (x.word >= 0 && c >= 0 && c < cols) walk.column[0] = (int)c;
                 }
-                if constexpr (KIND == kDz) rw = p.row[row];
             };
-            if constexpr (KIND != kOut && !SWAP) begin_row();
+            if constexpr (KIND != kOut && !SWAP) begin_row(ask(row));
             if (ok) ok = mbar_wait(tfull(buf), (done >> 1) & 1);
             tmem_fence_after();
             const uint32_t d = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + c0;
@@ -388,14 +411,25 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             };
             if (c0 >= BN || per == 0) release();
 #pragma unroll 1
-            for (int i = 0; i < per && c0 + i < BN; i += 32) {
-                uint32_t bits[32];
-                tmem_load32(d + i, bits);
-                tmem_wait_load();
-                if (i + 32 == per) release();
-                float v[32];
+            for (int i = 0; i < per && c0 + i < BN; i += kW) {
+                float v[kW / 32][32];
+                {
+                    uint32_t bits[kW / 32][32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = ok ? __uint_as_float(bits[j]) : NAN;
+                    for (int h = 0; h < kW / 32; ++h) tmem_load32(d + i + 32 * h, bits[h]);
+                    tmem_wait_load();
+                    if (i + kW >= per) release();
+#pragma unroll
+                    for (int h = 0; h < kW / 32; ++h)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[h][j] = __uint_as_float(bits[h][j]);
+                }
+                if (!ok) {
+#pragma unroll
+                    for (int h = 0; h < kW / 32; ++h)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[h][j] = NAN;
+                }
                 if constexpr (SWAP) {
                     // [token][word], each row turned by its number: no two lanes meet
                     // in a bank
@@ -403,44 +437,51 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                     auto at = [&](int r, int c) { return stage + (r * 32 + ((c + r) & 31)) * 4; };
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(j, lane)), "f"(v[j])
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(j, lane)), "f"(v[0][j])
                                      : "memory");
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(at(lane, j))
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0][j]) : "r"(at(lane, j))
                                      : "memory");
                     __syncwarp();
                     row = row0 + i + lane;
                     live = row < jb.rows;
-                    if constexpr (KIND != kOut) begin_row();
+                    if constexpr (KIND != kOut) begin_row(i == 0 ? mine[0] : mine[1]);
                     top = -INFINITY;
                     sum = 0.0f;
                 }
-                const int c = SWAP ? 0 : i;  // column of v[0] from col0 on
+                const int c = SWAP ? 0 : i;  // column of v[0][0] from col0 on
+                const int reach = SWAP ? min(32, cols) : 32;
                 if constexpr (KIND == kStats) {
-                    while (walk.next < c + (SWAP ? min(32, cols) : 32)) {
-                        p.z[LIST ? row * p.k + walk.at : row] = pick(v, (uint32_t)(walk.next - c));
-                        walk.advance();
-                    }
-                    if (c + 32 > cols) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = c + j < cols ? v[j] : -INFINITY;
+                    for (int h = 0; h < kW / 32; ++h)
+                        while (walk.next() < c + 32 * h + reach) {
+                            p.z[LIST ? row * p.k + walk.at : row] =
+                                pick(v[h], (uint32_t)(walk.next() - c - 32 * h));
+                            walk.advance();
+                        }
+                    if (c + kW > cols) {
+#pragma unroll
+                        for (int h = 0; h < kW / 32; ++h)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                v[h][j] = c + 32 * h + j < cols ? v[h][j] : -INFINITY;
                     }
                     // four chains of each; exp(z / temperature) = 2^(beta z)
                     float m[4], s[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) m[j] = v[j];
+                    for (int j = 0; j < 4; ++j) m[j] = v[0][j];
 #pragma unroll
-                    for (int j = 4; j < 32; ++j) m[j % 4] = fmaxf(m[j % 4], v[j]);
+                    for (int j = 4; j < kW; ++j) m[j % 4] = fmaxf(m[j % 4], v[j / 32][j % 32]);
                     const float new_top =
                         fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * p.beta);
                     const float shift = new_top == -INFINITY ? 0.0f : -new_top;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] = exp2_fast(__fmaf_rn(v[j], p.beta, shift));
+                    for (int j = 0; j < 4; ++j) s[j] = exp2_fast(__fmaf_rn(v[0][j], p.beta, shift));
 #pragma unroll
-                    for (int j = 4; j < 32; ++j)
-                        s[j % 4] += exp2_fast(__fmaf_rn(v[j], p.beta, shift));
+                    for (int j = 4; j < kW; ++j)
+                        s[j % 4] += exp2_fast(__fmaf_rn(v[j / 32][j % 32], p.beta, shift));
                     sum = __fmaf_rn(sum, exp2_fast(top + shift), (s[0] + s[1]) + (s[2] + s[3]));
                     top = new_top;
                     if constexpr (SWAP)
@@ -448,22 +489,24 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 } else if constexpr (KIND == kDz) {
                     const bool none = rw.x == 0.0f;  // also where the logits are not finite
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = exp2_fast(__fmaf_rn(v[j], p.beta, -rw.y)) * rw.x;
-                    while (walk.next < c + (SWAP ? min(32, cols) : 32)) {
-                        float q = rw.x;
-                        if constexpr (LIST) q = q * p.q[row * p.k + walk.at];
-                        const int hit = walk.next - c;
+                    for (int h = 0; h < kW / 32; ++h) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (j == hit) v[j] -= q;
-                        walk.advance();
+                            v[h][j] = exp2_fast(__fmaf_rn(v[h][j], p.beta, -rw.y)) * rw.x;
+                        while (walk.next() < c + 32 * h + reach) {
+                            const float q = rw.x * walk.share[0];
+                            const int hit = walk.next() - c - 32 * h;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j == hit) v[h][j] -= q;
+                            walk.advance();
+                        }
                     }
                     // rounded once to bf16, the type of the products' operands
-                    uint32_t w[16];
+                    uint32_t w[kW / 2];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        w[j] = none ? 0u : pack_bf16x2(v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < kW / 2; ++j)
+                        w[j] = none ? 0u : pack_bf16x2(v[j / 16][2 * j % 32], v[j / 16][2 * j % 32 + 1]);
                     if constexpr (SWAP) {
                         uint16_t *o = p.dz + row * p.dz_pitch + col0;
 #pragma unroll
@@ -472,21 +515,33 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                                 *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
                                     w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                     } else {
-                        store_bf16(jb, stage, lane, i, w, col0, row0);
+                        await_box(lane);
+#pragma unroll
+                        for (int j = 0; j < kW / 8; ++j)
+                            st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[4 * j],
+                                      w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                        store_box(jb, stage, lane, col0 + i, row0, 0);
                     }
                 } else if (SWAP || jb.out_f32) {
-                    if constexpr (!SWAP) await_box(lane);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
-                                  __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                  __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-                    store_box(jb, stage, lane, col0 + c, SWAP ? row0 + i : row0, t.split);
-                } else {
-                    uint32_t w[16];
+                    for (int h = 0; h < kW / 32; ++h) {
+                        if (h > 0 && i + 32 >= per) break;
+                        if constexpr (!SWAP) await_box(lane);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-                    if (i % 64 == 0 && i + 64 > bn - c0 && col0 + i + 32 < jb.cols) {
+                        for (int j = 0; j < 8; ++j)
+                            st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
+                                      __float_as_uint(v[h][4 * j]), __float_as_uint(v[h][4 * j + 1]),
+                                      __float_as_uint(v[h][4 * j + 2]),
+                                      __float_as_uint(v[h][4 * j + 3]));
+                        store_box(jb, stage, lane, col0 + c + 32 * h, SWAP ? row0 + i : row0,
+                                  t.split);
+                    }
+                } else if constexpr (!SWAP) {
+                    uint32_t w[kW / 2];
+#pragma unroll
+                    for (int j = 0; j < kW / 2; ++j)
+                        w[j] = pack_bf16x2(v[j / 16][2 * j % 32], v[j / 16][2 * j % 32 + 1]);
+                    if (i + 32 == bn - c0 && col0 + i + 32 < jb.cols) {
                         // half a box at the tile's end, the next tile's columns behind it
                         uint16_t *o = jb.out_at + row * jb.out_pitch + col0 + i;
 #pragma unroll
@@ -495,9 +550,12 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                                 *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
                                     w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                     } else {
-                        store_bf16(jb, stage, lane, i, w, col0, row0);
-                        if (i % 64 == 0 && i + 32 == per)  // the box's other half is clipped
-                            store_box(jb, stage, lane, col0 + i, row0, 0);
+                        await_box(lane);
+#pragma unroll
+                        for (int j = 0; j < kW / 8; ++j)
+                            st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[4 * j],
+                                      w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                        store_box(jb, stage, lane, col0 + i, row0, 0);
                     }
                 }
             }
@@ -646,7 +704,7 @@ struct JoinArgs {
     RowArgs row;
     const float2 *part;
     const float *z;
-    double2 *sums;         // of each block
+    float4 *sums;          // of each block
     unsigned *done;        // 0 at the start
     float *loss, *lse, *total;
 };
@@ -659,19 +717,29 @@ __device__ __forceinline__ float2 join2(float2 x, float2 y) {
     return make_float2(m, __fmaf_rn(x.y, exp2_fast(x.x - s), y.y * exp2_fast(y.x - s)));
 }
 
-// The sum of the block's values, in a fixed order; in thread 0.
-__device__ __forceinline__ double2 block_sum(double2 v, double2 *warps) {
-    for (int o = 16; o > 0; o /= 2) {
-        v.x += __shfl_down_sync(~0u, v.x, o);
-        v.y += __shfl_down_sync(~0u, v.y, o);
+// A sum as a pair of binary32 (Knuth's two-sum): {sum, what its roundings lost}.
+// Binary64 additions are too few a clock here: with them the join of 8192
+// tokens took 19 us.
+__device__ __forceinline__ float2 pair_add(float2 x, float2 y) {
+    const float s = __fadd_rn(x.x, y.x), b = __fsub_rn(s, x.x);
+    const float e = __fadd_rn(__fsub_rn(x.x, __fsub_rn(s, b)), __fsub_rn(y.x, b));
+    // beyond binary32, or not a number, the sum has no remainder
+    return make_float2(s, isfinite(s) ? __fadd_rn(e, __fadd_rn(x.y, y.y)) : 0.0f);
+}
+
+// Two sums over groups of 2 FROM lanes, in a fixed order.
+template <int FROM>
+__device__ __forceinline__ float4 pairs_over_lanes(float4 v) {
+#pragma unroll
+    for (int o = FROM; o > 0; o /= 2) {
+        const float2 x = pair_add(make_float2(v.x, v.y),
+                                  make_float2(__shfl_xor_sync(~0u, v.x, o),
+                                              __shfl_xor_sync(~0u, v.y, o)));
+        const float2 y = pair_add(make_float2(v.z, v.w),
+                                  make_float2(__shfl_xor_sync(~0u, v.z, o),
+                                              __shfl_xor_sync(~0u, v.w, o)));
+        v = make_float4(x.x, x.y, y.x, y.y);
     }
-    if (threadIdx.x % 32 == 0) warps[threadIdx.x / 32] = v;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        for (int w = 1; w < kJoinThreads / 32; ++w) {
-            v.x += warps[w].x;
-            v.y += warps[w].y;
-        }
     return v;
 }
 
@@ -685,12 +753,21 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
     constexpr int kWarps = kJoinThreads / 32;
     __shared__ float2 joined[kWarps][TOK];
     __shared__ float lists[kWarps][TOK];
-    __shared__ double2 warps[2][kWarps];
+    __shared__ float4 warps[kWarps];
     __shared__ bool last;
     pdl_enter();
     const int tok = threadIdx.x % TOK, slice = threadIdx.x / TOK, warp = threadIdx.x / 32;
     const int64_t t = (int64_t)blockIdx.x * TOK + tok;
     const bool live = t < a.row.tokens;
+    // what the loss needs beside the sums, asked for before them
+    int64_t word = 0;
+    Row state = kLeftOut;
+    float weight = 1.0f, z = 0.0f;
+    if (live) {
+        state = state_of(a.row, t, &word);
+        if (a.row.weights) weight = a.row.weights[t];
+        if (a.row.k == 0) z = a.z[t];
+    }
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (live) {
         for (int n = slice; n < a.row.parts; n += 8 * kSlices) {
@@ -713,12 +790,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
                                      __shfl_xor_sync(~0u, acc.y, o)));
     if (threadIdx.x % 32 < TOK) joined[warp][tok] = acc;
     __syncthreads();
-    acc = joined[0][tok];
-    for (int w = 1; w < kWarps; ++w) acc = join2(acc, joined[w][tok]);
+    if (a.row.k > 0 || warp == 0) {
+        acc = joined[0][tok];
+        for (int w = 1; w < kWarps; ++w) acc = join2(acc, joined[w][tok]);
+    }
     // a sum that is not a number stays one through the logarithm
     const float lse = (acc.x + log2f(acc.y)) * kLn2;
-    int64_t word = 0;
-    const Row state = live ? state_of(a.row, t, &word) : kLeftOut;
     if (a.row.k > 0) {
         float part = 0.0f;
         const float inv = __fdiv_rn(1.0f, a.row.temperature);
@@ -735,44 +812,59 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
         if (threadIdx.x % 32 < TOK) lists[warp][tok] = part;
         __syncthreads();
     }
-    double2 mine = make_double2(0.0, 0.0);
-    if (slice == 0 && live) {
-        float loss = 0.0f;
-        if (state == kBad) {
-            loss = NAN;
-        } else if (state == kCounts && a.row.k > 0) {
-            for (int w = 0; w < kWarps; ++w) loss += lists[w][tok];
-            loss *= a.row.temperature * a.row.temperature;
-        } else if (state == kCounts) {
-            loss = lse - a.z[t];
+    if (warp == 0) {
+        float4 mine = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (slice == 0 && live) {
+            float loss = 0.0f;
+            if (state == kBad) {
+                loss = NAN;
+            } else if (state == kCounts && a.row.k > 0) {
+                for (int w = 0; w < kWarps; ++w) loss += lists[w][tok];
+                loss *= a.row.temperature * a.row.temperature;
+            } else if (state == kCounts) {
+                loss = lse - z;
+            }
+            a.loss[t] = loss;
+            a.lse[t] = state == kLeftOut ? 0.0f : lse;
+            if (state != kLeftOut && weight != 0.0f) {
+                const float x = weight * loss;
+                mine = make_float4(x, isfinite(x) ? __fmaf_rn(weight, loss, -x) : 0.0f, weight,
+                                   0.0f);
+            }
         }
-        a.loss[t] = loss;
-        a.lse[t] = state == kLeftOut ? 0.0f : lse;
-        const float w = state == kLeftOut ? 0.0f : a.row.weights ? a.row.weights[t] : 1.0f;
-        if (w != 0.0f) mine = make_double2((double)w * (double)loss, (double)w);
-    }
-    mine = block_sum(mine, warps[0]);
-    if (gridDim.x > 1) {
+        mine = pairs_over_lanes<TOK / 2>(mine);
         if (threadIdx.x == 0) {
-            a.sums[blockIdx.x] = mine;
-            __threadfence();
-            last = atomicAdd(a.done, 1u) == gridDim.x - 1;
-            __threadfence();
+            if (gridDim.x == 1) {
+                a.total[0] = mine.x + mine.y;
+                a.total[1] = mine.z + mine.w;
+            } else {
+                a.sums[blockIdx.x] = mine;
+                __threadfence();
+                last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+                __threadfence();
+            }
         }
-        __syncthreads();
-        if (!last) return;
-        mine = make_double2(0.0, 0.0);
-        for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) {
-            const double2 x = __ldcg(a.sums + i);  // from L2, where the other blocks left them
-            mine.x += x.x;
-            mine.y += x.y;
-        }
-        mine = block_sum(mine, warps[1]);
     }
-    if (threadIdx.x == 0) {
-        a.total[0] = (float)mine.x;
-        a.total[1] = (float)mine.y;
+    if (gridDim.x == 1) return;
+    __syncthreads();
+    if (!last) return;
+    float2 x = make_float2(0.0f, 0.0f), y = x;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) {
+        const float4 v = __ldcg(a.sums + i);  // from L2, where the other blocks left them
+        x = pair_add(x, make_float2(v.x, v.y));
+        y = pair_add(y, make_float2(v.z, v.w));
     }
+    const float4 v = pairs_over_lanes<16>(make_float4(x.x, x.y, y.x, y.y));
+    if (threadIdx.x % 32 == 0) warps[warp] = v;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    x = y = make_float2(0.0f, 0.0f);
+    for (int w = 0; w < kWarps; ++w) {
+        x = pair_add(x, make_float2(warps[w].x, warps[w].y));
+        y = pair_add(y, make_float2(warps[w].z, warps[w].w));
+    }
+    a.total[0] = x.x + x.y;
+    a.total[1] = y.x + y.y;
 }
 
 struct FactorArgs {
@@ -1160,7 +1252,7 @@ cudaError_t launch_head_forward(const HeadArgs &a, cudaStream_t s) {
     j.row = r;
     j.part = m.part;
     j.z = m.z;
-    j.sums = reinterpret_cast<double2 *>(a.ws + p.sums);
+    j.sums = reinterpret_cast<float4 *>(a.ws + p.sums);
     j.done = m.done;
     j.loss = a.loss;
     j.lse = a.lse;

@@ -38,7 +38,7 @@ struct HeadPlan {
     // byte offsets into the workspace
     int64_t part;        // float2 [parts][tokens]: maximum, sum of exponentials
     int64_t z;           // float [tokens][max(k, 1)]: logits of the target or the list
-    int64_t sums;        // double2 [blocks]: the join's
+    int64_t sums;        // float4 [blocks]: the join's
     int64_t done;        // int: joined blocks
     int64_t state;       // int8 [tokens]: Row
     int64_t index, q;    // int32, float [tokens][k]: the list by ascending word
