@@ -202,9 +202,8 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     constexpr int S = stages<BN, CG>();
     constexpr int kA = 128 * kBK * 2;
     constexpr int kStage = stage_bytes<BN, CG>();
-    constexpr int kBRows = BN / CG;  // of b that this CTA loads
     constexpr int kCols = 2 * BN;    // of tensor memory: two tiles
-    const int bn = KIND == kOut && !SWAP ? p.job.cut.bn : BN;  // columns of a tile
+    const int bn = SWAP ? BN : p.job.cut.bn;  // columns of a tile
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
     const uint32_t staging = base + S * kStage;
@@ -252,7 +251,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         // what their sums are is not looked at
         const int b_boxes = BMN ? (bn / CG + 63) / 64 : 0;  // of 64 columns
         const uint32_t bytes = CG * (uint32_t)(jb.cut.tile_m * 128 +
-                                               (BMN ? b_boxes * 64 : kBRows) * kBK * 2);
+                                               (BMN ? b_boxes * 64 : bn / CG) * kBK * 2);
         for (int item = group; ok && item < items; item += groups) {
             const Tile t = tile_of(jb, item);
             const int m0 = jb.a_m + t.m * (jb.cut.tile_m * CG) + (int)rank * 128;
@@ -374,7 +373,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             const int cols =  // valid ones among them
                 (int)min((int64_t)(SWAP ? min(32, jb.cut.tile_m - quad * 32) : min(kPer, bn - c0)),
                          jb.cols - col0);
-            const int per = KIND == kOut && !SWAP ? max(0, min(kPer, (cols + 31) / 32 * 32)) : kPer;
+            const int per = SWAP ? kPer : max(0, min(kPer, (cols + 31) / 32 * 32));
             int64_t row = row0 + lane;
             bool live = row < jb.rows;
             [[maybe_unused]] Walk<LIST, LIST && KIND == kDz> walk;
@@ -392,8 +391,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                     walk.end = f[(walk.word0 + cols - 1) / kGrain + 1];
 #pragma unroll
                     for (int i = 0; i < walk.kHeld; ++i) walk.load(i);
-                    if constexpr (SWAP)  // a quarter may begin within a grain
-                        while (walk.next() < 0) walk.advance();
+                    while (walk.next() < 0) walk.advance();  // the grain began before
                 } else {
                     const int64_t c = x.word - p.word0 - col0;
                     if (x.word >= 0 && c >= 0 && c < cols) walk.column[0] = (int)c;
@@ -408,6 +406,26 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_leader(tempty(buf)));
+            };
+            // this row's 64 columns from i on as bf16
+            [[maybe_unused]] auto put = [&](int i, const uint32_t (&w)[kW / 2], uint16_t *out,
+                                            int64_t pitch) {
+                if (i + 32 == bn - c0 && col0 + i + 32 < jb.cols) {
+                    // half a box at the tile's end, the next tile's columns behind it
+                    uint16_t *o = out + row * pitch + col0 + i;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (live)
+                            *reinterpret_cast<uint4 *>(o + 8 * j) =
+                                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                } else {
+                    await_box(lane);
+#pragma unroll
+                    for (int j = 0; j < kW / 8; ++j)
+                        st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[4 * j],
+                                  w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    store_box(jb, stage, lane, col0 + i, row0, 0);
+                }
             };
             if (c0 >= BN || per == 0) release();
 #pragma unroll 1
@@ -452,11 +470,10 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                     sum = 0.0f;
                 }
                 const int c = SWAP ? 0 : i;  // column of v[0][0] from col0 on
-                const int reach = SWAP ? min(32, cols) : 32;
                 if constexpr (KIND == kStats) {
 #pragma unroll
                     for (int h = 0; h < kW / 32; ++h)
-                        while (walk.next() < c + 32 * h + reach) {
+                        while (walk.next() < min(c + 32 * h + 32, cols)) {
                             p.z[LIST ? row * p.k + walk.at : row] =
                                 pick(v[h], (uint32_t)(walk.next() - c - 32 * h));
                             walk.advance();
@@ -493,7 +510,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             v[h][j] = exp2_fast(__fmaf_rn(v[h][j], p.beta, -rw.y)) * rw.x;
-                        while (walk.next() < c + 32 * h + reach) {
+                        while (walk.next() < min(c + 32 * h + 32, cols)) {
                             const float q = rw.x * walk.share[0];
                             const int hit = walk.next() - c - 32 * h;
 #pragma unroll
@@ -515,12 +532,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                                 *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
                                     w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                     } else {
-                        await_box(lane);
-#pragma unroll
-                        for (int j = 0; j < kW / 8; ++j)
-                            st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[4 * j],
-                                      w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                        store_box(jb, stage, lane, col0 + i, row0, 0);
+                        put(i, w, p.dz, p.dz_pitch);
                     }
                 } else if (SWAP || jb.out_f32) {
 #pragma unroll
@@ -541,22 +553,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                     for (int j = 0; j < kW / 2; ++j)
                         w[j] = pack_bf16x2(v[j / 16][2 * j % 32], v[j / 16][2 * j % 32 + 1]);
-                    if (i + 32 == bn - c0 && col0 + i + 32 < jb.cols) {
-                        // half a box at the tile's end, the next tile's columns behind it
-                        uint16_t *o = jb.out_at + row * jb.out_pitch + col0 + i;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (live)
-                                *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
-                                    w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                    } else {
-                        await_box(lane);
-#pragma unroll
-                        for (int j = 0; j < kW / 8; ++j)
-                            st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[4 * j],
-                                      w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                        store_box(jb, stage, lane, col0 + i, row0, 0);
-                    }
+                    put(i, w, jb.out_at, jb.out_pitch);
                 }
             }
             if constexpr (KIND == kStats && !SWAP)
@@ -1053,7 +1050,7 @@ cudaError_t launch_d_weight(const MmaArgs &p, cudaStream_t s) {
 
 constexpr int64_t kFew = 128;  // tokens that SWAP takes
 
-// The logits' tiles.  Few tokens: the weight's rows are cut so that every SM has
+// The logits' tiles, for all words or a piece of them.  Few tokens: the weight's rows are cut so that every SM has
 // the same number of tiles, none more than 128 rows.
 Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
     Cut c{};
@@ -1068,11 +1065,20 @@ Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
         c.m_tiles = (int32_t)ceil_div(words, c.tile_m);
         c.n_tiles = 1;
     } else {
+        // columns of a tile: what leaves the last wave of tiles fullest, a tile
+        // costing as much as 24 columns beside its own
         c.cg = 2;
-        c.bn = 256;
         c.tile_m = 128;
         c.m_tiles = (int32_t)ceil_div(tokens, 256);
-        c.n_tiles = (int32_t)ceil_div(words, 256);
+        int64_t best = 0;
+        for (int bn = 256; bn >= 128; bn -= 32) {
+            const int64_t waves = ceil_div(c.m_tiles * ceil_div(words, bn), kHeadSMs / 2);
+            if (best == 0 || waves * (bn + 24) < best) {
+                best = waves * (bn + 24);
+                c.bn = bn;
+            }
+        }
+        c.n_tiles = (int32_t)ceil_div(words, c.bn);
     }
     return c;
 }
@@ -1173,7 +1179,8 @@ bool logits_job(MmaArgs *m, const HeadArgs &a, const Cut &cut, int64_t w0, int64
     CUtensorMap *hidden = cut.swap ? &jb.b : &jb.a, *weight = cut.swap ? &jb.a : &jb.b;
     (cut.swap ? jb.a_m : jb.b_n) = (int32_t)w0;
     return make_map(hidden, a.hidden, p.dim, p.tokens, a.hidden_stride, cut.swap ? cut.bn : 128) &&
-           make_map(weight, a.weight, p.dim, p.vocab, a.weight_stride, cut.tile_m);
+           make_map(weight, a.weight, p.dim, p.vocab, a.weight_stride,
+                    cut.swap ? cut.tile_m : cut.bn / 2);
 }
 
 }  // namespace
@@ -1293,12 +1300,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
         const int64_t w0 = i * p.piece, words = std::min(p.piece, p.vocab - w0);
         const bool last = i + 1 == p.pieces;
         MmaArgs m{};
-        Cut cut = p.logits;
-        if (cut.swap)
-            cut.m_tiles = (int32_t)ceil_div(words, cut.tile_m);
-        else
-            cut.n_tiles = (int32_t)ceil_div(words, cut.bn);
-        if (!logits_job(&m, a, cut, w0, words) ||
+        if (!logits_job(&m, a, cut_logits(p.tokens, words, p.dim), w0, words) ||
             !make_out(&m.job.out, dz, false, words, p.tokens, p.piece, 1))
             return cudaErrorInvalidValue;
         m.row = f.factor;

@@ -71,6 +71,96 @@ class Unit:
         return st["hbm_step_layer"] - (st["hbm_allgather"] if self.resident is not None else 0)
 
 
+class Head:
+    """A model's loss over the vocabulary of one of its parameters, for all of
+    its logical ranks, with the gradients that a step begins from.
+
+    A call gathers the parameter's unit (a resident one is at hand), takes the
+    loss of every rank's tokens against the gathered copy in one forward pass,
+    and each rank's gradients: that of the weight into the parameter's part of
+    the rank's row of the unit's gradients, that of the hidden states into
+    `d_hidden`.  They are the gradients of the mean over all ranks' tokens that
+    count, times the number of ranks: the step's reduction divides by it."""
+
+    def __init__(self, model: Model, tokens: int, unit: int = 0, param: int = 0, k: int = 0):
+        self.model, self.unit, self.k = model, model.units[unit], k
+        u = self.unit
+        shape = u.w.shapes[param]
+        if len(shape) != 2:
+            raise ValueError(f"parameter {param} of unit {unit} is {list(shape)}, not "
+                             "[vocab, dim]")
+        self.vocab, self.dim = shape
+        self.tokens, self.ranks = tokens, u.w.n_ranks
+        first = u.L.full_off[param]
+        self._part = slice(first, first + self.vocab * self.dim)
+        rows, dev = (self.ranks, tokens), model.dev
+        self._made_on = torch.cuda.current_stream()
+        self.loss = torch.empty(rows, dtype=torch.float32, device=dev)
+        self.lse = torch.empty(rows, dtype=torch.float32, device=dev)
+        self.total = torch.empty(2, dtype=torch.float32, device=dev)
+        self.d_hidden = torch.empty((*rows, self.dim), dtype=torch.bfloat16, device=dev)
+        # the forward pass over all ranks, the gradients rank by rank
+        need = [z3.head_workspace(n, self.dim, self.vocab, k, grads, dev)
+                for n, grads in ((self.ranks * tokens, False), (tokens, True))]
+        self._workspace = max(need, key=lambda x: x.numel())
+
+    def __call__(self, hidden: torch.Tensor, targets: torch.Tensor | None = None, *,
+                 teacher: torch.Tensor | None = None, index: torch.Tensor | None = None,
+                 temperature: float = 1.0, weights: torch.Tensor | None = None,
+                 scale: float = 1.0, grads: bool = True, stream=None) -> torch.Tensor:
+        """hidden: bf16 [ranks, tokens, dim]; either targets [ranks, tokens], or
+        a teacher's logits [ranks, tokens, k] with their words, index; weights:
+        fp32 [ranks, tokens] or None.  Leaves loss, lse and total, and unless
+        `grads` is false the gradients of scale times the mean; returns total,
+        {sum of weighted losses, sum of weights} over all ranks."""
+        if (targets is None) == (teacher is None) or (teacher is None) != (index is None):
+            raise ValueError("give targets, or teacher and index")
+        rows = (self.ranks, self.tokens)
+        for x, name, tail in ((hidden, "hidden", (self.dim,)), (targets, "targets", ()),
+                              (teacher, "teacher", (self.k,)), (index, "index", (self.k,)),
+                              (weights, "weights", ())):
+            if x is not None and tuple(x.shape) != rows + tail:
+                raise ValueError(f"{name}: needs shape {list(rows + tail)}, has {list(x.shape)}")
+            if x is not None and not x.is_contiguous():
+                raise ValueError(f"{name}: must be contiguous")
+        self._await(stream)
+        u = self.unit
+        full = u.resident
+        if full is None:
+            full = self.model.full
+            z3.z3_allgather(u.L, u.shards, full, stream=stream)
+        weight = full[self._part].view(self.vocab, self.dim)
+        if teacher is None:
+            forward, backward, heads = z3.z3_xent, z3.z3_xent_grad, (targets,)
+            extra = ()
+        else:
+            forward, backward, heads = z3.z3_distill, z3.z3_distill_grad, (teacher, index)
+            extra = (temperature,)
+        forward(hidden.view(-1, self.dim), weight, *[x.view(-1, *x.shape[2:]) for x in heads],
+                *extra, self.loss.view(-1), self.lse.view(-1), self.total, self._workspace,
+                weights=None if weights is None else weights.view(-1), stream=stream)
+        for r in range(self.ranks if grads else 0):
+            backward(hidden[r], weight, *[x[r] for x in heads], *extra, self.lse[r], self.total,
+                     scale * self.ranks, self.d_hidden[r],
+                     u.grads[r, self._part].view(self.vocab, self.dim), self._workspace,
+                     weights=None if weights is None else weights[r], stream=stream)
+        return self.total
+
+    def _await(self, stream):
+        """The first call on another stream than the one that the buffers were
+        allocated on waits for that one; a captured call, which cannot wait for
+        what is outside its capture, leaves it to the next."""
+        if self._made_on is None:
+            return
+        s = _torch_stream(stream)
+        if s.cuda_stream != self._made_on.cuda_stream:
+            with torch.cuda.stream(s):
+                if torch.cuda.is_current_stream_capturing():
+                    return
+            s.wait_stream(self._made_on)
+        self._made_on = None
+
+
 class Model:
     """All units of a model plus the shared transient gathered buffer."""
 
@@ -93,6 +183,12 @@ class Model:
         """HBM bytes of a step that is not clipped; a clipped one moves 8 more
         per padded element (the fp32 gradient, stored and read back)."""
         return sum(u.step_bytes for u in self.units)
+
+    def head(self, tokens: int, unit: int = 0, param: int = 0, k: int = 0) -> Head:
+        """The loss of `tokens` tokens of every rank over the vocabulary of one
+        parameter, [vocab, dim] (an embedding's where the head is tied to it);
+        k: the length of a teacher's lists, where there is one."""
+        return Head(self, tokens, unit, param, k)
 
     def launches_per_step(self) -> int:
         """Kernel launches of a step that is not clipped."""
@@ -184,8 +280,11 @@ class Model:
             z3.z3_allgather(u.L, u.shards, u.resident, stream=stream)
 
     def step(self, hp: dict, stream=None, t: int | None = None, on_gather=None,
-             max_norm: float | None = None):
+             max_norm: float | None = None, loss=None):
         """One training step, scheduled by the library (z3_model_step).
+        `loss(stream)` is called where the backward pass begins, such as for a
+        Head's call: after the forward gathers of a step with hooks, and before
+        a step that the library schedules as a whole.
         With `max_norm` the gradients of all units are clipped to that global
         norm first (z3_model_step_clipped); `clip` then holds [norm, coef] on
         the device, coef NaN where the norm was not finite and the step was
@@ -201,12 +300,16 @@ class Model:
             self.t += 1
             t = self.t
         if on_gather is None:
+            if loss is not None:
+                loss(stream)
             self._library_step([self.full], hp, t, max_norm, stream)
             return
         for i, u in enumerate(self.units):            # forward
             if u.resident is None:
                 z3.z3_allgather(u.L, u.shards, self.full, stream=stream)
             on_gather("forward", i)
+        if loss is not None:
+            loss(stream)
         for i in range(len(self.units) - 1, -1, -1):    # backward, reverse order
             u = self.units[i]
             if u.resident is None:
@@ -249,11 +352,13 @@ class PrefetchModel(Model):
         self.gstream = torch.cuda.Stream(device=dev)
 
     def step(self, hp: dict, stream=None, t: int | None = None, on_gather=None,
-             max_norm: float | None = None):
+             max_norm: float | None = None, loss=None):
         if t is None:
             self.t += 1
             t = self.t
         if on_gather is None:
+            if loss is not None:
+                loss(stream)
             self._library_step(self.bufs, hp, t, max_norm, stream, self.gstream)
             return
         if self.depth != 1:
@@ -268,6 +373,9 @@ class PrefetchModel(Model):
                 z3.z3_allgather(u.L, u.shards, self.bufs[i % 2], stream=g.cuda_stream)
             with torch.cuda.stream(g):
                 on_gather("forward", i)
+        if loss is not None:
+            with torch.cuda.stream(g):
+                loss(g)
         order = list(range(n - 1, -1, -1))
         gathered = {}
 
