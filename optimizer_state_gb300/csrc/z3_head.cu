@@ -100,8 +100,10 @@ struct Tile {
     int m, n, split;
 };
 
-__device__ __forceinline__ Tile tile_of(const Job &jb, int item) {
-    const int tiles = jb.cut.m_tiles * jb.cut.n_tiles;
+template <int PAIRS>
+__device__ __forceinline__ Tile tile_of(const Job &jb, int item, int pair) {
+    const int m_tiles = (jb.cut.m_tiles + PAIRS - 1) / PAIRS;  // of a cluster
+    const int tiles = m_tiles * jb.cut.n_tiles;
     Tile t;
     t.split = item / tiles;
     int i = item - t.split * tiles;
@@ -109,14 +111,15 @@ __device__ __forceinline__ Tile tile_of(const Job &jb, int item) {
         t.m = i / jb.cut.n_tiles;
         t.n = i - t.m * jb.cut.n_tiles;
     } else {
-        constexpr int kGroup = 32;  // row tiles whose operand stays in L2
+        constexpr int kGroup = 32 / PAIRS;  // row tiles whose operand stays in L2
         const int per = kGroup * jb.cut.n_tiles;
         const int g = i / per;
-        const int rows = min(kGroup, jb.cut.m_tiles - g * kGroup);
+        const int rows = min(kGroup, m_tiles - g * kGroup);
         i -= g * per;
         t.n = i / rows;
         t.m = g * kGroup + i - t.n * rows;
     }
+    t.m = t.m * PAIRS + pair;
     return t;
 }
 
@@ -194,9 +197,13 @@ __device__ __forceinline__ void await_box(int lane) {
 // and N along tokens, so that the weight fills the tiles; a warp turns its 32
 // x 32 values over in shared memory, after which thread, row and columns mean
 // what they mean without SWAP.
+// PAIRS = 2: clusters of two CTA pairs, which take the same columns of two row
+// tiles.  Each pair loads half of b's tile for both, so that L2 is read for 48
+// bytes a clock and SM instead of 64; it gives about 50.  In exchange only 36
+// such clusters, 144 SMs, fit the GPU.
 // Every wait ends (mbar_wait); an epilogue whose tile did not come takes NaN for
 // its values.
-template <int CG, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
+template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 k_head_mma(const __grid_constant__ MmaArgs p) {
     constexpr int S = stages<BN, CG>();
@@ -214,17 +221,21 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     auto tempty = [&](int i) { return bars + 8 * (2 * S + 2 + i); };
     const uint32_t tmem_at = bars + 8 * (2 * S + 4);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t rank = CG == 1 ? 0 : cluster_rank();
-    const int group = blockIdx.x / CG, groups = gridDim.x / CG;
+    const uint32_t place = CG == 1 ? 0 : cluster_rank();  // in the cluster
+    const uint32_t rank = place % CG;                      // in the pair
+    const int pair = place / CG;
+    const uint32_t leader = place - rank;
+    const int group = blockIdx.x / (CG * PAIRS), groups = gridDim.x / (CG * PAIRS);
     const Job &jb = p.job;
-    const int items = jb.cut.m_tiles * jb.cut.n_tiles * jb.cut.splits;
+    const int items =
+        (jb.cut.m_tiles + PAIRS - 1) / PAIRS * jb.cut.n_tiles * jb.cut.splits;
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_map(&jb.a);
         tma_prefetch_map(&jb.b);
         for (int i = 0; i < S; ++i) {
             mbar_init(full(i), 1);
-            mbar_init(empty(i), 1);
+            mbar_init(empty(i), PAIRS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull(i), 1);
@@ -235,7 +246,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     if (warp == 2) tmem_alloc<CG>(tmem_at, kCols);
     __syncwarp();
     tmem_fence_before();
-    group_sync<CG>();
+    group_sync<CG * PAIRS>();
     if constexpr (CG > 1) __syncthreads();
     tmem_fence_after();
     uint32_t tmem;
@@ -253,7 +264,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         const uint32_t bytes = CG * (uint32_t)(jb.cut.tile_m * 128 +
                                                (BMN ? b_boxes * 64 : bn / CG) * kBK * 2);
         for (int item = group; ok && item < items; item += groups) {
-            const Tile t = tile_of(jb, item);
+            const Tile t = tile_of<PAIRS>(jb, item, pair);
             const int m0 = jb.a_m + t.m * (jb.cut.tile_m * CG) + (int)rank * 128;
             const int n0 = jb.b_n + t.n * bn + (int)rank * (bn / CG);
             const int k0 = t.split * jb.cut.k_chunk;
@@ -263,7 +274,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 if (!ok) break;
                 const uint32_t a = base + stage * kStage, b = a + kA;
                 if (rank == 0) mbar_expect(full(stage), bytes);
-                const uint32_t bar = CG == 1 ? full(stage) : in_leader(full(stage));
+                const uint32_t bar = CG == 1 ? full(stage) : in_cta(full(stage), leader);
                 const int ka = jb.a_k + kt * kBK, kb = jb.b_k + kt * kBK;
                 if constexpr (AMN) {
                     for (int i = 0; i < 2; ++i)
@@ -271,7 +282,11 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 } else {
                     tma_load<CG>(a, &jb.a, bar, ka, m0);
                 }
-                if constexpr (BMN) {
+                if constexpr (PAIRS == 2) {  // half of it, for both pairs
+                    static_assert(PAIRS == 1 || !BMN);
+                    tma_load_many(b + pair * (bn / 4) * 128, &jb.b, bar, kb, n0 + pair * (bn / 4),
+                                  5 << rank);
+                } else if constexpr (BMN) {
                     for (int i = 0; i < b_boxes; ++i)
                         tma_load<CG>(b + i * (64 * kBK * 2), &jb.b, bar, n0 + 64 * i, kb);
                 } else {
@@ -300,7 +315,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         uint32_t phase = 0;
         bool ok = true;
         for (int item = group; ok && item < items; item += groups, ++done) {
-            const Tile t = tile_of(jb, item);
+            const Tile t = tile_of<PAIRS>(jb, item, pair);
             const int k0 = t.split * jb.cut.k_chunk;
             const int k1 = min(jb.cut.k_tiles, k0 + jb.cut.k_chunk);
             const int buf = done & 1;
@@ -319,7 +334,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                 for (int k = 0; k < decltype(steps)::value; ++k)
                     mma<CG>(d, da + k * kStepA, db + k * kStepB, idesc, kt > k0 || k > 0);
-                mma_commit<CG>(empty(stage));
+                mma_commit<CG>(empty(stage), PAIRS == 2 ? 15 : 3);
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1;
@@ -333,7 +348,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 if (jb.steps == 2) product(whole, Steps<2>{});
                 if (jb.steps == 3) product(whole, Steps<3>{});
             }
-            if (ok) mma_commit<CG>(tfull(buf));
+            if (ok) mma_commit<CG>(tfull(buf), 3 << leader);
         }
     } else if (warp >= 4) {
         const int quad = warp % 4;  // its 32 lanes of tensor memory
@@ -363,7 +378,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         int done = 0;
         bool ok = true;
         for (int item = group; item < items; item += groups, ++done) {
-            const Tile t = tile_of(jb, item);
+            const Tile t = tile_of<PAIRS>(jb, item, pair);
             const int buf = done & 1;
             // this warp's first row and column; with SWAP its columns are those of the
             // quarter, and its rows go on with each 32
@@ -405,7 +420,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             auto release = [&] {
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_leader(tempty(buf)));
+                if (lane == 0) mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_cta(tempty(buf), leader));
             };
             // this row's 64 columns from i on as bf16
             [[maybe_unused]] auto put = [&](int i, const uint32_t (&w)[kW / 2], uint16_t *out,
@@ -564,7 +579,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
-    group_sync<CG>();
+    group_sync<CG * PAIRS>();
     tmem_fence_after();
     if (warp == 2) tmem_free<CG>(tmem, kCols);
 }
@@ -999,16 +1014,19 @@ bool make_out(CUtensorMap *m, void *p, bool f32, int64_t cols, int64_t rows, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CG, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
+// Clusters that the GPU holds at a time.
+int64_t room(int cg, int pairs) { return pairs == 2 ? 36 : kHeadSMs / cg; }
+
+template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
 cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
-    auto *kernel = k_head_mma<CG, BN, SWAP, AMN, BMN, KIND, LIST>;
+    auto *kernel = k_head_mma<CG, PAIRS, BN, SWAP, AMN, BMN, KIND, LIST>;
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const Cut &c = p.job.cut;
-    const int64_t items = (int64_t)c.m_tiles * c.n_tiles * c.splits;
+    const int64_t items = ceil_div(c.m_tiles, PAIRS) * c.n_tiles * c.splits;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, kHeadSMs / CG)));
+    cfg.gridDim = dim3((unsigned)(CG * PAIRS * std::min<int64_t>(items, room(CG, PAIRS))));
     cfg.blockDim = dim3(kMmaThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
@@ -1016,7 +1034,7 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = CG * PAIRS;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG > 1 ? 2 : 1;
@@ -1028,32 +1046,40 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
 template <Kind KIND, bool LIST>
 cudaError_t launch_logits(const MmaArgs &p, cudaStream_t s) {
     const Cut &c = p.job.cut;
-    if (!c.swap) return launch_mma<2, 256, false, false, false, KIND, LIST>(p, s);
-    if (c.bn == 32) return launch_mma<1, 32, true, false, false, KIND, LIST>(p, s);
-    return launch_mma<1, 128, true, false, false, KIND, LIST>(p, s);
+    if (c.pairs == 2) return launch_mma<2, 2, 256, false, false, false, KIND, LIST>(p, s);
+    if (!c.swap) return launch_mma<2, 1, 256, false, false, false, KIND, LIST>(p, s);
+    if (c.bn == 32) return launch_mma<1, 1, 32, true, false, false, KIND, LIST>(p, s);
+    return launch_mma<1, 1, 128, true, false, false, KIND, LIST>(p, s);
+}
+
+// a product of dz
+template <bool AMN>
+cudaError_t launch_out(const MmaArgs &p, cudaStream_t s) {
+    return p.job.cut.bn > 128 ? launch_mma<2, 1, 256, false, AMN, true, kOut, false>(p, s)
+                              : launch_mma<2, 1, 128, false, AMN, true, kOut, false>(p, s);
 }
 
 cudaError_t launch_d_hidden(const MmaArgs &p, cudaStream_t s) {
     const Cut &c = p.job.cut;
-    if (c.swap)
-        return c.bn == 32 ? launch_mma<1, 32, true, true, false, kOut, false>(p, s)
-                          : launch_mma<1, 128, true, true, false, kOut, false>(p, s);
-    return c.bn > 128 ? launch_mma<2, 256, false, false, true, kOut, false>(p, s)
-                      : launch_mma<2, 128, false, false, true, kOut, false>(p, s);
+    if (!c.swap) return launch_out<false>(p, s);
+    return c.bn == 32 ? launch_mma<1, 1, 32, true, true, false, kOut, false>(p, s)
+                      : launch_mma<1, 1, 128, true, true, false, kOut, false>(p, s);
 }
 
-cudaError_t launch_d_weight(const MmaArgs &p, cudaStream_t s) {
-    return p.job.cut.bn > 128 ? launch_mma<2, 256, false, true, true, kOut, false>(p, s)
-                              : launch_mma<2, 128, false, true, true, kOut, false>(p, s);
-}
-
+cudaError_t launch_d_weight(const MmaArgs &p, cudaStream_t s) { return launch_out<true>(p, s); }
 
 constexpr int64_t kFew = 128;  // tokens that SWAP takes
 
 // The logits' tiles, for all words or a piece of them.  Few tokens: the weight's rows are cut so that every SM has
 // the same number of tiles, none more than 128 rows.
-Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
+// Two pairs to a cluster where a call's product has up to 3e11 operations (0.16
+// ms): what L2 gives bounds it then.  1999 x 10007 x 520 took 26.8 us with them
+// and 27.5 without, a step of 3001 x 32003 x 1032 603 and 626 us.  Long products
+// run against the power limit, and the 8 more SMs of single pairs tell: a
+// distillation step of 4096 x 50257 x 1024 1,164 us with two, 1,151 with one.
+Cut cut_logits(int64_t tokens, int64_t words, int64_t dim, int64_t vocab) {
     Cut c{};
+    c.pairs = 1;
     c.k_tiles = c.k_chunk = (int32_t)ceil_div(dim, kBK);
     c.splits = 1;
     c.swap = tokens <= kFew;
@@ -1065,16 +1091,18 @@ Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
         c.m_tiles = (int32_t)ceil_div(words, c.tile_m);
         c.n_tiles = 1;
     } else {
-        // columns of a tile: what leaves the last wave of tiles fullest, a tile
-        // costing as much as 24 columns beside its own
         c.cg = 2;
         c.tile_m = 128;
         c.m_tiles = (int32_t)ceil_div(tokens, 256);
+        c.pairs = c.m_tiles > 1 && 2.0 * tokens * vocab * dim <= 3e11 ? 2 : 1;
+        // columns of a tile: what leaves the last wave of tiles fullest, a tile
+        // costing as much as 24 columns beside its own
         int64_t best = 0;
         for (int bn = 256; bn >= 128; bn -= 32) {
-            const int64_t waves = ceil_div(c.m_tiles * ceil_div(words, bn), kHeadSMs / 2);
-            if (best == 0 || waves * (bn + 24) < best) {
-                best = waves * (bn + 24);
+            const int64_t tiles = ceil_div(c.m_tiles, c.pairs) * ceil_div(words, bn);
+            const int64_t x = ceil_div(tiles, room(2, c.pairs)) * (bn + 24);
+            if (best == 0 || x < best) {
+                best = x;
                 c.bn = bn;
             }
         }
@@ -1089,6 +1117,7 @@ Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
 Cut cut_out(int64_t m, int64_t n, int64_t k, bool swap, int64_t tokens) {
     Cut c{};
     c.swap = swap;
+    c.pairs = 1;
     c.cg = swap ? 1 : 2;
     // the columns in equal tiles of up to 256, in steps of 32
     c.bn = swap ? (tokens <= 32 ? 32 : 128)
@@ -1098,9 +1127,9 @@ Cut cut_out(int64_t m, int64_t n, int64_t k, bool swap, int64_t tokens) {
     c.n_tiles = (int32_t)ceil_div(n, c.bn);
     c.k_tiles = (int32_t)ceil_div(k, kBK);
     int64_t splits = 1;
-    const int64_t tiles = (int64_t)c.m_tiles * c.n_tiles, room = kHeadSMs / c.cg;
-    if (tiles * 2 <= room)
-        splits = std::max<int64_t>(1, std::min<int64_t>(room / tiles, c.k_tiles / 4));
+    const int64_t tiles = (int64_t)c.m_tiles * c.n_tiles, at_a_time = room(c.cg, 1);
+    if (tiles * 2 <= at_a_time)
+        splits = std::max<int64_t>(1, std::min<int64_t>(at_a_time / tiles, c.k_tiles / 4));
     c.k_chunk = (int32_t)ceil_div(c.k_tiles, splits);
     c.splits = (int32_t)ceil_div(c.k_tiles, c.k_chunk);
     return c;
@@ -1180,7 +1209,7 @@ bool logits_job(MmaArgs *m, const HeadArgs &a, const Cut &cut, int64_t w0, int64
     (cut.swap ? jb.a_m : jb.b_n) = (int32_t)w0;
     return make_map(hidden, a.hidden, p.dim, p.tokens, a.hidden_stride, cut.swap ? cut.bn : 128) &&
            make_map(weight, a.weight, p.dim, p.vocab, a.weight_stride,
-                    cut.swap ? cut.tile_m : cut.bn / 2);
+                    cut.swap ? cut.tile_m : cut.bn / 2 / cut.pairs);
 }
 
 }  // namespace
@@ -1199,7 +1228,7 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
         __builtin_mul_overflow(std::max(tokens, vocab), dim, &probe) || probe > (1ll << 56) ||
         ceil_div(std::max(tokens, dim), 64) * ceil_div(std::max(vocab, tokens), 64) > kMost)
         return false;
-    p->logits = cut_logits(tokens, vocab, dim);
+    p->logits = cut_logits(tokens, vocab, dim, vocab);
     p->parts = p->logits.swap ? p->logits.m_tiles * 4 : p->logits.n_tiles * 2;
     int64_t at = 0;
     bool fits = true;
@@ -1300,7 +1329,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
         const int64_t w0 = i * p.piece, words = std::min(p.piece, p.vocab - w0);
         const bool last = i + 1 == p.pieces;
         MmaArgs m{};
-        if (!logits_job(&m, a, cut_logits(p.tokens, words, p.dim), w0, words) ||
+        if (!logits_job(&m, a, cut_logits(p.tokens, words, p.dim, p.vocab), w0, words) ||
             !make_out(&m.job.out, dz, false, words, p.tokens, p.piece, 1))
             return cudaErrorInvalidValue;
         m.row = f.factor;

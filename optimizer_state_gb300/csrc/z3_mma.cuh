@@ -50,10 +50,10 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
                  : "memory");
 }
 
-// An address of this CTA's shared memory in the first CTA of its cluster.
-__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+// An address of this CTA's shared memory in another CTA of its cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
 
@@ -71,9 +71,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-template <int CG>
+template <int CTAS>
 __device__ __forceinline__ void group_sync() {
-    if constexpr (CG == 1) {
+    if constexpr (CTAS == 1) {
         __syncthreads();
     } else {
         asm volatile(
@@ -138,6 +138,18 @@ __device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, u
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z),
                  "r"(w)
                  : "memory");
+}
+
+// The same box into the CTAs of `mask`, for CTA pairs.  Each of them has its
+// bytes counted by the barrier at `bar`'s place in its pair's even CTA.
+__device__ __forceinline__ void tma_load_many(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                              int x, int y, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(
+            dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "h"(mask)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
@@ -236,10 +248,10 @@ __device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint3
     }
 }
 
-// The barrier (with CG = 2 that of both CTAs) is arrived at once all products
-// issued by this thread so far are done.
+// The barrier (with CG = 2 that of the CTAs of `mask`) is arrived at once all
+// products issued by this thread so far are done.
 template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t mask) {
     if constexpr (CG == 1) {
         asm volatile(
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -249,7 +261,7 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
             ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)3)
+            "h"(mask)
             : "memory");
     }
 }

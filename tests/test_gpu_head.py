@@ -117,7 +117,7 @@ SIZES = [(1, 1, 8), (1, 2, 8), (3, 64, 64), (128, 256, 64), (127, 63, 72), (129,
          (1, 1000, 136), (2, 5003, 520), (300, 65, 200), (128, 1024, 512), (257, 1000, 64),
          (777, 5003, 136), (130, 300, 1032), (1500, 129, 8), (32, 777, 64), (33, 5003, 72),
          (100, 20011, 64), (16, 40009, 128), (300, 520, 520), (200, 300, 296), (150, 300, 1000),
-         (600, 333, 1288), (140, 4000, 24)]
+         (600, 333, 1288), (140, 4000, 24), (2000, 5003, 1032), (1300, 20011, 520)]
 
 
 @pytest.mark.parametrize("n,v,d", SIZES)
