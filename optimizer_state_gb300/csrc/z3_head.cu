@@ -40,6 +40,7 @@ struct Job {
     CUtensorMap a, b, out;
     Cut cut;
     int32_t steps;         // of 16 values in the last k tile
+    int32_t box_k;         // rows of K loaded of it, where both operands run along M and N
     int32_t n_fast;        // walk a row of tiles before the next row
     int32_t a_m, a_k;      // where in the maps this product begins
     int32_t b_n, b_k;
@@ -261,8 +262,10 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         // SWAP: a tile may have fewer than 128 rows; the others are not loaded, and
         // what their sums are is not looked at
         const int b_boxes = BMN ? (bn / CG + 63) / 64 : 0;  // of 64 columns
-        const uint32_t bytes = CG * (uint32_t)(jb.cut.tile_m * 128 +
-                                               (BMN ? b_boxes * 64 : bn / CG) * kBK * 2);
+        const uint32_t bytes = AMN && BMN
+                                   ? CG * (uint32_t)((2 + b_boxes) * jb.box_k * 128)
+                                   : CG * (uint32_t)(jb.cut.tile_m * 128 +
+                                                     (BMN ? b_boxes * 64 : bn / CG) * kBK * 2);
         for (int item = group; ok && item < items; item += groups) {
             const Tile t = tile_of<PAIRS>(jb, item, pair);
             const int m0 = jb.a_m + t.m * (jb.cut.tile_m * CG) + (int)rank * 128;
@@ -928,6 +931,7 @@ __global__ void __launch_bounds__(256) k_head_slabs(const float *slab, int split
     if (i >= rows * cols) return;
     const int64_t r = i / cols, c = i - r * cols;
     float v[8] = {};
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
         const float4 *f = reinterpret_cast<const float4 *>(slab + s * stride + i);
         const float4 x = f[0], y = f[1];
@@ -1392,8 +1396,10 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
             uint16_t *out = a.d_weight + w0 * a.d_weight_stride;
             jb.out_at = out;
             jb.out_pitch = a.d_weight_stride;
-            if (!make_map(&jb.a, dz, words, p.tokens, p.piece, kBK) ||
-                !make_map(&jb.b, hidden, p.dim, p.tokens, p.dim, kBK) ||
+            // few tokens: boxes of the rows that the products read
+            jb.box_k = p.tokens < kBK ? jb.steps * 16 : kBK;
+            if (!make_map(&jb.a, dz, words, p.tokens, p.piece, jb.box_k) ||
+                !make_map(&jb.b, hidden, p.dim, p.tokens, p.dim, jb.box_k) ||
                 !(jb.out_f32
                       ? make_out(&jb.out, slab, true, p.dim, words, p.dim, jb.cut.splits)
                       : make_out(&jb.out, out, false, p.dim, words, a.d_weight_stride, 1)))
