@@ -128,3 +128,224 @@ def test_xent(n, v, d):
 @pytest.mark.parametrize("n,v,d", SIZES)
 def test_distill(n, v, d):
     Case(n, v, d, k=7, tau=2.0).check()
+
+
+@pytest.mark.parametrize("k,teacher,index,tau,n,v", [
+    (1, torch.float32, torch.int32, 1.0, 200, 3000), (2, torch.bfloat16, torch.int64, 4.0, 40, 700),
+    (64, torch.bfloat16, torch.int32, 1.5, 300, 3000), (65, torch.float32, torch.int64, 0.5, 90, 999),
+    (200, torch.float32, torch.int32, 2.0, 513, 4003), (1024, torch.bfloat16, torch.int64, 1.0, 33, 200),
+    (1000, torch.float32, torch.int64, 3.0, 150, 20011)])
+def test_lists(k, teacher, index, tau, n, v):
+    """Lists of every length, longer than the vocabulary among them: words stand
+    in them many times."""
+    Case(n, v, 72, k=k, teacher=teacher, index=index, tau=tau, weighted=True).check(scale=0.3)
+
+
+@pytest.mark.parametrize("n", [5, 100, 700])
+@pytest.mark.parametrize("k", [0, 9])
+def test_rows_apart_weights_and_index_types(n, k):
+    for index, weighted, mean in itertools.product((torch.int32, torch.int64), (False, True),
+                                                   (False, True)):
+        Case(n, 1003, 136, k=k, tau=1.5 if k else 1.0, index=index, weighted=weighted, apart=8,
+             seed=n).check(scale=-2.0, mean=mean)
+
+
+@pytest.mark.parametrize("n", [7, 129, 600])
+@pytest.mark.parametrize("k", [0, 5])
+def test_rows_left_out_hold_anything(n, k):
+    """NaN and infinities in the rows of tokens that are left out, and of those
+    whose weight is 0, reach no gradient; all rows left out."""
+    c = Case(n, 700, 72, k=k, ignored=0.5, weighted=True)
+    out = (c.index < 0).all(dim=1) if k else c.targets < 0
+    want = c.reference()
+    c.hidden = c.hidden.clone()
+    c.hidden[out] = float("nan")
+    c.hidden[out.nonzero()[::2, 0]] = float("inf")
+    t, ws = c.outputs(), c.workspace()
+    c.forward(t, ws)
+    c.grad(t, ws)
+    torch.cuda.synchronize()
+    assert outside(t, want) == {}
+    # a weight of 0: the loss stays, NaN where its row is
+    zero = (~out).nonzero()[:3, 0]
+    c.weights[zero] = 0.0
+    want = c.reference()
+    c.hidden[zero] = float("nan")
+    c.forward(t, ws)
+    c.grad(t, ws)
+    torch.cuda.synchronize()
+    assert bool(t["loss"][zero].isnan().all())
+    t["loss"][zero] = want["loss"][0][zero].float()
+    t["lse"][zero] = want["lse"][0][zero].float()
+    assert outside(t, want) == {}
+    # nothing counts
+    if k:
+        c.index.fill_(-1)
+    else:
+        c.targets.fill_(-1)
+    c.hidden.fill_(float("nan"))
+    c.forward(t, ws)
+    c.grad(t, ws)
+    torch.cuda.synchronize()
+    assert all(bool((t[x] == 0).all()) for x in t)
+
+
+def test_lists_of_extreme_logits():
+    """The type's lowest value is a logit as any; -Inf leaves an entry out, and a
+    list of nothing else its token; +Inf and NaN spoil theirs."""
+    c = Case(40, 300, 64, k=6, ignored=0.0)
+    low = torch.finfo(torch.float32).min
+    c.index.clamp_(min=0)
+    c.teacher[0] = low                              # a uniform list
+    c.teacher[1, 1:] = low                          # one entry
+    c.teacher[2, ::2] = -torch.inf
+    c.teacher[3] = -torch.inf
+    c.teacher[4] = torch.finfo(torch.float32).max
+    c.teacher[5] = -torch.inf
+    c.teacher[5, 3] = -1.0
+    c.check()
+    for row, bad in ((6, torch.inf), (7, float("nan"))):
+        d = Case(40, 300, 64, k=6, ignored=0.0)
+        d.teacher[row, 2] = bad
+        d.index[row, 2] = 5
+        t, ws = d.outputs(), d.workspace()
+        d.forward(t, ws)
+        d.grad(t, ws)
+        torch.cuda.synchronize()
+        assert bool(t["loss"][row].isnan()) and int(t["loss"].isnan().sum()) == 1
+        assert bool(t["total"][0].isnan()) and bool(t["d_hidden"][row].isnan().all())
+
+
+@pytest.mark.parametrize("n", [6, 300])
+@pytest.mark.parametrize("k", [0, 4])
+def test_words_beyond_the_vocabulary(n, k):
+    """They read nothing, spoil their token's loss, and the weight's gradient."""
+    for beyond in (301, 2 ** 31 - 1, 2 ** 40):
+        c = Case(n, 301, 64, k=k, ignored=0.0)
+        want = c.reference()["loss"]
+        if k:
+            c.index[2, 1] = beyond
+        else:
+            c.targets[2] = beyond
+        t, ws = c.outputs(), c.workspace()
+        c.forward(t, ws)
+        c.grad(t, ws)
+        torch.cuda.synchronize()
+        assert bool(t["loss"][2].isnan()) and bool(t["total"][0].isnan())
+        others = torch.arange(n, device="cuda") != 2
+        assert bool(((t["loss"].double() - want[0]).abs() <= want[1])[others].all())
+        assert bool(t["d_hidden"][2].isnan().all()) and bool(t["d_weight"].isnan().all())
+        assert bool(t["d_hidden"][others].isfinite().all())
+        assert all(x.intact() for x in c.o.values())
+
+
+def test_logits_that_are_not_finite_spoil_their_token_alone():
+    c = Case(200, 500, 64, ignored=0.0)
+    want = c.reference()["loss"]
+    c.hidden[3, 5] = float("inf")
+    c.hidden[4, 5] = float("nan")
+    t, ws = c.outputs(), c.workspace()
+    c.forward(t, ws)
+    torch.cuda.synchronize()
+    others = torch.ones(200, dtype=torch.bool, device="cuda")
+    others[3:5] = False
+    assert bool(t["loss"][3:5].isnan().all())
+    assert bool(((t["loss"].double() - want[0]).abs() <= want[1])[others].all())
+
+
+@pytest.mark.parametrize("k", [0, 3])
+def test_no_tokens(k):
+    c = Case(0, 50, 64, k=k)
+    t, ws = c.outputs(), c.workspace()
+    c.forward(t, ws)
+    c.grad(t, ws)
+    torch.cuda.synchronize()
+    assert t["total"].tolist() == [0.0, 0.0] and bool((t["d_weight"] == 0).all())
+    assert all(x.intact() for x in c.o.values())
+
+
+def test_several_pieces_of_the_vocabulary():
+    """Sizes whose dz takes more than one piece, with a last one of odd length."""
+    for n, v, d, k in ((6000, 50021, 24, 0), (9000, 30011, 40, 5)):
+        assert n * v * 2 > 256 << 20
+        Case(n, v, d, k=k).check()
+
+
+@pytest.mark.parametrize("k", [0, 4])
+def test_either_gradient_alone(k):
+    c = Case(300, 900, 72, k=k)
+    t = c.check()
+    both = {x: t[x].clone() for x in ("d_hidden", "d_weight")}
+    for x in both:
+        t = c.outputs()
+        ws = c.workspace()
+        c.forward(t, ws)
+        other = "d_weight" if x == "d_hidden" else "d_hidden"
+        c.grad(t | {other: None}, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(t[x], both[x])
+        assert bool((t[other] == 77.0).all())
+
+
+@pytest.mark.parametrize("n,k", [(20, 0), (20, 6), (900, 0), (900, 6)])
+def test_the_same_bits_on_any_stream_and_replayed(n, k):
+    """Eager on two streams at a time, each with its workspace, and captured and
+    replayed on other inputs: the same bits."""
+    c = Case(n, 4001, 136, k=k)
+    first = {x: y.clone() for x, y in c.check().items()}
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    runs = [(c.outputs(), c.workspace()) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (t, ws) in zip(streams, runs):
+            c.forward(t, ws, stream=s)
+            c.grad(t, ws, stream=s)
+    torch.cuda.synchronize()
+    for t, _ in runs:
+        assert all(torch.equal(t[x], first[x]) for x in first)
+    t, ws = c.outputs(), c.workspace()
+    other = Case(n, 4001, 136, k=k, seed=1)
+    wanted = {x: y.clone() for x, y in other.check().items()}
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.forward(t, ws)
+        c.grad(t, ws)
+    names = ("hidden", "weight") + (("index", "teacher") if k else ("targets",))
+    kept = {x: getattr(c, x).clone() for x in names}
+    for values, want in ((kept, first), ({x: getattr(other, x) for x in names}, wanted),
+                         (kept, first)):
+        for x in names:
+            getattr(c, x).copy_(values[x])
+        ws.fill_(0xff)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(t[x], want[x]) for x in want)
+
+
+@pytest.mark.parametrize("k", [0, 5])
+def test_gradients_against_differences(k):
+    """The directional derivative of the loss in 64 bits, by central differences.
+    The third derivative along a unit step in every logit is at most a few
+    times the loss's weight: with steps of 2^-10 in directions whose logits
+    move by up to 1 the differences are off by less than 2^-18 in all."""
+    c = Case(60, 400, 64, k=k, tau=2.0 if k else 1.0, weighted=True)
+    t = c.check()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    args = (c.targets, c.index, c.teacher, c.tau, c.weights)
+    for name in ("hidden", "weight"):
+        x = getattr(c, name).double()
+        u = torch.randn(x.shape, device="cuda", generator=g, dtype=torch.float64)
+        y = (c.weight if name == "hidden" else c.hidden).double()
+        u /= (u @ y.T).abs().max()                   # logits move by up to 1
+        step = 2.0 ** -10
+
+        def mean(sign):
+            moved = x + sign * step * u
+            pair = (moved, c.weight) if name == "hidden" else (c.hidden, moved)
+            total = reference(*pair, *args)["total"][0]
+            return float(total[0] / total[1])
+        slope = (mean(1) - mean(-1)) / (2 * step)
+        value, bound = c.reference()["d_" + name]
+        got = float((t["d_" + name].double() * u).sum())
+        assert abs(got - slope) <= float((bound * u.abs()).sum()) + 2.0 ** -18
