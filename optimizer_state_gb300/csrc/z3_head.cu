@@ -124,12 +124,20 @@ __device__ __forceinline__ Tile tile_of(const Job &jb, int item, int pair) {
     return t;
 }
 
-// value of register `j` of a thread's own choice
+// The value at a place of a thread's own choice among its registers: by the
+// place's bits, 31 selections.
 __device__ __forceinline__ float pick(const float (&v)[32], uint32_t j) {
-    float x = v[0];
+    float x[16];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) x = j == (uint32_t)i ? v[i] : x;
-    return x;
+    for (int i = 0; i < 16; ++i) x[i] = (j & 1) ? v[2 * i + 1] : v[2 * i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (j & 2) ? x[2 * i + 1] : x[2 * i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (j & 4) ? x[2 * i + 1] : x[2 * i];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = (j & 8) ? x[2 * i + 1] : x[2 * i];
+    x[0] = (j & 16) ? x[1] : x[0];
+    return x[0];
 }
 
 // The entries of a token's list (or its target) among some columns of a
@@ -188,6 +196,26 @@ __device__ __forceinline__ void store_box(const Job &jb, uint32_t stage, int lan
 __device__ __forceinline__ void await_box(int lane) {
     if (lane == 0) tma_wait_read();
     __syncwarp();
+}
+
+// 64 columns of this thread's row as bf16 into the staging rows; or the first 32
+// straight to the result, where a tile ends with half a box and the next
+// tile's columns lie behind it.
+__device__ __forceinline__ void put64(uint32_t stage, int lane, const uint32_t (&w)[32], bool part,
+                                      bool live, uint16_t *out) {
+    if (part) {
+        if (!live) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(out + 8 * j) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        return;
+    }
+    await_box(lane);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[4 * j], w[4 * j + 1],
+                  w[4 * j + 2], w[4 * j + 3]);
 }
 
 // D tile by tile: 128 x CG rows by BN columns.  One thread feeds TMA, one issues
@@ -425,26 +453,6 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_cta(tempty(buf), leader));
             };
-            // this row's 64 columns from i on as bf16
-            [[maybe_unused]] auto put = [&](int i, const uint32_t (&w)[kW / 2], uint16_t *out,
-                                            int64_t pitch) {
-                if (i + 32 == bn - c0 && col0 + i + 32 < jb.cols) {
-                    // half a box at the tile's end, the next tile's columns behind it
-                    uint16_t *o = out + row * pitch + col0 + i;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (live)
-                            *reinterpret_cast<uint4 *>(o + 8 * j) =
-                                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                } else {
-                    await_box(lane);
-#pragma unroll
-                    for (int j = 0; j < kW / 8; ++j)
-                        st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4), w[4 * j],
-                                  w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                    store_box(jb, stage, lane, col0 + i, row0, 0);
-                }
-            };
             if (c0 >= BN || per == 0) release();
 #pragma unroll 1
             for (int i = 0; i < per && c0 + i < BN; i += kW) {
@@ -524,33 +532,53 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 } else if constexpr (KIND == kDz) {
                     const bool none = rw.x == 0.0f;  // also where the logits are not finite
 #pragma unroll
-                    for (int h = 0; h < kW / 32; ++h) {
+                    for (int h = 0; h < kW / 32; ++h)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             v[h][j] = exp2_fast(__fmaf_rn(v[h][j], p.beta, -rw.y)) * rw.x;
-                        while (walk.next() < min(c + 32 * h + 32, cols)) {
-                            const float q = rw.x * walk.share[0];
-                            const int hit = walk.next() - c - 32 * h;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j == hit) v[h][j] -= q;
-                            walk.advance();
-                        }
-                    }
                     // rounded once to bf16, the type of the products' operands
                     uint32_t w[kW / 2];
 #pragma unroll
                     for (int j = 0; j < kW / 2; ++j)
                         w[j] = none ? 0u : pack_bf16x2(v[j / 16][2 * j % 32], v[j / 16][2 * j % 32 + 1]);
+                    // the few words that the token asks for, in place of what was
+                    // written for them
+                    auto patch = [&](uint16_t *at, int swizzle) {
+#pragma unroll
+                        for (int h = 0; h < kW / 32; ++h)
+                            while (walk.next() < min(c + 32 * h + 32, cols)) {
+                                const int hit = walk.next();
+                                float x = pick(v[h], (uint32_t)(hit - c - 32 * h));
+                                do {  // all shares of a word
+                                    x -= rw.x * walk.share[0];
+                                    walk.advance();
+                                } while (LIST && walk.next() == hit);
+                                const int col = hit - c;
+                                at[((col / 8 ^ swizzle) << 3) + col % 8] =
+                                    none ? (uint16_t)0 : f32_to_bf16(x);
+                            }
+                    };
                     if constexpr (SWAP) {
                         uint16_t *o = p.dz + row * p.dz_pitch + col0;
+                        if (live) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)  // a pitch of 8s: room beyond the last word
-                            if (live && 8 * j < cols)
-                                *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
-                                    w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                            for (int j = 0; j < 4; ++j)  // a pitch of 8s: room beyond the last word
+                                if (8 * j < cols)
+                                    *reinterpret_cast<uint4 *>(o + 8 * j) = make_uint4(
+                                        w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                            patch(o, 0);
+                        }
                     } else {
-                        put(i, w, p.dz, p.dz_pitch);
+                        const bool part = i + 32 == bn - c0 && col0 + i + 32 < jb.cols;
+                        uint16_t *o = p.dz + row * p.dz_pitch + col0 + i;
+                        put64(stage, lane, w, part, live, o);
+                        if (part)
+                            patch(o, 0);
+                        else
+                            patch(reinterpret_cast<uint16_t *>(raw + (stage - smem_u32(raw)) +
+                                                               lane * 128),
+                                  lane & 7);
+                        if (!part) store_box(jb, stage, lane, col0 + i, row0, 0);
                     }
                 } else if (SWAP || jb.out_f32) {
 #pragma unroll
@@ -571,7 +599,9 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                     for (int j = 0; j < kW / 2; ++j)
                         w[j] = pack_bf16x2(v[j / 16][2 * j % 32], v[j / 16][2 * j % 32 + 1]);
-                    put(i, w, jb.out_at, jb.out_pitch);
+                    const bool part = i + 32 == bn - c0 && col0 + i + 32 < jb.cols;
+                    put64(stage, lane, w, part, live, jb.out_at + row * jb.out_pitch + col0 + i);
+                    if (!part) store_box(jb, stage, lane, col0 + i, row0, 0);
                 }
             }
             if constexpr (KIND == kStats && !SWAP)
