@@ -654,18 +654,23 @@ __device__ __forceinline__ float larger(float x, float y) {
 // A token's list by ascending word, with q = softmax(teacher / temperature), and
 // where the entries of every kGrain words begin.  Entries of a negative word
 // or a logit of -Inf are left out (at the end, q = 0); a word beyond the
-// vocabulary spoils the row.  N threads to a token: a warp for lists of up to
-// 64, whose bitonic sort of (word, place) then needs no barrier of the CTA
-// (4096 lists of 64: 9 us, 16 with 128 threads), 128 for longer ones (501
-// lists of 200: 10 us, 30 with a warp).  Equal words keep their order.
+// vocabulary spoils the row.  Equal words keep their order.
+// N threads to a token.  A warp takes lists of up to 64, which needs no barrier
+// of the CTA; an entry's place is the number of entries before it, counted
+// four words a load (a forward call with 777 lists of 19: 25.7 us, 26.5 by a
+// sort).  The counting grows as the square: longer lists take 128 threads and a
+// bitonic sort (501 lists of 200: 10.5 us, 13.5 by counting).
 template <int N>
-__global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, int pow2) {
+__global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, int room) {
+    constexpr bool RANK = N == 32;
     extern __shared__ uint64_t keys[];
     __shared__ float red[2][kSortThreads / 32];
     pdl_enter();
     const int tid = threadIdx.x % N;
     const int64_t t = (int64_t)blockIdx.x * (kSortThreads / N) + threadIdx.x / N;
-    uint64_t *key = keys + threadIdx.x / N * pow2;
+    // (word, place); by rank the words alone stand behind them, in the order given
+    uint64_t *key = keys + threadIdx.x / N * (RANK ? room + room / 2 : room);
+    uint32_t *given = reinterpret_cast<uint32_t *>(key + room);
     if (t >= a.tokens) return;  // all threads of the token
     auto sync = [] {
         if constexpr (N == 32) __syncwarp(); else __syncthreads();
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, in
     };
     bool bad = false;
     float top = -INFINITY;
-    for (int i = tid; i < pow2; i += N) {
+    for (int i = tid; i < room; i += N) {
         uint32_t word = 0x7fffffffu;
         if (i < a.k) {
             const int64_t w = load_index(a.index, a.index_bytes, t * a.k + i);
@@ -689,7 +694,8 @@ __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, in
                 top = larger(top, x);
             }
         }
-        key[i] = (uint64_t)word << 32 | (uint32_t)i;
+        if constexpr (RANK) given[i] = word;
+        else key[i] = (uint64_t)word << 32 | (uint32_t)i;
     }
     for (int o = 16; o > 0; o /= 2) top = larger(top, __shfl_xor_sync(~0u, top, o));
     if constexpr (N == 32) {
@@ -699,15 +705,31 @@ __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, in
         bad = __syncthreads_or(bad);
         for (int i = 0; i < N / 32; ++i) top = larger(top, red[0][i]);
     }
-    for (int size = 2; size <= pow2; size *= 2) {
-        for (int stride = size / 2; stride > 0; stride /= 2) {
-            sync();
-            for (int i = tid; i < pow2 / 2; i += N) {
-                const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
-                const uint64_t x = key[lo], y = key[hi];
-                if ((x > y) == ((lo & size) == 0)) {
-                    key[lo] = y;
-                    key[hi] = x;
+    if constexpr (RANK) {
+        sync();
+        for (int i = tid; i < room; i += N) {
+            const uint32_t mine = given[i];
+            int before = 0;
+            for (int j = 0; j < room; j += 4) {  // room is a multiple of 4
+                const uint4 w = *reinterpret_cast<const uint4 *>(given + j);
+                before += w.x < mine || (w.x == mine && j < i);
+                before += w.y < mine || (w.y == mine && j + 1 < i);
+                before += w.z < mine || (w.z == mine && j + 2 < i);
+                before += w.w < mine || (w.w == mine && j + 3 < i);
+            }
+            key[before] = (uint64_t)mine << 32 | (uint32_t)i;
+        }
+    } else {
+        for (int size = 2; size <= room; size *= 2) {
+            for (int stride = size / 2; stride > 0; stride /= 2) {
+                sync();
+                for (int i = tid; i < room / 2; i += N) {
+                    const int lo = 2 * i - (i & (stride - 1)), hi = lo + stride;
+                    const uint64_t x = key[lo], y = key[hi];
+                    if ((x > y) == ((lo & size) == 0)) {
+                        key[lo] = y;
+                        key[hi] = x;
+                    }
                 }
             }
         }
@@ -845,11 +867,18 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
         float part = 0.0f;
         const float inv = __fdiv_rn(1.0f, a.row.temperature);
         if (state == kCounts) {
-            for (int i = slice; i < a.row.k; i += kSlices) {
-                const float q = a.row.q[t * a.row.k + i];
-                // 0 log 0 = 0: an entry left out, or one whose q is below binary32
-                if (q != 0.0f)
-                    part += q * (logf(q) - a.z[t * a.row.k + i] * inv + lse);
+            for (int i = slice; i < a.row.k; i += 4 * kSlices) {
+                float q[4], x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int at = i + j * kSlices;
+                    q[j] = at < a.row.k ? a.row.q[t * a.row.k + at] : 0.0f;
+                    x[j] = at < a.row.k ? a.z[t * a.row.k + at] : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    // 0 log 0 = 0: an entry left out, or one whose q is below binary32
+                    if (q[j] != 0.0f) part += q[j] * (logf(q[j]) - x[j] * inv + lse);
             }
         }
 #pragma unroll
@@ -1208,14 +1237,15 @@ RowArgs row_args(const HeadArgs &a) {
 }
 
 cudaError_t launch_lists(const RowArgs &r, cudaStream_t s) {
+    constexpr int kN = kSortThreads;
+    const int room = (r.k + 3) / 4 * 4;
     int pow2 = 2;
     while (pow2 < r.k) pow2 *= 2;
-    if (pow2 <= 64)
-        launch_small(k_head_lists<32>, ceil_div(r.tokens, kSortThreads / 32), kSortThreads,
-                     kSortThreads / 32 * pow2 * sizeof(uint64_t), s, r, pow2);
+    if (r.k <= 64)
+        launch_small(k_head_lists<32>, ceil_div(r.tokens, kN / 32), kN, kN / 32 * room * 12, s, r,
+                     room);
     else
-        launch_small(k_head_lists<kSortThreads>, r.tokens, kSortThreads, pow2 * sizeof(uint64_t),
-                     s, r, pow2);
+        launch_small(k_head_lists<kN>, r.tokens, kN, pow2 * 8, s, r, pow2);
     return cudaGetLastError();
 }
 
