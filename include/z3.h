@@ -413,7 +413,10 @@ z3_status z3_model_step_clipped(const z3_unit *units, const z3_clip_unit *clips,
  * total[1] is 0: no token counts), else of scale * total[0].  A total of several
  * calls added up, such as every rank's, makes them those of the mean over all.
  *
- * Sums and softmax statistics are held in binary32.  dz, the gradient of the
+ * Sums and softmax statistics are held in binary32; the logits' sums are the
+ * tensor cores', which cut off instead of rounding (1e-6 of a logit at dim =
+ * 1024, 3e-6 at 4096), but for z3_xent's target logits, which are rounded: a
+ * likely target's loss keeps its digits.  dz, the gradient of the
  * logits, is rounded to bf16 (the operand type of the two products that
  * follow, whose sums are binary32), each result once more at its end.  Results
  * depend on the sizes only: the same call gives the same bits.  A head whose

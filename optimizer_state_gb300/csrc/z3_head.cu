@@ -67,9 +67,13 @@ struct MmaArgs {
     unsigned *done;        // zeroed for the join
     const void *targets;
     int32_t target_bytes;
+    const uint16_t *hidden, *weight;
+    int64_t hidden_stride, weight_stride, vocab;
+    int32_t dim;
     // kDz
     const float2 *row;
     const int32_t *words;
+    const float *target;   // dz at the target
     uint16_t *dz;
     int64_t dz_pitch;
 };
@@ -77,6 +81,28 @@ struct MmaArgs {
 __device__ __forceinline__ int64_t load_index(const void *p, int bytes, int64_t i) {
     return bytes == 8 ? static_cast<const int64_t *>(p)[i]
                       : (int64_t)static_cast<const int32_t *>(p)[i];
+}
+
+// The part of a row's dot product that one of `lanes` threads sums: products of
+// bf16 are exact, their sums rounded to nearest.
+__device__ __forceinline__ float dot_part(const uint16_t *x, const uint16_t *y, int64_t dim,
+                                          int lane, int lanes) {
+    float s[8] = {};
+#pragma unroll 4
+    for (int64_t i = lane * 8; i < dim; i += lanes * 8) {
+        float a[8], b[8];
+        unpack8(ld8b(x + i), a);
+        unpack8(ld8b(y + i), b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = __fmaf_rn(a[j], b[j], s[j]);
+    }
+    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(~0u, x, o);
+    return x;
 }
 
 template <int BN, int CG>
@@ -381,6 +407,17 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             }
             if (ok) mma_commit<CG>(tfull(buf), 3 << leader);
         }
+    } else if (KIND == kStats && !LIST && (warp == 2 || warp == 3)) {
+        // The targets' logits, summed with rounding: the tensor cores cut off, 1e-6
+        // of a sum of 1024 terms.  A likely target's loss is a small difference
+        // of lse and its logit, so that the logit's error would be the loss's.
+        for (int64_t t = 2 * blockIdx.x + warp - 2; t < jb.rows; t += 2 * gridDim.x) {
+            const int64_t w = load_index(p.targets, p.target_bytes, t);
+            if (w < 0 || w >= p.vocab) continue;
+            const float z = warp_sum(dot_part(p.hidden + t * p.hidden_stride,
+                                              p.weight + w * p.weight_stride, p.dim, lane, 32));
+            if (lane == 0) p.z[t] = z;
+        }
     } else if (warp >= 4) {
         const int quad = warp % 4;  // its 32 lanes of tensor memory
         const int half = (warp - 4) / 4;
@@ -392,14 +429,18 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         struct Ask {
             int64_t word;
             float2 rw;
+            float target;
         };
         [[maybe_unused]] auto ask = [&](int64_t row) {
-            Ask x{-1, make_float2(0.0f, 0.0f)};
+            Ask x{-1, make_float2(0.0f, 0.0f), 0.0f};
             if (row >= jb.rows) return x;
             if constexpr (!LIST)
                 x.word = KIND == kStats ? load_index(p.targets, p.target_bytes, row)
                                         : (int64_t)p.words[row];
-            if constexpr (KIND == kDz) x.rw = p.row[row];
+            if constexpr (KIND == kDz) {
+                x.rw = p.row[row];
+                if constexpr (!LIST) x.target = p.target[row];
+            }
             return x;
         };
         [[maybe_unused]] Ask mine[2];
@@ -424,9 +465,11 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             bool live = row < jb.rows;
             [[maybe_unused]] Walk<LIST, LIST && KIND == kDz> walk;
             [[maybe_unused]] float2 rw;
+            [[maybe_unused]] float target;
             [[maybe_unused]] auto begin_row = [&](const Ask &x) {
                 walk = {};
                 rw = x.rw;
+                target = x.target;
                 if (!live || cols <= 0) return;
                 if constexpr (LIST) {
                     const uint16_t *f = p.first + row * p.first_pitch;
@@ -500,8 +543,14 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                     for (int h = 0; h < kW / 32; ++h)
                         while (walk.next() < min(c + 32 * h + 32, cols)) {
-                            p.z[LIST ? row * p.k + walk.at : row] =
-                                pick(v[h], (uint32_t)(walk.next() - c - 32 * h));
+                            const int hit = walk.next() - c - 32 * h;
+                            if constexpr (LIST) {
+                                p.z[row * p.k + walk.at] = pick(v[h], (uint32_t)hit);
+                            } else {  // the target's share of the sum is added exactly
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (j == hit) v[h][j] = -INFINITY;
+                            }
                             walk.advance();
                         }
                     if (c + kW > cols) {
@@ -548,11 +597,16 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                         for (int h = 0; h < kW / 32; ++h)
                             while (walk.next() < min(c + 32 * h + 32, cols)) {
                                 const int hit = walk.next();
-                                float x = pick(v[h], (uint32_t)(hit - c - 32 * h));
-                                do {  // all shares of a word
-                                    x -= rw.x * walk.share[0];
+                                float x = target;
+                                if constexpr (LIST) {
+                                    x = pick(v[h], (uint32_t)(hit - c - 32 * h));
+                                    do {  // all shares of a word
+                                        x -= rw.x * walk.share[0];
+                                        walk.advance();
+                                    } while (walk.next() == hit);
+                                } else {
                                     walk.advance();
-                                } while (LIST && walk.next() == hit);
+                                }
                                 const int col = hit - c;
                                 at[((col / 8 ^ swizzle) << 3) + col % 8] =
                                     none ? (uint16_t)0 : f32_to_bf16(x);
@@ -861,8 +915,21 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
         acc = joined[0][tok];
         for (int w = 1; w < kWarps; ++w) acc = join2(acc, joined[w][tok]);
     }
-    // a sum that is not a number stays one through the logarithm
-    const float lse = (acc.x + log2f(acc.y)) * kLn2;
+    // a sum that is not a number stays one through the logarithms
+    float lse = (acc.x + log2f(acc.y)) * kLn2;
+    float loss1 = 0.0f;
+    if (a.row.k == 0 && state == kCounts) {
+        // the sums are without the target's term: loss = log(1 + the others / its)
+        const float more = __fmaf_rn(-z, kLog2e, acc.x);
+        if (acc.y == 0.0f) {  // a vocabulary of one, or all others below binary32
+            lse = z;
+        } else if (more < 64.0f) {
+            loss1 = log1pf(acc.y * exp2f(more));
+            lse = z + loss1;
+        } else {  // its term is below the sum's last bit
+            loss1 = lse - z;
+        }
+    }
     if (a.row.k > 0) {
         float part = 0.0f;
         const float inv = __fdiv_rn(1.0f, a.row.temperature);
@@ -896,7 +963,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
                 for (int w = 0; w < kWarps; ++w) loss += lists[w][tok];
                 loss *= a.row.temperature * a.row.temperature;
             } else if (state == kCounts) {
-                loss = lse - z;
+                loss = loss1;
             }
             a.loss[t] = loss;
             a.lse[t] = state == kLeftOut ? 0.0f : lse;
@@ -948,16 +1015,22 @@ struct FactorArgs {
     float scale;
     float2 *factor;
     int32_t *words;
+    float *target;
     const uint16_t *hidden;
     int64_t stride;
+    const uint16_t *weight;
+    int64_t weight_stride;
     uint16_t *copy;        // null: not needed
 };
 
-// Each token's factor a = scale w / total[1] (times the temperature) and its
-// lse in powers of two; and the hidden states with zeros in the rows left out:
-// what stands there may be anything, and 0 * NaN would reach d_weight.  The
-// copy costs 4 bytes a value, 5 us of the 1.9 ms at 8192 x 1024.
+// Each token's factor a = scale w / total[1] (times the temperature), its lse in
+// powers of two and, with a target, dz there: a (exp(z - lse) - 1) of a logit
+// that is summed with rounding, as in the forward call.  And the hidden states
+// with zeros in the rows left out: what stands there may be anything, and 0 *
+// NaN would reach d_weight.  The copy costs 4 bytes a value, the targets' rows
+// of the weight 2 more: 13 us of the 2.2 ms at 8192 x 1024.
 __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
+    __shared__ float dots[4];
     pdl_enter();
     const int64_t t = blockIdx.x;
     int64_t word = -1;
@@ -968,15 +1041,27 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
     if (a.row.k > 0) f = __fmul_rn(f, a.row.temperature);
     if (state == kLeftOut) f = 0.0f;
     if (state == kBad) f = NAN;
+    const float lse = a.lse[t];
+    const uint16_t *row = a.hidden + t * a.stride;
+    if (a.row.k == 0 && state == kCounts) {
+        const float part =
+            warp_sum(dot_part(row, a.weight + word * a.weight_stride, a.row.dim, threadIdx.x, 128));
+        if (threadIdx.x % 32 == 0) dots[threadIdx.x / 32] = part;
+        __syncthreads();
+    }
     if (threadIdx.x == 0) {
-        a.factor[t] = make_float2(f, __fmul_rn(a.lse[t], kLog2e));
-        if (a.row.k == 0) a.words[t] = state == kCounts ? (int32_t)word : -1;
+        a.factor[t] = make_float2(f, __fmul_rn(lse, kLog2e));
+        if (a.row.k == 0) {
+            a.words[t] = state == kCounts ? (int32_t)word : -1;
+            const float z = (dots[0] + dots[1]) + (dots[2] + dots[3]);
+            a.target[t] = state == kCounts ? f * expm1f(z - lse) : 0.0f;
+        }
     }
     if (a.copy == nullptr) return;
     const bool keep = f != 0.0f;
     for (int64_t i = threadIdx.x * 8; i < a.row.dim; i += 128 * 8) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (keep) x = ld8b(a.hidden + t * a.stride + i);
+        if (keep) x = ld8b(row + i);
         *reinterpret_cast<uint4 *>(a.copy + t * a.row.dim + i) = x;
     }
 }
@@ -1207,7 +1292,10 @@ Cut cut_d_weight(int64_t tokens, int64_t dim, int64_t words) {
     return cut_out(words, dim, tokens, false, tokens);
 }
 
-constexpr int64_t kPieceBytes = 256ll << 20;  // of dz
+// dz of a piece of the vocabulary: 256 MB, but 2048 words at least, so that the
+// sums of d_hidden, read and written once a piece, cost less than its products.
+constexpr int64_t kPieceBytes = 256ll << 20;
+constexpr int64_t kPieceWords = 2048;
 
 // Up to the end of the last tile.
 int64_t first_pitch(const HeadPlan &p) { return ceil_div(p.vocab, 256) * (256 / kGrain) + 1; }
@@ -1314,12 +1402,14 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
     p->q = take(tokens * k, 4);
     p->first = take(k ? tokens * first_pitch(*p) : 0, 2);
     if (grads && tokens > 0) {
-        const int64_t most = std::max<int64_t>(1, kPieceBytes / 512 / tokens) * 256;
+        const int64_t most =
+            std::max<int64_t>(kPieceWords / 256, kPieceBytes / 512 / tokens) * 256;
         p->pieces = ceil_div(vocab, most);
         p->piece = ceil_div(ceil_div(vocab, p->pieces), 256) * 256;
         p->pieces = ceil_div(vocab, p->piece);
         p->rows = take(tokens, 8);
         p->words = take(tokens, 4);
+        p->target = take(tokens, 4);
         p->hidden = take(tokens * dim, 2);
         p->dz = take(tokens * p->piece, 2);
         const Cut h = cut_d_hidden(tokens, dim, p->piece);
@@ -1345,6 +1435,12 @@ cudaError_t launch_head_forward(const HeadArgs &a, cudaStream_t s) {
     m.done = reinterpret_cast<unsigned *>(a.ws + p.done);
     m.targets = a.index;
     m.target_bytes = a.index_bytes;
+    m.hidden = a.hidden;
+    m.weight = a.weight;
+    m.hidden_stride = a.hidden_stride;
+    m.weight_stride = a.weight_stride;
+    m.vocab = p.vocab;
+    m.dim = (int32_t)p.dim;
     fill_lists(&m, r);
     e = r.k > 0 ? launch_logits<kStats, true>(m, s) : launch_logits<kStats, false>(m, s);
     if (e != cudaSuccess) return e;
@@ -1382,8 +1478,11 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
     f.scale = a.scale;
     f.factor = reinterpret_cast<float2 *>(a.ws + p.rows);
     f.words = reinterpret_cast<int32_t *>(a.ws + p.words);
+    f.target = reinterpret_cast<float *>(a.ws + p.target);
     f.hidden = a.hidden;
     f.stride = a.hidden_stride;
+    f.weight = a.weight;
+    f.weight_stride = a.weight_stride;
     f.copy = a.d_weight ? hidden : nullptr;
     launch_small(k_head_factors, p.tokens, 128, 0, s, f);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -1398,6 +1497,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
             return cudaErrorInvalidValue;
         m.row = f.factor;
         m.words = f.words;
+        m.target = f.target;
         m.dz = dz;
         m.dz_pitch = p.piece;
         fill_lists(&m, r);
