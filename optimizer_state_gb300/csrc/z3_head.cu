@@ -88,7 +88,7 @@ __device__ __forceinline__ int64_t load_index(const void *p, int bytes, int64_t 
 __device__ __forceinline__ float dot_part(const uint16_t *x, const uint16_t *y, int64_t dim,
                                           int lane, int lanes) {
     float s[8] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = lane * 8; i < dim; i += lanes * 8) {
         float a[8], b[8];
         unpack8(ld8b(x + i), a);
@@ -411,12 +411,19 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         // The targets' logits, summed with rounding: the tensor cores cut off, 1e-6
         // of a sum of 1024 terms.  A likely target's loss is a small difference
         // of lse and its logit, so that the logit's error would be the loss's.
-        for (int64_t t = 2 * blockIdx.x + warp - 2; t < jb.rows; t += 2 * gridDim.x) {
-            const int64_t w = load_index(p.targets, p.target_bytes, t);
-            if (w < 0 || w >= p.vocab) continue;
-            const float z = warp_sum(dot_part(p.hidden + t * p.hidden_stride,
-                                              p.weight + w * p.weight_stride, p.dim, lane, 32));
-            if (lane == 0) p.z[t] = z;
+        // Eight lanes to a token.
+        for (int64_t t0 = 4 * (2 * blockIdx.x + warp - 2); t0 < jb.rows; t0 += 8 * gridDim.x) {
+            const int64_t t = t0 + lane / 8;
+            int64_t w = -1;
+            if (t < jb.rows) w = load_index(p.targets, p.target_bytes, t);
+            float z = 0.0f;
+            const bool counts = w >= 0 && w < p.vocab;
+            if (counts)
+                z = dot_part(p.hidden + t * p.hidden_stride, p.weight + w * p.weight_stride, p.dim,
+                             lane % 8, 8);
+#pragma unroll
+            for (int o = 4; o > 0; o /= 2) z += __shfl_xor_sync(~0u, z, o);
+            if (counts && lane % 8 == 0) p.z[t] = z;
         }
     } else if (warp >= 4) {
         const int quad = warp % 4;  // its 32 lanes of tensor memory
@@ -561,30 +568,47 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                                 v[h][j] = c + 32 * h + j < cols ? v[h][j] : -INFINITY;
                     }
                     // four chains of each; exp(z / temperature) = 2^(beta z)
-                    float m[4], s[4];
+                    float m[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) m[j] = v[0][j];
+                    for (int j = 0; j < 4; ++j) m[j] = fmaxf(v[0][2 * j], v[0][2 * j + 1]);
 #pragma unroll
-                    for (int j = 4; j < kW; ++j) m[j % 4] = fmaxf(m[j % 4], v[j / 32][j % 32]);
+                    for (int j = 8; j < kW; j += 2)
+                        m[j / 2 % 4] = max3(m[j / 2 % 4], v[j / 32][j % 32], v[j / 32][j % 32 + 1]);
                     const float new_top =
                         fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * p.beta);
                     const float shift = new_top == -INFINITY ? 0.0f : -new_top;
+                    const float2 beta2 = make_float2(p.beta, p.beta);
+                    const float2 shift2 = make_float2(shift, shift);
+                    float2 s[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] = exp2_fast(__fmaf_rn(v[0][j], p.beta, shift));
-#pragma unroll
-                    for (int j = 4; j < kW; ++j)
-                        s[j % 4] += exp2_fast(__fmaf_rn(v[j / 32][j % 32], p.beta, shift));
-                    sum = __fmaf_rn(sum, exp2_fast(top + shift), (s[0] + s[1]) + (s[2] + s[3]));
+                    for (int j = 0; j < kW; j += 2) {
+                        float2 e = fma2(make_float2(v[j / 32][j % 32], v[j / 32][j % 32 + 1]),
+                                        beta2, shift2);
+                        e.x = exp2_fast(e.x);
+                        e.y = exp2_fast(e.y);
+                        s[j / 2 % 4] = j < 8 ? e : add2(s[j / 2 % 4], e);
+                    }
+                    const float2 s2 = add2(add2(s[0], s[1]), add2(s[2], s[3]));
+                    sum = __fmaf_rn(sum, exp2_fast(top + shift), s2.x + s2.y);
                     top = new_top;
                     if constexpr (SWAP)
                         if (live) p.part[(t.m * 4 + quad) * jb.rows + row] = make_float2(top, sum);
                 } else if constexpr (KIND == kDz) {
                     const bool none = rw.x == 0.0f;  // also where the logits are not finite
+                    const float2 beta2 = make_float2(p.beta, p.beta);
+                    const float2 lse2 = make_float2(-rw.y, -rw.y);
+                    const float2 factor2 = make_float2(rw.x, rw.x);
 #pragma unroll
                     for (int h = 0; h < kW / 32; ++h)
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[h][j] = exp2_fast(__fmaf_rn(v[h][j], p.beta, -rw.y)) * rw.x;
+                        for (int j = 0; j < 32; j += 2) {
+                            float2 e = fma2(make_float2(v[h][j], v[h][j + 1]), beta2, lse2);
+                            e.x = exp2_fast(e.x);
+                            e.y = exp2_fast(e.y);
+                            e = mul2(e, factor2);
+                            v[h][j] = e.x;
+                            v[h][j + 1] = e.y;
+                        }
                     // rounded once to bf16, the type of the products' operands
                     uint32_t w[kW / 2];
 #pragma unroll
