@@ -1045,6 +1045,7 @@ struct FactorArgs {
     const uint16_t *weight;
     int64_t weight_stride;
     uint16_t *copy;        // null: not needed
+    int64_t copy_stride;
 };
 
 // Each token's factor a = scale w / total[1] (times the temperature), its lse in
@@ -1086,7 +1087,7 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
     for (int64_t i = threadIdx.x * 8; i < a.row.dim; i += 128 * 8) {
         uint4 x = make_uint4(0, 0, 0, 0);
         if (keep) x = ld8b(row + i);
-        *reinterpret_cast<uint4 *>(a.copy + t * a.row.dim + i) = x;
+        *reinterpret_cast<uint4 *>(a.copy + t * a.copy_stride + i) = x;
     }
 }
 
@@ -1244,12 +1245,12 @@ constexpr int64_t kFew = 128;  // tokens that SWAP takes
 
 // The logits' tiles, for all words or a piece of them.  Few tokens: the weight's rows are cut so that every SM has
 // the same number of tiles, none more than 128 rows.
-// Two pairs to a cluster where a call's product has up to 3e11 operations (0.16
-// ms): what L2 gives bounds it then.  1999 x 10007 x 520 took 26.8 us with them
-// and 27.5 without, a step of 3001 x 32003 x 1032 603 and 626 us.  Long products
-// run against the power limit, and the 8 more SMs of single pairs tell: a
-// distillation step of 4096 x 50257 x 1024 1,164 us with two, 1,151 with one.
-Cut cut_logits(int64_t tokens, int64_t words, int64_t dim, int64_t vocab) {
+// Two pairs to a cluster where rows do not start on lines of 128 bytes: a box's
+// rows then touch two lines each, and what L2 gives bounds the product (3001 x
+// 32003 x 1032: 139 us with single pairs, 134 with two; 8192 x 50257 x 1032: 546
+// and 492).  Where they do, the 8 more SMs of single pairs tell (8192 x 50257
+// x 1024: 510 us and 521).
+Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
     Cut c{};
     c.pairs = 1;
     c.k_tiles = c.k_chunk = (int32_t)ceil_div(dim, kBK);
@@ -1266,7 +1267,7 @@ Cut cut_logits(int64_t tokens, int64_t words, int64_t dim, int64_t vocab) {
         c.cg = 2;
         c.tile_m = 128;
         c.m_tiles = (int32_t)ceil_div(tokens, 256);
-        c.pairs = c.m_tiles > 1 && 2.0 * tokens * vocab * dim <= 3e11 ? 2 : 1;
+        c.pairs = c.m_tiles > 1 && dim % 64 != 0 ? 2 : 1;
         // columns of a tile: what leaves the last wave of tiles fullest, a tile
         // costing as much as 24 columns beside its own
         int64_t best = 0;
@@ -1404,7 +1405,7 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
         __builtin_mul_overflow(std::max(tokens, vocab), dim, &probe) || probe > (1ll << 56) ||
         ceil_div(std::max(tokens, dim), 64) * ceil_div(std::max(vocab, tokens), 64) > kMost)
         return false;
-    p->logits = cut_logits(tokens, vocab, dim, vocab);
+    p->logits = cut_logits(tokens, vocab, dim);
     p->parts = p->logits.swap ? p->logits.m_tiles * 4 : p->logits.n_tiles * 2;
     int64_t at = 0;
     bool fits = true;
@@ -1434,7 +1435,8 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
         p->rows = take(tokens, 8);
         p->words = take(tokens, 4);
         p->target = take(tokens, 4);
-        p->hidden = take(tokens * dim, 2);
+        p->hidden_pitch = ceil_div(dim, 64) * 64;
+        p->hidden = take(tokens * p->hidden_pitch, 2);
         p->dz = take(tokens * p->piece, 2);
         const Cut h = cut_d_hidden(tokens, dim, p->piece);
         const Cut w = cut_d_weight(tokens, dim, p->piece);
@@ -1508,15 +1510,22 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
     f.weight = a.weight;
     f.weight_stride = a.weight_stride;
     f.copy = a.d_weight ? hidden : nullptr;
+    f.copy_stride = p.hidden_pitch;
     launch_small(k_head_factors, p.tokens, 128, 0, s, f);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
+    // the copy's rows start on lines of 128 bytes, whatever the caller's do
+    HeadArgs from = a;
+    if (a.d_weight) {
+        from.hidden = hidden;
+        from.hidden_stride = p.hidden_pitch;
+    }
     uint16_t *dz = reinterpret_cast<uint16_t *>(a.ws + p.dz);
     for (int64_t i = 0; i < p.pieces; ++i) {
         const int64_t w0 = i * p.piece, words = std::min(p.piece, p.vocab - w0);
         const bool last = i + 1 == p.pieces;
         MmaArgs m{};
-        if (!logits_job(&m, a, cut_logits(p.tokens, words, p.dim, p.vocab), w0, words) ||
+        if (!logits_job(&m, from, cut_logits(p.tokens, words, p.dim), w0, words) ||
             !make_out(&m.job.out, dz, false, words, p.tokens, p.piece, 1))
             return cudaErrorInvalidValue;
         m.row = f.factor;
@@ -1583,7 +1592,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
             // few tokens: boxes of the rows that the products read
             jb.box_k = p.tokens < kBK ? jb.steps * 16 : kBK;
             if (!make_map(&jb.a, dz, words, p.tokens, p.piece, jb.box_k) ||
-                !make_map(&jb.b, hidden, p.dim, p.tokens, p.dim, jb.box_k) ||
+                !make_map(&jb.b, hidden, p.dim, p.tokens, p.hidden_pitch, jb.box_k) ||
                 !(jb.out_f32
                       ? make_out(&jb.out, slab, true, p.dim, words, p.dim, jb.cut.splits)
                       : make_out(&jb.out, out, false, p.dim, words, a.d_weight_stride, 1)))

@@ -47,7 +47,8 @@ struct HeadPlan {
     int64_t rows;        // float2 [tokens]: factor, lse * log2 e
     int64_t words;       // int32 [tokens]: the target
     int64_t target;      // float [tokens]: dz there
-    int64_t hidden;      // bf16 [tokens][dim]: zero where the row is left out
+    int64_t hidden;      // bf16 [tokens][hidden_pitch]: zero where the row is left out
+    int64_t hidden_pitch;
     int64_t dz;          // bf16 [tokens][piece]
     int64_t slab_h;      // float [splits][tokens][dim]
     int64_t slab_w;      // float [splits][piece][dim]
