@@ -136,7 +136,7 @@ class Head:
         else:
             forward, backward, heads = z3.z3_distill, z3.z3_distill_grad, (teacher, index)
             extra = (temperature,)
-        forward(hidden.view(-1, self.dim), weight, *[x.view(-1, *x.shape[2:]) for x in heads],
+        forward(hidden.flatten(0, 1), weight, *[x.flatten(0, 1) for x in heads],
                 *extra, self.loss.view(-1), self.lse.view(-1), self.total, self._workspace,
                 weights=None if weights is None else weights.view(-1), stream=stream)
         for r in range(self.ranks if grads else 0):
