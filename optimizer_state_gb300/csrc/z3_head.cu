@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "z3_device.cuh"
@@ -1194,9 +1195,17 @@ int64_t room(int cg, int pairs) { return pairs == 2 ? 36 : kHeadSMs / cg; }
 template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
 cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
     auto *kernel = k_head_mma<CG, PAIRS, BN, SWAP, AMN, BMN, KIND, LIST>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    // once for each device (1 us of host time)
+    static std::atomic<uint64_t> allowed{0};
+    int device;
+    cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (device & 63);
+    if (device > 63 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        allowed.fetch_or(bit, std::memory_order_relaxed);
+    }
     const Cut &c = p.job.cut;
     const int64_t items = ceil_div(c.m_tiles, PAIRS) * c.n_tiles * c.splits;
     cudaLaunchConfig_t cfg{};

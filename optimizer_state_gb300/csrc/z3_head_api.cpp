@@ -23,17 +23,19 @@ struct Span {
 z3_status check_spans(const char *fn, const Span *b, int n) {
     for (int i = 0; i < n; ++i) {
         if (b[i].bytes == 0) continue;
-        const std::string what = std::string(fn) + ": " + b[i].name;
-        if (b[i].ptr == nullptr) return fail(Z3_ERR_INVALID_ARG, what + " is NULL");
+        auto refuse = [&](z3_status st, const std::string &what) {
+            return fail(st, std::string(fn) + ": " + b[i].name + what);
+        };
+        if (b[i].ptr == nullptr) return refuse(Z3_ERR_INVALID_ARG, " is NULL");
         if (reinterpret_cast<uintptr_t>(b[i].ptr) % (uintptr_t)b[i].align != 0)
-            return fail(Z3_ERR_ALIGNMENT,
-                        what + " is not " + std::to_string(b[i].align) + "-byte aligned");
+            return refuse(Z3_ERR_ALIGNMENT,
+                          " is not " + std::to_string(b[i].align) + "-byte aligned");
         for (int j = 0; j < i; ++j) {
             if (b[j].bytes == 0 || !(b[i].written || b[j].written)) continue;
             const uintptr_t x = reinterpret_cast<uintptr_t>(b[i].ptr);
             const uintptr_t y = reinterpret_cast<uintptr_t>(b[j].ptr);
             if (x < y + (uintptr_t)b[j].bytes && y < x + (uintptr_t)b[i].bytes)
-                return fail(Z3_ERR_INVALID_ARG, what + " overlaps " + b[j].name);
+                return refuse(Z3_ERR_INVALID_ARG, std::string(" overlaps ") + b[j].name);
         }
     }
     return Z3_OK;
@@ -42,31 +44,34 @@ z3_status check_spans(const char *fn, const Span *b, int n) {
 // The bytes that `rows` rows of `dim` bf16 values span, `stride` values apart.
 z3_status check_matrix(const char *fn, const char *name, int64_t rows, int64_t dim, int64_t stride,
                        int64_t *bytes) {
-    const std::string what = std::string(fn) + ": " + name + "_stride";
-    if (stride < dim) return fail(Z3_ERR_INVALID_ARG, what + " < dim");
+    auto refuse = [&](z3_status st, const char *what) {
+        return fail(st, std::string(fn) + ": " + name + what);
+    };
+    if (stride < dim) return refuse(Z3_ERR_INVALID_ARG, "_stride < dim");
     if (stride % kVec != 0)
-        return fail(Z3_ERR_ALIGNMENT, what + " is not a multiple of 8 elements");
+        return refuse(Z3_ERR_ALIGNMENT, "_stride is not a multiple of 8 elements");
     int64_t n;
     // a tensor map's strides have 40 bits
     if (stride >= (1ll << 39) || __builtin_mul_overflow(rows, stride, &n) || n > (1ll << 60))
-        return fail(Z3_ERR_OVERFLOW, std::string(fn) + ": " + name + " does not fit");
+        return refuse(Z3_ERR_OVERFLOW, " does not fit");
     *bytes = rows ? ((rows - 1) * stride + dim) * 2 : 0;
     return Z3_OK;
 }
 
 z3_status check_sizes(const char *fn, int64_t tokens, int64_t dim, int64_t vocab, int64_t k,
                       bool grads, HeadPlan *plan) {
-    const std::string name(fn);
-    if (tokens < 0) return fail(Z3_ERR_INVALID_ARG, name + ": tokens < 0");
-    if (vocab < 1) return fail(Z3_ERR_INVALID_ARG, name + ": vocab < 1");
-    if (dim < 1) return fail(Z3_ERR_INVALID_ARG, name + ": dim < 1");
-    if (dim % kVec != 0)
-        return fail(Z3_ERR_INVALID_ARG, name + ": dim is not a multiple of 8");
+    auto refuse = [&](z3_status st, const std::string &what) {
+        return fail(st, std::string(fn) + ": " + what);
+    };
+    if (tokens < 0) return refuse(Z3_ERR_INVALID_ARG, "tokens < 0");
+    if (vocab < 1) return refuse(Z3_ERR_INVALID_ARG, "vocab < 1");
+    if (dim < 1) return refuse(Z3_ERR_INVALID_ARG, "dim < 1");
+    if (dim % kVec != 0) return refuse(Z3_ERR_INVALID_ARG, "dim is not a multiple of 8");
     if (k < 0 || k > kHeadMaxList)
-        return fail(Z3_ERR_INVALID_ARG,
-                    name + ": k is not within 0.." + std::to_string(kHeadMaxList));
+        return refuse(Z3_ERR_INVALID_ARG,
+                      "k is not within 0.." + std::to_string(kHeadMaxList));
     if (!head_plan(tokens, dim, vocab, k, grads, plan))
-        return fail(Z3_ERR_OVERFLOW, name + ": the sizes do not fit");
+        return refuse(Z3_ERR_OVERFLOW, "the sizes do not fit");
     return Z3_OK;
 }
 
@@ -74,20 +79,21 @@ z3_status check_sizes(const char *fn, int64_t tokens, int64_t dim, int64_t vocab
 z3_status check_head(const char *fn, const z3_head *h, const void *index, int32_t index_bytes,
                      const z3_teacher *t, bool grads, void *ws, int64_t ws_bytes, HeadArgs *a,
                      Span *spans) {
-    const std::string name(fn);
-    if (h == nullptr) return fail(Z3_ERR_INVALID_ARG, name + ": head is NULL");
+    auto refuse = [&](const std::string &what) {
+        return fail(Z3_ERR_INVALID_ARG, std::string(fn) + ": " + what);
+    };
+    if (h == nullptr) return refuse("head is NULL");
     a->temperature = 1.0f;
     int64_t k = 0;
     if (t != nullptr) {
         k = t->k;
         if (k < 1 || k > kHeadMaxList)
-            return fail(Z3_ERR_INVALID_ARG,
-                        name + ": k is not within 1.." + std::to_string(kHeadMaxList));
+            return refuse("k is not within 1.." + std::to_string(kHeadMaxList));
         if (t->dtype != Z3_BF16 && t->dtype != Z3_F32)
-            return fail(Z3_ERR_INVALID_ARG, name + ": the teacher's logits are Z3_BF16 or Z3_F32");
+            return refuse("the teacher's logits are Z3_BF16 or Z3_F32");
         const float tau = t->temperature;
         if (!(tau > 0.0f) || !std::isfinite(tau * tau) || !std::isfinite(2.0f / tau))
-            return fail(Z3_ERR_INVALID_ARG, name + ": temperature");
+            return refuse("temperature");
         index = t->index;
         index_bytes = t->index_bytes;
         a->teacher = t->logits;
@@ -95,12 +101,12 @@ z3_status check_head(const char *fn, const z3_head *h, const void *index, int32_
         a->temperature = tau;
     }
     if (index_bytes != 4 && index_bytes != 8)
-        return fail(Z3_ERR_INVALID_ARG, name + ": index_bytes must be 4 or 8");
+        return refuse("index_bytes must be 4 or 8");
     z3_status st = check_sizes(fn, h->tokens, h->dim, h->vocab, k, grads, &a->plan);
     if (st != Z3_OK) return st;
     if (ws_bytes < a->plan.bytes)
-        return fail(Z3_ERR_INVALID_ARG, name + ": the workspace has " + std::to_string(ws_bytes) +
-                                            " bytes, needs " + std::to_string(a->plan.bytes));
+        return refuse("the workspace has " + std::to_string(ws_bytes) + " bytes, needs " +
+                      std::to_string(a->plan.bytes));
     int64_t hb, wb;
     if ((st = check_matrix(fn, "hidden", h->tokens, h->dim, h->hidden_stride, &hb)) != Z3_OK ||
         (st = check_matrix(fn, "weight", h->vocab, h->dim, h->weight_stride, &wb)) != Z3_OK)

@@ -599,7 +599,7 @@ def _matrix(t, rows, cols, here, name: str):
     may lie apart."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: needs shape [{rows}, {cols}], has {list(t.shape)}")
     apart, step = t.stride()
     if rows <= 1:
@@ -607,7 +607,7 @@ def _matrix(t, rows, cols, here, name: str):
     if cols > 1 and step != 1 or apart < cols:
         raise ValueError(f"{name}: strides {t.stride()}: rows must be contiguous and apart")
     b16 = _head_types()[0]
-    if not t.is_cuda or t.get_device() != here or t.dtype not in b16:
+    if t.get_device() != here or t.dtype not in b16:
         _dev(t[:0], b16, 0, name)                   # says what is wrong
     return t.data_ptr(), apart
 
@@ -615,9 +615,9 @@ def _matrix(t, rows, cols, here, name: str):
 def _vector(t, dtypes, shape, here, name: str):
     if t is None:
         return None
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: needs shape {list(shape)}, has {list(t.shape)}")
-    if not t.is_cuda or t.get_device() != here or t.dtype not in dtypes or not t.is_contiguous():
+    if t.get_device() != here or t.dtype not in dtypes or not t.is_contiguous():
         _dev(t, dtypes, 0, name)                    # says what is wrong
     return t.data_ptr()
 
@@ -626,9 +626,9 @@ class _HeadCall:
     """The arguments that the calls below share, from tensors."""
 
     def __init__(self, hidden, weight, weights, workspace, stream):
-        for t, name in ((hidden, "hidden"), (weight, "weight")):
-            if t.dim() != 2:
-                raise ValueError(f"{name}: needs two dimensions, has shape {list(t.shape)}")
+        if hidden.dim() != 2 or weight.dim() != 2:
+            t, name = (weight, "weight") if hidden.dim() == 2 else (hidden, "hidden")
+            raise ValueError(f"{name}: needs two dimensions, has shape {list(t.shape)}")
         self.n, self.d = n, d = hidden.shape
         self.v = v = weight.shape[0]
         self.here = here = _current_device()() if hidden.is_cuda else None
@@ -636,8 +636,11 @@ class _HeadCall:
         w, ws = _matrix(weight, v, d, here, "weight")
         self.head = ctypes.byref(Head(h, hs, w, ws, n, v, d, self.vector(weights, 1, (n,),
                                                                          "weights")))
-        self.end = (_vector(workspace, _head_types()[4], workspace.shape[:1], here, "workspace"),
-                    workspace.shape[0], _stream(stream))
+        space = workspace.numel()
+        if stream is None:
+            stream = _torch()._C._cuda_getCurrentRawStream(here)
+        self.end = (_vector(workspace, _head_types()[4], (space,), here, "workspace"), space,
+                    _stream(stream))
 
     def vector(self, t, kind, shape, name):
         return _vector(t, _head_types()[kind], shape, self.here, name)
