@@ -42,7 +42,8 @@ struct Job {
     CUtensorMap a, b, out;
     Cut cut;
     int32_t steps;         // of 16 values in the last k tile
-    int32_t box_k;         // rows of K loaded of it, where both operands run along M and N
+    int32_t a_mn;          // kOut without SWAP: a's rows run along M rather than K ...
+    int32_t box_k;         // ... and boxes of a and b hold this many of K's
     int32_t n_fast;        // walk a row of tiles before the next row
     int32_t a_m, a_k;      // where in the maps this product begins
     int32_t b_n, b_k;
@@ -54,7 +55,11 @@ struct Job {
 };
 
 struct MmaArgs {
-    Job job;
+    // JOINT: the first product's tiles go round the groups, which leaves the first
+    // `more` groups with one more than the others.  The second's go round the
+    // others `ahead` times, then round all.
+    Job job[2];
+    int32_t more, ahead;
     // kStats, kDz
     float beta;            // log2(e) / temperature: exponents are powers of two
     int32_t word0;         // the word of column 0
@@ -260,14 +265,18 @@ __device__ __forceinline__ void put64(uint32_t stage, int lane, const uint32_t (
 // such clusters, 144 SMs, fit the GPU.
 // Every wait ends (mbar_wait); an epilogue whose tile did not come takes NaN for
 // its values.
-template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
+// AMN, BMN: an operand's rows run along M or N rather than K.
+// JOINT: d_hidden and d_weight in one launch, whose tiles fill each other's last
+// wave; a's rows run either way, by job.
+template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST,
+          bool JOINT>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 k_head_mma(const __grid_constant__ MmaArgs p) {
     constexpr int S = stages<BN, CG>();
     constexpr int kA = 128 * kBK * 2;
     constexpr int kStage = stage_bytes<BN, CG>();
     constexpr int kCols = 2 * BN;    // of tensor memory: two tiles
-    const int bn = SWAP ? BN : p.job.cut.bn;  // columns of a tile
+    const int bn = SWAP ? BN : p.job[0].cut.bn;  // columns of a tile
     extern __shared__ uint8_t raw[];
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
     const uint32_t staging = base + S * kStage;
@@ -283,13 +292,33 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     const int pair = place / CG;
     const uint32_t leader = place - rank;
     const int group = blockIdx.x / (CG * PAIRS), groups = gridDim.x / (CG * PAIRS);
-    const Job &jb = p.job;
-    const int items =
-        (jb.cut.m_tiles + PAIRS - 1) / PAIRS * jb.cut.n_tiles * jb.cut.splits;
+    const int items = (p.job[0].cut.m_tiles + PAIRS - 1) / PAIRS * p.job[0].cut.n_tiles *
+                      p.job[0].cut.splits;
+    [[maybe_unused]] const int second_items =
+        JOINT ? p.job[1].cut.m_tiles * p.job[1].cut.n_tiles * p.job[1].cut.splits : 0;
+    const int first_items = items > group ? (items - group + groups - 1) / groups : 0;
+    // this group's n-th tile: which of which job
+    auto take = [&](int n, int *job, int *item) {
+        *job = 0;
+        *item = group + n * groups;
+        if (n < first_items) return true;
+        if constexpr (!JOINT) return false;
+        *job = 1;
+        n -= first_items;
+        const int others = groups - p.more;
+        if (group >= p.more && n < p.ahead) {
+            *item = n * others + group - p.more;
+        } else {
+            if (group >= p.more) n -= p.ahead;
+            *item = p.ahead * others + n * groups + group;
+        }
+        return *item < second_items;
+    };
+    int job, item;
 
     if (warp == 0 && lane == 0) {
-        tma_prefetch_map(&jb.a);
-        tma_prefetch_map(&jb.b);
+        tma_prefetch_map(&p.job[0].a);
+        tma_prefetch_map(&p.job[0].b);
         for (int i = 0; i < S; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), PAIRS);
@@ -318,12 +347,16 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         // SWAP: a tile may have fewer than 128 rows; the others are not loaded, and
         // what their sums are is not looked at
         const int b_boxes = BMN ? (bn / CG + 63) / 64 : 0;  // of 64 columns
-        const uint32_t bytes = AMN && BMN
-                                   ? CG * (uint32_t)((2 + b_boxes) * jb.box_k * 128)
-                                   : CG * (uint32_t)(jb.cut.tile_m * 128 +
-                                                     (BMN ? b_boxes * 64 : bn / CG) * kBK * 2);
-        for (int item = group; ok && item < items; item += groups) {
+        for (int n = 0; ok && take(n, &job, &item); ++n) {
+            const Job &jb = p.job[JOINT ? job : 0];
             const Tile t = tile_of<PAIRS>(jb, item, pair);
+            const bool a_mn = JOINT ? jb.a_mn != 0 : AMN;
+            const uint32_t bytes =
+                KIND == kOut && !SWAP
+                      ? CG * (uint32_t)((a_mn ? 2 * jb.box_k : 128) * 128 +
+                                        b_boxes * jb.box_k * 128)
+                      : CG * (uint32_t)(jb.cut.tile_m * 128 +
+                                        (BMN ? b_boxes * 64 : bn / CG) * kBK * 2);
             const int m0 = jb.a_m + t.m * (jb.cut.tile_m * CG) + (int)rank * 128;
             const int n0 = jb.b_n + t.n * bn + (int)rank * (bn / CG);
             const int k0 = t.split * jb.cut.k_chunk;
@@ -335,7 +368,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 if (rank == 0) mbar_expect(full(stage), bytes);
                 const uint32_t bar = CG == 1 ? full(stage) : in_cta(full(stage), leader);
                 const int ka = jb.a_k + kt * kBK, kb = jb.b_k + kt * kBK;
-                if constexpr (AMN) {
+                if (a_mn) {
                     for (int i = 0; i < 2; ++i)
                         tma_load<CG>(a + i * (64 * kBK * 2), &jb.a, bar, m0 + 64 * i, ka);
                 } else {
@@ -367,14 +400,16 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             }
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        const uint32_t idesc = mma_desc(128 * CG, bn, AMN, BMN);
-        constexpr uint32_t kStepA = AMN ? 16 * 128 / 16 : 32 / 16;  // 16 values of K on
-        constexpr uint32_t kStepB = BMN ? 16 * 128 / 16 : 32 / 16;
-        int stage = 0, done = 0;
+        constexpr uint32_t kStepB = BMN ? 16 * 128 / 16 : 32 / 16;  // 16 values of K on
+        int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int item = group; ok && item < items; item += groups, ++done) {
+        for (int done = 0; ok && take(done, &job, &item); ++done) {
+            const Job &jb = p.job[JOINT ? job : 0];
             const Tile t = tile_of<PAIRS>(jb, item, pair);
+            const bool a_mn = JOINT ? jb.a_mn != 0 : AMN;
+            const uint32_t idesc = mma_desc(128 * CG, bn, a_mn, BMN);
+            const uint32_t step_a = a_mn ? 16 * 128 / 16 : 32 / 16;
             const int k0 = t.split * jb.cut.k_chunk;
             const int k1 = min(jb.cut.k_tiles, k0 + jb.cut.k_chunk);
             const int buf = done & 1;
@@ -388,11 +423,12 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 if (!ok) return;
                 tmem_fence_after();
                 const uint32_t a = base + stage * kStage;
-                const uint64_t da = operand_desc<AMN>(a, 64 * kBK * 2);
+                // (K-major tiles have no use for the distance of their blocks)
+                const uint64_t da = operand_desc<AMN || JOINT>(a, 64 * kBK * 2);
                 const uint64_t db = operand_desc<BMN>(a + kA, 64 * kBK * 2);
 #pragma unroll
                 for (int k = 0; k < decltype(steps)::value; ++k)
-                    mma<CG>(d, da + k * kStepA, db + k * kStepB, idesc, kt > k0 || k > 0);
+                    mma<CG>(d, da + k * step_a, db + k * kStepB, idesc, kt > k0 || k > 0);
                 mma_commit<CG>(empty(stage), PAIRS == 2 ? 15 : 3);
                 if (++stage == S) {
                     stage = 0;
@@ -414,10 +450,11 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         // of a sum of 1024 terms.  A likely target's loss is a small difference
         // of lse and its logit, so that the logit's error would be the loss's.
         // Eight lanes to a token.
-        for (int64_t t0 = 4 * (2 * blockIdx.x + warp - 2); t0 < jb.rows; t0 += 8 * gridDim.x) {
+        const int64_t tokens = p.job[0].rows;
+        for (int64_t t0 = 4 * (2 * blockIdx.x + warp - 2); t0 < tokens; t0 += 8 * gridDim.x) {
             const int64_t t = t0 + lane / 8;
             int64_t w = -1;
-            if (t < jb.rows) w = load_index(p.targets, p.target_bytes, t);
+            if (t < tokens) w = load_index(p.targets, p.target_bytes, t);
             float z = 0.0f;
             const bool counts = w >= 0 && w < p.vocab;
             if (counts)
@@ -442,7 +479,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         };
         [[maybe_unused]] auto ask = [&](int64_t row) {
             Ask x{-1, make_float2(0.0f, 0.0f), 0.0f};
-            if (row >= jb.rows) return x;
+            if (row >= p.job[0].rows) return x;
             if constexpr (!LIST)
                 x.word = KIND == kStats ? load_index(p.targets, p.target_bytes, row)
                                         : (int64_t)p.words[row];
@@ -456,9 +493,9 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         if constexpr (SWAP && KIND != kOut)  // the same tokens in every tile
             for (int i = 0; i < 2; ++i)
                 if (32 * i < kPer) mine[i] = ask(c0 + 32 * i + lane);
-        int done = 0;
         bool ok = true;
-        for (int item = group; item < items; item += groups, ++done) {
+        for (int done = 0; take(done, &job, &item); ++done) {
+            const Job &jb = p.job[JOINT ? job : 0];
             const Tile t = tile_of<PAIRS>(jb, item, pair);
             const int buf = done & 1;
             // this warp's first row and column; with SWAP its columns are those of the
@@ -1192,9 +1229,14 @@ bool make_out(CUtensorMap *m, void *p, bool f32, int64_t cols, int64_t rows, int
 // Clusters that the GPU holds at a time.
 int64_t room(int cg, int pairs) { return pairs == 2 ? 36 : kHeadSMs / cg; }
 
-template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST>
+int64_t tiles(const Cut &c, int pairs = 1) {
+    return ceil_div(c.m_tiles, pairs) * c.n_tiles * c.splits;
+}
+
+template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST,
+          bool JOINT = false>
 cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
-    auto *kernel = k_head_mma<CG, PAIRS, BN, SWAP, AMN, BMN, KIND, LIST>;
+    auto *kernel = k_head_mma<CG, PAIRS, BN, SWAP, AMN, BMN, KIND, LIST, JOINT>;
     // once for each device (1 us of host time)
     static std::atomic<uint64_t> allowed{0};
     int device;
@@ -1206,8 +1248,8 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    const Cut &c = p.job.cut;
-    const int64_t items = ceil_div(c.m_tiles, PAIRS) * c.n_tiles * c.splits;
+    const int64_t items =
+        tiles(p.job[0].cut, PAIRS) + (JOINT ? tiles(p.job[1].cut) : 0);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(CG * PAIRS * std::min<int64_t>(items, room(CG, PAIRS))));
     cfg.blockDim = dim3(kMmaThreads);
@@ -1228,28 +1270,52 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
 // tokens x words
 template <Kind KIND, bool LIST>
 cudaError_t launch_logits(const MmaArgs &p, cudaStream_t s) {
-    const Cut &c = p.job.cut;
+    const Cut &c = p.job[0].cut;
     if (c.pairs == 2) return launch_mma<2, 2, 256, false, false, false, KIND, LIST>(p, s);
     if (!c.swap) return launch_mma<2, 1, 256, false, false, false, KIND, LIST>(p, s);
     if (c.bn == 32) return launch_mma<1, 1, 32, true, false, false, KIND, LIST>(p, s);
     return launch_mma<1, 1, 128, true, false, false, KIND, LIST>(p, s);
 }
 
-// a product of dz
+// One product of dz; or both, in any order.
 template <bool AMN>
 cudaError_t launch_out(const MmaArgs &p, cudaStream_t s) {
-    return p.job.cut.bn > 128 ? launch_mma<2, 1, 256, false, AMN, true, kOut, false>(p, s)
-                              : launch_mma<2, 1, 128, false, AMN, true, kOut, false>(p, s);
+    return p.job[0].cut.bn > 128 ? launch_mma<2, 1, 256, false, AMN, true, kOut, false>(p, s)
+                                 : launch_mma<2, 1, 128, false, AMN, true, kOut, false>(p, s);
 }
 
-cudaError_t launch_d_hidden(const MmaArgs &p, cudaStream_t s) {
-    const Cut &c = p.job.cut;
-    if (!c.swap) return launch_out<false>(p, s);
-    return c.bn == 32 ? launch_mma<1, 1, 32, true, true, false, kOut, false>(p, s)
-                      : launch_mma<1, 1, 128, true, true, false, kOut, false>(p, s);
+cudaError_t launch_both(MmaArgs &p, cudaStream_t s) {
+    // a tile's cost: its depth, and two k tiles' time between tiles
+    auto cost = [](const Job &jb) { return (int64_t)jb.cut.k_chunk + 2; };
+    if (cost(p.job[0]) < cost(p.job[1])) std::swap(p.job[0], p.job[1]);
+    const int64_t first = tiles(p.job[0].cut), second = tiles(p.job[1].cut);
+    const int64_t groups = std::min(room(2, 1), first + second);
+    const int64_t more = first % groups, each = first / groups;
+    const int64_t c0 = cost(p.job[0]), c1 = cost(p.job[1]);
+    // tiles of the second that a group ends in this time after `firsts` of the first
+    auto fits = [&](int64_t time, int64_t firsts) {
+        return std::max<int64_t>(0, (time - firsts * c0) / c1);
+    };
+    int64_t lo = 0, hi = (each + 1) * c0 + second * c1;
+    while (lo < hi) {  // the least time in which all groups end all of them
+        const int64_t mid = (lo + hi) / 2;
+        if (more * fits(mid, each + 1) + (groups - more) * fits(mid, each) >= second)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    p.more = (int32_t)more;
+    p.ahead = more > 0 ? (int32_t)(fits(lo, each) - fits(lo, each + 1)) : 0;
+    return p.job[0].cut.bn > 128
+               ? launch_mma<2, 1, 256, false, false, true, kOut, false, true>(p, s)
+               : launch_mma<2, 1, 128, false, false, true, kOut, false, true>(p, s);
 }
 
-cudaError_t launch_d_weight(const MmaArgs &p, cudaStream_t s) { return launch_out<true>(p, s); }
+// d_hidden of few tokens
+cudaError_t launch_d_hidden_few(const MmaArgs &p, cudaStream_t s) {
+    return p.job[0].cut.bn == 32 ? launch_mma<1, 1, 32, true, true, false, kOut, false>(p, s)
+                                 : launch_mma<1, 1, 128, true, true, false, kOut, false>(p, s);
+}
 
 constexpr int64_t kFew = 128;  // tokens that SWAP takes
 
@@ -1387,7 +1453,7 @@ int last_steps(int64_t k) { return (int)ceil_div(k - (ceil_div(k, kBK) - 1) * kB
 // The product of the hidden states with the words from w0 on.
 bool logits_job(MmaArgs *m, const HeadArgs &a, const Cut &cut, int64_t w0, int64_t words) {
     const HeadPlan &p = a.plan;
-    Job &jb = m->job;
+    Job &jb = m->job[0];
     jb.cut = cut;
     jb.steps = last_steps(p.dim);
     jb.rows = p.tokens;
@@ -1538,7 +1604,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
         const bool last = i + 1 == p.pieces;
         MmaArgs m{};
         if (!logits_job(&m, from, cut_logits(p.tokens, words, p.dim), w0, words) ||
-            !make_out(&m.job.out, dz, false, words, p.tokens, p.piece, 1))
+            !make_out(&m.job[0].out, dz, false, words, p.tokens, p.piece, 1))
             return cudaErrorInvalidValue;
         m.row = f.factor;
         m.words = f.words;
@@ -1549,72 +1615,87 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
         e = r.k > 0 ? launch_logits<kDz, true>(m, s) : launch_logits<kDz, false>(m, s);
         if (e != cudaSuccess) return e;
 
+        // the two products of dz: in one launch, but for few tokens' d_hidden
+        MmaArgs h{}, few{};
+        int jobs = 0, splits_h = 0, used_h = 0, splits_w = 0;
+        uint16_t *out_w = nullptr;
+        float *slab_h = reinterpret_cast<float *>(a.ws + p.slab_h);
+        float *slab_w = reinterpret_cast<float *>(a.ws + p.slab_w);
+        bool f32_h = false;
+        auto join_h = [&] {
+            launch_small(k_head_slabs, ceil_div(p.tokens * p.dim, 2048), 256, 0, s, slab_h,
+                         p.pieces > 1 ? splits_h : used_h, p.tokens * p.dim, p.tokens, p.dim,
+                         a.d_hidden, a.d_hidden_stride);
+            return cudaGetLastError();
+        };
         if (a.d_hidden) {
-            MmaArgs h{};
-            Job &jb = h.job;
-            jb.cut = cut_d_hidden(p.tokens, p.dim, p.piece);
-            const int splits = jb.cut.splits;
+            const Cut cut = cut_d_hidden(p.tokens, p.dim, p.piece);
+            Job &jb = cut.swap ? few.job[0] : h.job[jobs++];
+            jb.cut = cut;
+            splits_h = cut.splits;
             jb.cut.k_tiles = (int32_t)ceil_div(words, kBK);
-            jb.cut.splits = (int32_t)ceil_div(jb.cut.k_tiles, jb.cut.k_chunk);
+            used_h = jb.cut.splits = (int32_t)ceil_div(jb.cut.k_tiles, jb.cut.k_chunk);
             jb.steps = last_steps(words);
+            jb.box_k = kBK;
             jb.n_fast = 1;
             jb.rows = p.tokens;
             jb.cols = p.dim;
-            jb.out_f32 = jb.cut.swap || splits > 1 || p.pieces > 1;
+            jb.out_f32 = f32_h = cut.swap || splits_h > 1 || p.pieces > 1;
             jb.add = i > 0;
-            float *slab = reinterpret_cast<float *>(a.ws + p.slab_h);
+            jb.out_at = a.d_hidden;
+            jb.out_pitch = a.d_hidden_stride;
             bool ok;
-            if (jb.cut.swap) {
+            if (cut.swap) {
                 jb.a_k = (int32_t)w0;
                 ok = make_map(&jb.a, a.weight, p.dim, p.vocab, a.weight_stride, kBK) &&
-                     make_map(&jb.b, dz, words, p.tokens, p.piece, jb.cut.bn);
+                     make_map(&jb.b, dz, words, p.tokens, p.piece, cut.bn);
             } else {
                 jb.b_k = (int32_t)w0;
                 ok = make_map(&jb.a, dz, words, p.tokens, p.piece, 128) &&
                      make_map(&jb.b, a.weight, p.dim, p.vocab, a.weight_stride, kBK);
             }
-            ok = ok && (jb.out_f32 ? make_out(&jb.out, slab, true, p.dim, p.tokens, p.dim, splits)
-                                   : make_out(&jb.out, a.d_hidden, false, p.dim, p.tokens,
-                                              a.d_hidden_stride, 1));
-            jb.out_at = a.d_hidden;
-            jb.out_pitch = a.d_hidden_stride;
+            ok = ok && (f32_h ? make_out(&jb.out, slab_h, true, p.dim, p.tokens, p.dim, splits_h)
+                              : make_out(&jb.out, a.d_hidden, false, p.dim, p.tokens,
+                                         a.d_hidden_stride, 1));
             if (!ok) return cudaErrorInvalidValue;
-            if ((e = launch_d_hidden(h, s)) != cudaSuccess) return e;
-            if (last && jb.out_f32) {
-                launch_small(k_head_slabs, ceil_div(p.tokens * p.dim, 2048), 256, 0, s, slab,
-                             p.pieces > 1 ? splits : jb.cut.splits, p.tokens * p.dim, p.tokens,
-                             p.dim, a.d_hidden, a.d_hidden_stride);
-                if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            if (cut.swap) {
+                if ((e = launch_d_hidden_few(few, s)) != cudaSuccess) return e;
+                if (last && (e = join_h()) != cudaSuccess) return e;
             }
         }
         if (a.d_weight) {
-            MmaArgs g{};
-            Job &jb = g.job;
+            Job &jb = h.job[jobs++];
             jb.cut = cut_d_weight(p.tokens, p.dim, p.piece);
-            jb.cut.m_tiles = (int32_t)ceil_div(words, 128 * jb.cut.cg);
+            splits_w = jb.cut.splits;
+            jb.cut.m_tiles = (int32_t)ceil_div(words, 256);
             jb.steps = last_steps(p.tokens);
+            jb.a_mn = 1;
+            // few tokens: boxes of the rows that the products read
+            jb.box_k = p.tokens < kBK ? jb.steps * 16 : kBK;
             jb.n_fast = 1;
             jb.rows = words;
             jb.cols = p.dim;
-            jb.out_f32 = jb.cut.splits > 1;
-            float *slab = reinterpret_cast<float *>(a.ws + p.slab_w);
-            uint16_t *out = a.d_weight + w0 * a.d_weight_stride;
-            jb.out_at = out;
+            jb.out_f32 = splits_w > 1;
+            out_w = a.d_weight + w0 * a.d_weight_stride;
+            jb.out_at = out_w;
             jb.out_pitch = a.d_weight_stride;
-            // few tokens: boxes of the rows that the products read
-            jb.box_k = p.tokens < kBK ? jb.steps * 16 : kBK;
             if (!make_map(&jb.a, dz, words, p.tokens, p.piece, jb.box_k) ||
                 !make_map(&jb.b, hidden, p.dim, p.tokens, p.hidden_pitch, jb.box_k) ||
-                !(jb.out_f32
-                      ? make_out(&jb.out, slab, true, p.dim, words, p.dim, jb.cut.splits)
-                      : make_out(&jb.out, out, false, p.dim, words, a.d_weight_stride, 1)))
+                !(splits_w > 1
+                      ? make_out(&jb.out, slab_w, true, p.dim, words, p.dim, splits_w)
+                      : make_out(&jb.out, out_w, false, p.dim, words, a.d_weight_stride, 1)))
                 return cudaErrorInvalidValue;
-            if ((e = launch_d_weight(g, s)) != cudaSuccess) return e;
-            if (jb.out_f32) {
-                launch_small(k_head_slabs, ceil_div(words * p.dim, 2048), 256, 0, s, slab,
-                             jb.cut.splits, words * p.dim, words, p.dim, out, a.d_weight_stride);
-                if ((e = cudaGetLastError()) != cudaSuccess) return e;
-            }
+        }
+        if (jobs > 0) {
+            e = jobs == 2 ? launch_both(h, s)
+                          : h.job[0].a_mn ? launch_out<true>(h, s) : launch_out<false>(h, s);
+            if (e != cudaSuccess) return e;
+        }
+        if (last && f32_h && few.job[0].cut.swap == 0 && (e = join_h()) != cudaSuccess) return e;
+        if (splits_w > 1) {
+            launch_small(k_head_slabs, ceil_div(words * p.dim, 2048), 256, 0, s, slab_w, splits_w,
+                         words * p.dim, words, p.dim, out_w, a.d_weight_stride);
+            if ((e = cudaGetLastError()) != cudaSuccess) return e;
         }
     }
     return cudaSuccess;
