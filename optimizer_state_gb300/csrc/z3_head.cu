@@ -60,6 +60,7 @@ struct MmaArgs {
     // others `ahead` times, then round all.
     Job job[2];
     int32_t more, ahead;
+    int32_t early;         // the operands may be read before the kernel before has ended
     // kStats, kDz
     float beta;            // log2(e) / temperature: exponents are powers of two
     int32_t word0;         // the word of column 0
@@ -337,7 +338,10 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     tmem_fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_at) : "memory");
-    pdl_enter();  // barriers and tensor memory are set up beside the kernel before
+    // Barriers and tensor memory are set up beside the kernel before.  With `early`
+    // that one writes neither operand, and waited itself before it let this one
+    // start: loads and products begin, the epilogue waits.
+    if (!p.early || warp >= 2) pdl_enter();
     if (KIND == kStats && blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
 
     if (warp == 0 && lane == 0) {
@@ -1534,6 +1538,7 @@ cudaError_t launch_head_forward(const HeadArgs &a, cudaStream_t s) {
     if (r.k > 0 && (e = launch_lists(r, s)) != cudaSuccess) return e;
     MmaArgs m{};
     if (!logits_job(&m, a, p.logits, 0, p.vocab)) return cudaErrorInvalidValue;
+    m.early = r.k > 0;  // after the lists' launch
     m.part = reinterpret_cast<float2 *>(a.ws + p.part);
     m.z = reinterpret_cast<float *>(a.ws + p.z);
     m.done = reinterpret_cast<unsigned *>(a.ws + p.done);
@@ -1592,9 +1597,9 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
     launch_small(k_head_factors, p.tokens, 128, 0, s, f);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
-    // the copy's rows start on lines of 128 bytes, whatever the caller's do
+    // the copy's rows start on lines of 128 bytes, where the caller's do not
     HeadArgs from = a;
-    if (a.d_weight) {
+    if (a.d_weight && a.hidden_stride % 64 != 0) {
         from.hidden = hidden;
         from.hidden_stride = p.hidden_pitch;
     }
@@ -1606,6 +1611,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
         if (!logits_job(&m, from, cut_logits(p.tokens, words, p.dim), w0, words) ||
             !make_out(&m.job[0].out, dz, false, words, p.tokens, p.piece, 1))
             return cudaErrorInvalidValue;
+        m.early = i > 0 || from.hidden == a.hidden;  // else the copy is awaited
         m.row = f.factor;
         m.words = f.words;
         m.target = f.target;
