@@ -1097,10 +1097,12 @@ struct FactorArgs {
 // with zeros in the rows left out: what stands there may be anything, and 0 *
 // NaN would reach d_weight.  The copy costs 4 bytes a value, the targets' rows
 // of the weight 2 more: 13 us of the 2.2 ms at 8192 x 1024.
+// A warp to a token.
 __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
-    __shared__ float dots[4];
     pdl_enter();
-    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x % 32;
+    const int64_t t = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+    if (t >= a.row.tokens) return;
     int64_t word = -1;
     const Row state = state_of(a.row, t, &word);
     float f = a.scale;
@@ -1111,23 +1113,20 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
     if (state == kBad) f = NAN;
     const float lse = a.lse[t];
     const uint16_t *row = a.hidden + t * a.stride;
-    if (a.row.k == 0 && state == kCounts) {
-        const float part =
-            warp_sum(dot_part(row, a.weight + word * a.weight_stride, a.row.dim, threadIdx.x, 128));
-        if (threadIdx.x % 32 == 0) dots[threadIdx.x / 32] = part;
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) {
+    float z = lse;
+    if (a.row.k == 0 && state == kCounts)
+        z = warp_sum(dot_part(row, a.weight + word * a.weight_stride, a.row.dim, lane, 32));
+    if (lane == 0) {
         a.factor[t] = make_float2(f, __fmul_rn(lse, kLog2e));
         if (a.row.k == 0) {
             a.words[t] = state == kCounts ? (int32_t)word : -1;
-            const float z = (dots[0] + dots[1]) + (dots[2] + dots[3]);
-            a.target[t] = state == kCounts ? f * expm1f(z - lse) : 0.0f;
+            a.target[t] = f * expm1f(z - lse);
         }
     }
     if (a.copy == nullptr) return;
     const bool keep = f != 0.0f;
-    for (int64_t i = threadIdx.x * 8; i < a.row.dim; i += 128 * 8) {
+#pragma unroll 4
+    for (int64_t i = lane * 8; i < a.row.dim; i += 32 * 8) {
         uint4 x = make_uint4(0, 0, 0, 0);
         if (keep) x = ld8b(row + i);
         *reinterpret_cast<uint4 *>(a.copy + t * a.copy_stride + i) = x;
@@ -1594,7 +1593,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
     f.weight_stride = a.weight_stride;
     f.copy = a.d_weight ? hidden : nullptr;
     f.copy_stride = p.hidden_pitch;
-    launch_small(k_head_factors, p.tokens, 128, 0, s, f);
+    launch_small(k_head_factors, ceil_div(p.tokens, 4), 128, 0, s, f);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
 
     // the copy's rows start on lines of 128 bytes, where the caller's do not
