@@ -933,7 +933,7 @@ __device__ __forceinline__ float4 pairs_over_lanes(float4 v) {
 
 // Joins the tiles' maxima and sums, TOK tokens to a block, and finishes each
 // token's loss; the last block adds up the blocks' sums in their order.
-// Bound by latency: with 8192 tokens it reads 26 MB, eight loads of a thread in
+// Bound by latency: with 8192 tokens it reads 26 MB (10 us), eight loads of a thread in
 // flight.  Few tokens take a block each.
 template <int TOK>
 __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
@@ -958,18 +958,24 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
     }
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (live) {
+        const float2 *part = a.part + t;
         for (int n = slice; n < a.row.parts; n += 8 * kSlices) {
             float2 x[8];
 #pragma unroll
+            for (int i = 0; i < 8; ++i)  // none is left to a branch: all are on their way
+                x[i] = part[min(n + i * kSlices, a.row.parts - 1) * a.row.tokens];
+#pragma unroll
             for (int i = 0; i < 8; ++i)
-                x[i] = n + i * kSlices < a.row.parts
-                           ? a.part[(int64_t)(n + i * kSlices) * a.row.tokens + t]
-                           : make_float2(-INFINITY, 0.0f);
+                if (n + i * kSlices >= a.row.parts) x[i] = make_float2(-INFINITY, 0.0f);
+            float m = acc.x;
 #pragma unroll
-            for (int i = 4; i > 0; i /= 2)
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, x[i].x);
+            const float shift = m == -INFINITY ? 0.0f : m;
+            float sum = acc.y * exp2_fast(acc.x - shift);
 #pragma unroll
-                for (int j = 0; j < i; ++j) x[j] = join2(x[j], x[j + i]);
-            acc = join2(acc, x[0]);
+            for (int i = 0; i < 8; ++i)
+                sum = __fmaf_rn(x[i].y, exp2_fast(x[i].x - shift), sum);
+            acc = make_float2(m, sum);
         }
     }
 #pragma unroll
@@ -1406,7 +1412,7 @@ constexpr int64_t kPieceWords = 2048;
 // Up to the end of the last tile.
 int64_t first_pitch(const HeadPlan &p) { return ceil_div(p.vocab, 256) * (256 / kGrain) + 1; }
 
-int join_tokens(int64_t tokens) { return tokens <= kFew ? 1 : 8; }
+int join_tokens(int64_t tokens) { return tokens <= kFew ? 1 : 16; }
 
 RowArgs row_args(const HeadArgs &a) {
     const HeadPlan &p = a.plan;
@@ -1564,7 +1570,7 @@ cudaError_t launch_head_forward(const HeadArgs &a, cudaStream_t s) {
     if (join_tokens(p.tokens) == 1)
         launch_small(k_head_join<1>, p.tokens, kJoinThreads, 0, s, j);
     else
-        launch_small(k_head_join<8>, ceil_div(p.tokens, 8), kJoinThreads, 0, s, j);
+        launch_small(k_head_join<16>, ceil_div(p.tokens, 16), kJoinThreads, 0, s, j);
     return cudaGetLastError();
 }
 
