@@ -536,7 +536,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                     if (x.word >= 0 && c >= 0 && c < cols) walk.column[0] = (int)c;
                 }
             };
-            if constexpr (KIND != kOut && !SWAP) begin_row(ask(row));
+            if constexpr (KIND != kOut) begin_row(SWAP ? mine[0] : ask(row));
             if (ok) ok = mbar_wait(tfull(buf), (done >> 1) & 1);
             tmem_fence_after();
             const uint32_t d = tmem + ((uint32_t)(quad * 32) << 16) + buf * BN + c0;
@@ -549,6 +549,11 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             if (c0 >= BN || per == 0) release();
 #pragma unroll 1
             for (int i = 0; i < per && c0 + i < BN; i += kW) {
+                if (SWAP && i > 0) {
+                    row = row0 + i + lane;
+                    live = row < jb.rows;
+                    if constexpr (KIND != kOut) begin_row(mine[1]);
+                }
                 float v[kW / 32][32];
                 {
                     uint32_t bits[kW / 32][32];
@@ -582,9 +587,6 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[0][j]) : "r"(at(lane, j))
                                      : "memory");
                     __syncwarp();
-                    row = row0 + i + lane;
-                    live = row < jb.rows;
-                    if constexpr (KIND != kOut) begin_row(i == 0 ? mine[0] : mine[1]);
                     top = -INFINITY;
                     sum = 0.0f;
                 }
@@ -776,14 +778,15 @@ __device__ __forceinline__ float larger(float x, float y) {
 // where the entries of every kGrain words begin.  Entries of a negative word
 // or a logit of -Inf are left out (at the end, q = 0); a word beyond the
 // vocabulary spoils the row.  Equal words keep their order.
-// N threads to a token.  A warp takes lists of up to 64, which needs no barrier
-// of the CTA; an entry's place is the number of entries before it, counted
-// four words a load (a forward call with 777 lists of 19: 25.7 us, 26.5 by a
-// sort).  The counting grows as the square: longer lists take 128 threads and a
+// RANK, for lists of up to 64: an entry's place is the number of entries before
+// it, counted four words a load (a forward call with 777 lists of 19: 25.7 us,
+// 26.5 by a sort).  The counting grows as the square: longer lists take a
 // bitonic sort (501 lists of 200: 10.5 us, 13.5 by counting).
-template <int N>
+// N threads to a token: a warp, which needs no barrier of the CTA, for many short
+// lists; else 128 (92 lists of 48, with the beginnings of 643 grains each, take a
+// warp 11 us, 128 threads 7).
+template <int N, bool RANK>
 __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, int room) {
-    constexpr bool RANK = N == 32;
     extern __shared__ uint64_t keys[];
     __shared__ float red[2][kSortThreads / 32];
     pdl_enter();
@@ -1139,25 +1142,46 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
     }
 }
 
-// The splits' sums, in their order, rounded once to bf16.
+// The splits' sums, in a fixed order, rounded once to bf16.  Eight values to a
+// thread; SLICES threads share the splits of small results, whose time is the
+// loads' latency (8 x 336 by 50 splits: 9 us with one slice, 4.5 with eight).
+template <int SLICES>
 __global__ void __launch_bounds__(256) k_head_slabs(const float *slab, int splits, int64_t stride,
                                                     int64_t rows, int64_t cols, uint16_t *out,
                                                     int64_t pitch) {
+    constexpr int kWide = 256 / SLICES;
+    __shared__ float4 sums[SLICES > 1 ? 256 : 1][2];
     pdl_enter();
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-    if (i >= rows * cols) return;
-    const int64_t r = i / cols, c = i - r * cols;
-    float v[8] = {};
+    const int at = threadIdx.x % kWide, slice = threadIdx.x / kWide;
+    const int64_t i = ((int64_t)blockIdx.x * kWide + at) * 8;
+    const bool live = i < rows * cols;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+    auto add = [](float4 &x, const float4 &y) {
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+    };
+    if (live) {
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
-        const float4 *f = reinterpret_cast<const float4 *>(slab + s * stride + i);
-        const float4 x = f[0], y = f[1];
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+        for (int s = slice; s < splits; s += SLICES) {
+            const float4 *f = reinterpret_cast<const float4 *>(slab + s * stride + i);
+            add(a, f[0]);
+            add(b, f[1]);
+        }
     }
+    if constexpr (SLICES > 1) {
+        sums[threadIdx.x][0] = a;
+        sums[threadIdx.x][1] = b;
+        __syncthreads();
+        if (slice > 0) return;
+        for (int s = 1; s < SLICES; ++s) {
+            add(a, sums[s * kWide + at][0]);
+            add(b, sums[s * kWide + at][1]);
+        }
+    }
+    if (!live) return;
+    const int64_t r = i / cols, c = i - r * cols;
     *reinterpret_cast<uint4 *>(out + r * pitch + c) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                   pack_bf16x2(v[6], v[7]));
+        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                   pack_bf16x2(b.z, b.w));
 }
 
 // --------------------------------------------------------------------------
@@ -1441,11 +1465,13 @@ cudaError_t launch_lists(const RowArgs &r, cudaStream_t s) {
     const int room = (r.k + 3) / 4 * 4;
     int pow2 = 2;
     while (pow2 < r.k) pow2 *= 2;
-    if (r.k <= 64)
-        launch_small(k_head_lists<32>, ceil_div(r.tokens, kN / 32), kN, kN / 32 * room * 12, s, r,
-                     room);
+    if (r.k <= 64 && r.tokens > 1024)
+        launch_small(k_head_lists<32, true>, ceil_div(r.tokens, kN / 32), kN, kN / 32 * room * 12,
+                     s, r, room);
+    else if (r.k <= 64)
+        launch_small(k_head_lists<kN, true>, r.tokens, kN, room * 12, s, r, room);
     else
-        launch_small(k_head_lists<kN>, r.tokens, kN, pow2 * 8, s, r, pow2);
+        launch_small(k_head_lists<kN, false>, r.tokens, kN, pow2 * 8, s, r, pow2);
     return cudaGetLastError();
 }
 
@@ -1455,6 +1481,18 @@ void fill_lists(MmaArgs *m, const RowArgs &r) {
     m->q = r.q;
     m->first = r.first;
     m->first_pitch = r.first_pitch;
+}
+
+cudaError_t launch_slabs(const float *slab, int splits, int64_t rows, int64_t cols, uint16_t *out,
+                         int64_t pitch, cudaStream_t s) {
+    const int64_t n = rows * cols;
+    if (splits >= 8)
+        launch_small(k_head_slabs<8>, ceil_div(n, 256), 256, 0, s, slab, splits, n, rows, cols, out,
+                     pitch);
+    else
+        launch_small(k_head_slabs<1>, ceil_div(n, 2048), 256, 0, s, slab, splits, n, rows, cols,
+                     out, pitch);
+    return cudaGetLastError();
 }
 
 int last_steps(int64_t k) { return (int)ceil_div(k - (ceil_div(k, kBK) - 1) * kBK, 16); }
@@ -1634,10 +1672,8 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
         float *slab_w = reinterpret_cast<float *>(a.ws + p.slab_w);
         bool f32_h = false;
         auto join_h = [&] {
-            launch_small(k_head_slabs, ceil_div(p.tokens * p.dim, 2048), 256, 0, s, slab_h,
-                         p.pieces > 1 ? splits_h : used_h, p.tokens * p.dim, p.tokens, p.dim,
-                         a.d_hidden, a.d_hidden_stride);
-            return cudaGetLastError();
+            return launch_slabs(slab_h, p.pieces > 1 ? splits_h : used_h, p.tokens, p.dim,
+                                a.d_hidden, a.d_hidden_stride, s);
         };
         if (a.d_hidden) {
             const Cut cut = cut_d_hidden(p.tokens, p.dim, p.piece);
@@ -1703,11 +1739,9 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
             if (e != cudaSuccess) return e;
         }
         if (last && f32_h && few.job[0].cut.swap == 0 && (e = join_h()) != cudaSuccess) return e;
-        if (splits_w > 1) {
-            launch_small(k_head_slabs, ceil_div(words * p.dim, 2048), 256, 0, s, slab_w, splits_w,
-                         words * p.dim, words, p.dim, out_w, a.d_weight_stride);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        }
+        if (splits_w > 1 && (e = launch_slabs(slab_w, splits_w, words, p.dim, out_w,
+                                              a.d_weight_stride, s)) != cudaSuccess)
+            return e;
     }
     return cudaSuccess;
 }
