@@ -349,3 +349,31 @@ def test_gradients_against_differences(k):
         value, bound = c.reference()["d_" + name]
         got = float((t["d_" + name].double() * u).sum())
         assert abs(got - slope) <= float((bound * u.abs()).sum()) + 2.0 ** -18
+
+
+@pytest.mark.parametrize("k", [0, 3])
+def test_offsets_beyond_32_bits(k):
+    """More logits than 2^31, in chunks of tokens against the reference."""
+    n, v, d = 70001, 40009, 24
+    assert n * v > 2 ** 31
+    c = Case(n, v, d, k=k, weighted=True)
+    t, ws = c.outputs(), c.workspace()
+    c.forward(t, ws)
+    c.grad(t, ws, mean=False, scale=1e-3)
+    torch.cuda.synchronize()
+    weight, bound = (torch.zeros(v, d, dtype=torch.float64, device="cuda") for _ in range(2))
+    total = torch.zeros(2, dtype=torch.float64, device="cuda")
+    slack = torch.zeros(2, dtype=torch.float64, device="cuda")
+    for first in range(0, n, 10000):
+        rows = slice(first, min(n, first + 10000))
+        part = [None if x is None else x[rows] for x in (c.targets, c.index, c.teacher)]
+        ref = reference(c.hidden[rows], c.weight, *part, c.tau, c.weights[rows], scale=1e-3,
+                        mean=False)
+        assert outside({x: t[x][rows] for x in ("loss", "lse", "d_hidden")}, ref) == {}
+        weight += ref["d_weight"][0]
+        bound += ref["d_weight"][1]
+        total += ref["total"][0]
+        slack += ref["total"][1]
+    assert outside(dict(d_weight=t["d_weight"], total=t["total"]),
+                   dict(d_weight=(weight, bound), total=(total, slack))) == {}
+    assert all(x.intact() for x in c.o.values())
