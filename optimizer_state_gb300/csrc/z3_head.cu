@@ -54,6 +54,43 @@ struct Job {
     int64_t rows, cols;    // tokens x words, or the rows and columns of kOut's result
 };
 
+// The splits' sums of a result [rows][cols], rounded once to bf16.
+struct Slabs {
+    const float *slab;     // [splits][rows][cols]; null: none to join
+    int32_t splits;
+    int64_t rows, cols;
+    uint16_t *out;
+    int64_t pitch;
+};
+
+struct Sum8 {
+    float4 a, b;
+    __device__ __forceinline__ Sum8() : a(make_float4(0.0f, 0.0f, 0.0f, 0.0f)), b(a) {}
+    __device__ __forceinline__ void add(const float4 &x, const float4 &y) {
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+        b.x += y.x; b.y += y.y; b.z += y.z; b.w += y.w;
+    }
+};
+
+// Every `step`-th split's eight values from i on, `first` the first.
+__device__ __forceinline__ Sum8 sum_splits(const Slabs &p, int64_t i, int first, int step) {
+    Sum8 x;
+    const int64_t stride = p.rows * p.cols;
+#pragma unroll 8
+    for (int s = first; s < p.splits; s += step) {
+        const float4 *f = reinterpret_cast<const float4 *>(p.slab + s * stride + i);
+        x.add(f[0], f[1]);
+    }
+    return x;
+}
+
+__device__ __forceinline__ void store_sum(const Slabs &p, int64_t i, const Sum8 &x) {
+    const int64_t r = i / p.cols, c = i - r * p.cols;
+    *reinterpret_cast<uint4 *>(p.out + r * p.pitch + c) =
+        make_uint4(pack_bf16x2(x.a.x, x.a.y), pack_bf16x2(x.a.z, x.a.w),
+                   pack_bf16x2(x.b.x, x.b.y), pack_bf16x2(x.b.z, x.b.w));
+}
+
 struct MmaArgs {
     // JOINT: the first product's tiles go round the groups, which leaves the first
     // `more` groups with one more than the others.  The second's go round the
@@ -61,6 +98,7 @@ struct MmaArgs {
     Job job[2];
     int32_t more, ahead;
     int32_t early;         // the operands may be read before the kernel before has ended
+    Slabs join;            // kOut without SWAP: what the launch before left to join
     // kStats, kDz
     float beta;            // log2(e) / temperature: exponents are powers of two
     int32_t word0;         // the word of column 0
@@ -473,6 +511,12 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             for (int o = 4; o > 0; o /= 2) z += __shfl_xor_sync(~0u, z, o);
             if (counts && lane % 8 == 0) p.z[t] = z;
         }
+    } else if (KIND == kOut && !SWAP && (warp == 2 || warp == 3)) {
+        // few tokens' d_hidden, beside the tiles of d_weight
+        if (p.join.slab != nullptr)
+            for (int64_t i = ((int64_t)blockIdx.x * 64 + threadIdx.x - 64) * 8;
+                 i < p.join.rows * p.join.cols; i += (int64_t)gridDim.x * 64 * 8)
+                store_sum(p.join, i, sum_splits(p.join, i, 0, 1));
     } else if (warp >= 4) {
         const int quad = warp % 4;  // its 32 lanes of tensor memory
         const int half = (warp - 4) / 4;
@@ -1147,46 +1191,27 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
     }
 }
 
-// The splits' sums, in a fixed order, rounded once to bf16.  Eight values to a
-// thread; SLICES threads share the splits of small results, whose time is the
-// loads' latency (8 x 336 by 50 splits: 9 us with one slice, 4.5 with eight).
+// The splits' sums, in a fixed order.  Eight values to a thread; SLICES threads
+// share the splits of small results, whose time is the loads' latency (8 x 336 by
+// 50 splits: 9 us with one slice, 4.5 with eight).
 template <int SLICES>
-__global__ void __launch_bounds__(256) k_head_slabs(const float *slab, int splits, int64_t stride,
-                                                    int64_t rows, int64_t cols, uint16_t *out,
-                                                    int64_t pitch) {
+__global__ void __launch_bounds__(256) k_head_slabs(const Slabs p) {
     constexpr int kWide = 256 / SLICES;
     __shared__ float4 sums[SLICES > 1 ? 256 : 1][2];
     pdl_enter();
     const int at = threadIdx.x % kWide, slice = threadIdx.x / kWide;
     const int64_t i = ((int64_t)blockIdx.x * kWide + at) * 8;
-    const bool live = i < rows * cols;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-    auto add = [](float4 &x, const float4 &y) {
-        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-    };
-    if (live) {
-#pragma unroll 8
-        for (int s = slice; s < splits; s += SLICES) {
-            const float4 *f = reinterpret_cast<const float4 *>(slab + s * stride + i);
-            add(a, f[0]);
-            add(b, f[1]);
-        }
-    }
+    const bool live = i < p.rows * p.cols;
+    Sum8 x;
+    if (live) x = sum_splits(p, i, slice, SLICES);
     if constexpr (SLICES > 1) {
-        sums[threadIdx.x][0] = a;
-        sums[threadIdx.x][1] = b;
+        sums[threadIdx.x][0] = x.a;
+        sums[threadIdx.x][1] = x.b;
         __syncthreads();
         if (slice > 0) return;
-        for (int s = 1; s < SLICES; ++s) {
-            add(a, sums[s * kWide + at][0]);
-            add(b, sums[s * kWide + at][1]);
-        }
+        for (int s = 1; s < SLICES; ++s) x.add(sums[s * kWide + at][0], sums[s * kWide + at][1]);
     }
-    if (!live) return;
-    const int64_t r = i / cols, c = i - r * cols;
-    *reinterpret_cast<uint4 *>(out + r * pitch + c) =
-        make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
-                   pack_bf16x2(b.z, b.w));
+    if (live) store_sum(p, i, x);
 }
 
 // --------------------------------------------------------------------------
@@ -1488,15 +1513,12 @@ void fill_lists(MmaArgs *m, const RowArgs &r) {
     m->first_pitch = r.first_pitch;
 }
 
-cudaError_t launch_slabs(const float *slab, int splits, int64_t rows, int64_t cols, uint16_t *out,
-                         int64_t pitch, cudaStream_t s) {
-    const int64_t n = rows * cols;
-    if (splits >= 8)
-        launch_small(k_head_slabs<8>, ceil_div(n, 256), 256, 0, s, slab, splits, n, rows, cols, out,
-                     pitch);
+cudaError_t launch_slabs(const Slabs &p, cudaStream_t s) {
+    const int64_t n = p.rows * p.cols;
+    if (p.splits >= 8)
+        launch_small(k_head_slabs<8>, ceil_div(n, 256), 256, 0, s, p);
     else
-        launch_small(k_head_slabs<1>, ceil_div(n, 2048), 256, 0, s, slab, splits, n, rows, cols,
-                     out, pitch);
+        launch_small(k_head_slabs<1>, ceil_div(n, 2048), 256, 0, s, p);
     return cudaGetLastError();
 }
 
@@ -1676,10 +1698,7 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
         float *slab_h = reinterpret_cast<float *>(a.ws + p.slab_h);
         float *slab_w = reinterpret_cast<float *>(a.ws + p.slab_w);
         bool f32_h = false;
-        auto join_h = [&] {
-            return launch_slabs(slab_h, p.pieces > 1 ? splits_h : used_h, p.tokens, p.dim,
-                                a.d_hidden, a.d_hidden_stride, s);
-        };
+        Slabs join_h{};
         if (a.d_hidden) {
             const Cut cut = cut_d_hidden(p.tokens, p.dim, p.piece);
             Job &jb = cut.swap ? few.job[0] : h.job[jobs++];
@@ -1710,9 +1729,16 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
                               : make_out(&jb.out, a.d_hidden, false, p.dim, p.tokens,
                                          a.d_hidden_stride, 1));
             if (!ok) return cudaErrorInvalidValue;
+            if (last && f32_h)
+                join_h = Slabs{slab_h,     p.pieces > 1 ? splits_h : used_h,
+                               p.tokens,   p.dim,
+                               a.d_hidden, a.d_hidden_stride};
             if (cut.swap) {
                 if ((e = launch_d_hidden_few(few, s)) != cudaSuccess) return e;
-                if (last && (e = join_h()) != cudaSuccess) return e;
+                if (a.d_weight) {  // joined beside it
+                    h.join = join_h;
+                    join_h = Slabs{};
+                }
             }
         }
         if (a.d_weight) {
@@ -1743,9 +1769,10 @@ cudaError_t launch_head_grad(const HeadArgs &a, cudaStream_t s) {
                           : h.job[0].a_mn ? launch_out<true>(h, s) : launch_out<false>(h, s);
             if (e != cudaSuccess) return e;
         }
-        if (last && f32_h && few.job[0].cut.swap == 0 && (e = join_h()) != cudaSuccess) return e;
-        if (splits_w > 1 && (e = launch_slabs(slab_w, splits_w, words, p.dim, out_w,
-                                              a.d_weight_stride, s)) != cudaSuccess)
+        if (join_h.slab != nullptr && (e = launch_slabs(join_h, s)) != cudaSuccess) return e;
+        if (splits_w > 1 &&
+            (e = launch_slabs(Slabs{slab_w, splits_w, words, p.dim, out_w, a.d_weight_stride},
+                              s)) != cudaSuccess)
             return e;
     }
     return cudaSuccess;
