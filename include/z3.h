@@ -441,9 +441,9 @@ typedef struct z3_head {
     const float *weights; /* [tokens], or NULL */
 } z3_head;
 
-/* Bytes of the workspace of the calls below, for at most these sizes' call:
- * k the length of the teacher's lists (0: cross entropy), grads != 0 with the
- * gradient calls.  What it holds before a call does not matter and nothing is
+/* Bytes of the workspace of the calls below at these sizes (smaller ones may
+ * need more): k the length of the teacher's lists (0: cross entropy), grads !=
+ * 0 with the gradient calls.  What it holds before a call does not matter and nothing is
  * kept in it between calls; calls that may overlap on the GPU, captured ones
  * among them, need one each. */
 z3_status z3_head_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, int32_t k,

@@ -593,7 +593,8 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             auto release = [&] {
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_cta(tempty(buf), leader));
+                if (lane == 0)
+                    mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_cta(tempty(buf), leader));
             };
             if (c0 >= BN || per == 0) release();
 #pragma unroll 1
@@ -707,7 +708,8 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                     uint32_t w[kW / 2];
 #pragma unroll
                     for (int j = 0; j < kW / 2; ++j)
-                        w[j] = none ? 0u : pack_bf16x2(v[j / 16][2 * j % 32], v[j / 16][2 * j % 32 + 1]);
+                        w[j] = none ? 0u
+                                    : pack_bf16x2(v[j / 16][2 * j % 32], v[j / 16][2 * j % 32 + 1]);
                     // the few words that the token asks for, in place of what was
                     // written for them
                     auto patch = [&](uint16_t *at, int swizzle) {
@@ -760,7 +762,8 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
                             st_shared(stage + lane * 128 + ((j ^ (lane & 7)) << 4),
-                                      __float_as_uint(v[h][4 * j]), __float_as_uint(v[h][4 * j + 1]),
+                                      __float_as_uint(v[h][4 * j]),
+                                      __float_as_uint(v[h][4 * j + 1]),
                                       __float_as_uint(v[h][4 * j + 2]),
                                       __float_as_uint(v[h][4 * j + 3]));
                         store_box(jb, stage, lane, col0 + c + 32 * h, SWAP ? row0 + i : row0,
@@ -1326,7 +1329,13 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG > 1 ? 2 : 1;
-    (void)cudaLaunchKernelEx(&cfg, kernel, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e == cudaErrorInvalidValue) {  // the device was reset since
+        (void)cudaGetLastError();
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        (void)cudaLaunchKernelEx(&cfg, kernel, p);
+    }
     return cudaGetLastError();
 }
 

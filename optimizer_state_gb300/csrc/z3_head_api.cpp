@@ -158,10 +158,11 @@ z3_status gradient(const char *fn, const char *range, const z3_head *h, const vo
     z3_status st = check_head(fn, h, targets, index_bytes, t, true, ws, ws_bytes, &a, spans);
     if (st != Z3_OK) return st;
     int64_t hb = 0, wb = 0;
-    if (d_hidden && (st = check_matrix(fn, "d_hidden", h->tokens, h->dim, d_hidden_stride, &hb)) != Z3_OK)
-        return st;
-    if (d_weight && (st = check_matrix(fn, "d_weight", h->vocab, h->dim, d_weight_stride, &wb)) != Z3_OK)
-        return st;
+    if (d_hidden)
+        st = check_matrix(fn, "d_hidden", h->tokens, h->dim, d_hidden_stride, &hb);
+    if (st == Z3_OK && d_weight)
+        st = check_matrix(fn, "d_weight", h->vocab, h->dim, d_weight_stride, &wb);
+    if (st != Z3_OK) return st;
     spans[6] = {lse, 4 * h->tokens, "lse", 4, false};
     spans[7] = {total, total ? 8 : 0, "total", 4, false};
     spans[8] = {d_hidden, hb, "d_hidden", 16, true};
