@@ -844,9 +844,10 @@ __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, in
     pdl_enter();
     const int tid = threadIdx.x % N;
     const int64_t t = (int64_t)blockIdx.x * (kSortThreads / N) + threadIdx.x / N;
-    // (word, place); by rank the words alone stand behind them, in the order given
-    uint64_t *key = keys + threadIdx.x / N * (RANK ? room + room / 2 : room);
-    uint32_t *given = reinterpret_cast<uint32_t *>(key + room);
+    // (word, place); behind them, in the order given, the logits and by rank the words
+    uint64_t *key = keys + threadIdx.x / N * (RANK ? 2 * room : room + room / 2);
+    float *logits = reinterpret_cast<float *>(key + room);
+    uint32_t *given = reinterpret_cast<uint32_t *>(logits + room);
     if (t >= a.tokens) return;  // all threads of the token
     auto sync = [] {
         if constexpr (N == 32) __syncwarp(); else __syncthreads();
@@ -863,6 +864,7 @@ __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, in
         if (i < a.k) {
             const int64_t w = load_index(a.index, a.index_bytes, t * a.k + i);
             const float x = logit(i);
+            logits[i] = x;
             if (w >= a.vocab) {
                 bad = true;
             } else if (w >= 0 && x != -INFINITY) {
@@ -923,7 +925,7 @@ __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, in
     const float inv = __fdiv_rn(1.0f, a.temperature);
     float sum = 0.0f;
     for (int i = tid; i < count; i += N)
-        sum += exp2f((logit((int)(uint32_t)key[i]) - top) * inv * kLog2e);
+        sum += exp2f((logits[(uint32_t)key[i]] - top) * inv * kLog2e);
     for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
     if constexpr (N > 32) {
         if (tid % 32 == 0) red[1][tid / 32] = sum;
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(kSortThreads) k_head_lists(const RowArgs a, in
     for (int i = tid; i < a.k; i += N) {
         a.list[t * a.k + i] = (int32_t)(key[i] >> 32);
         a.q[t * a.k + i] =
-            i < count ? exp2f((logit((int)(uint32_t)key[i]) - top) * inv * kLog2e) * norm : 0.0f;
+            i < count ? exp2f((logits[(uint32_t)key[i]] - top) * inv * kLog2e) * norm : 0.0f;
     }
     for (int n = tid; n < a.first_pitch; n += N)
         a.first[t * a.first_pitch + n] =
@@ -1505,12 +1507,12 @@ cudaError_t launch_lists(const RowArgs &r, cudaStream_t s) {
     int pow2 = 2;
     while (pow2 < r.k) pow2 *= 2;
     if (r.k <= 64 && r.tokens > 1024)
-        launch_small(k_head_lists<32, true>, ceil_div(r.tokens, kN / 32), kN, kN / 32 * room * 12,
+        launch_small(k_head_lists<32, true>, ceil_div(r.tokens, kN / 32), kN, kN / 32 * room * 16,
                      s, r, room);
     else if (r.k <= 64)
-        launch_small(k_head_lists<kN, true>, r.tokens, kN, room * 12, s, r, room);
+        launch_small(k_head_lists<kN, true>, r.tokens, kN, room * 16, s, r, room);
     else
-        launch_small(k_head_lists<kN, false>, r.tokens, kN, pow2 * 8, s, r, pow2);
+        launch_small(k_head_lists<kN, false>, r.tokens, kN, pow2 * 12, s, r, pow2);
     return cudaGetLastError();
 }
 
