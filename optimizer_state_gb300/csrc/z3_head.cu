@@ -299,9 +299,9 @@ __device__ __forceinline__ void put64(uint32_t stage, int lane, const uint32_t (
 // x 32 values over in shared memory, after which thread, row and columns mean
 // what they mean without SWAP.
 // PAIRS = 2: clusters of two CTA pairs, which take the same columns of two row
-// tiles.  Each pair loads half of b's tile for both, so that L2 is read for 48
-// bytes a clock and SM instead of 64; it gives about 50.  In exchange only 36
-// such clusters, 144 SMs, fit the GPU.
+// tiles.  Each pair loads half of b's tile for both, so that L2 hands out a
+// quarter less.  In exchange only 36 such clusters, 144 SMs, fit the GPU
+// (cut_logits says where it pays).
 // Bound by the tensor cores: 256 x 256 values of one k tile take 528 clocks, 512
 // at their nominal rate.  6 stages of 64 values of K hide L2's latency; the
 // epilogue takes 2,800 clocks a tile beside the next one's products (8,450 at
