@@ -419,8 +419,11 @@ z3_status z3_model_step_clipped(const z3_unit *units, const z3_clip_unit *clips,
  * likely target's loss keeps its digits.  dz, the gradient of the
  * logits, is rounded to bf16 (the operand type of the two products that
  * follow, whose sums are binary32), each result once more at its end.  Results
- * depend on the sizes only: the same call gives the same bits.  A head whose
- * logits are not finite has a NaN loss and gradient.
+ * depend on the sizes only: the same call gives the same bits.
+ *
+ * A token with a logit of NaN or +Inf has a NaN loss and lse, and its gradients
+ * are NaN; so has one whose target, or a listed word with q > 0, has a logit of
+ * -Inf.  Another word's logit of -Inf is a probability of 0.
  *
  * dim is a multiple of 8, at most 2^31 - 1024 as are tokens and vocab (a call
  * of 0 tokens writes total = {0, 0}, and zeros to d_weight); strides are in

@@ -998,6 +998,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
     constexpr int kWarps = kJoinThreads / 32;
     __shared__ float2 joined[kWarps][TOK];
     __shared__ float lists[kWarps][TOK];
+    __shared__ bool beyond[kWarps][TOK];
     __shared__ float4 warps[kWarps];
     __shared__ bool last;
     pdl_enter();
@@ -1051,7 +1052,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
     if (a.row.k == 0 && state == kCounts) {
         // the sums are without the target's term: loss = log(1 + the others / its)
         const float more = __fmaf_rn(-z, kLog2e, acc.x);
-        if (acc.y == 0.0f) {  // a vocabulary of one, or all others below binary32
+        if (!isfinite(z)) {  // of which the others' sums know nothing
+            lse = loss1 = NAN;
+        } else if (acc.y == 0.0f) {  // a vocabulary of one, or all others below binary32
             lse = z;
         } else if (more < 64.0f) {
             loss1 = log1pf(acc.y * exp2f(more));
@@ -1062,6 +1065,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
     }
     if (a.row.k > 0) {
         float part = 0.0f;
+        bool wild = false;  // a word with a share whose logit is not finite
         const float inv = __fdiv_rn(1.0f, a.row.temperature);
         if (state == kCounts) {
             for (int i = slice; i < a.row.k; i += 4 * kSlices) {
@@ -1075,12 +1079,21 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     // 0 log 0 = 0: an entry left out, or one whose q is below binary32
-                    if (q[j] != 0.0f) part += q[j] * (logf(q[j]) - x[j] * inv + lse);
+                    if (q[j] != 0.0f) {
+                        part += q[j] * (logf(q[j]) - x[j] * inv + lse);
+                        wild |= !isfinite(x[j]);
+                    }
             }
         }
 #pragma unroll
-        for (int o = 16; o >= TOK; o /= 2) part += __shfl_xor_sync(~0u, part, o);
-        if (threadIdx.x % 32 < TOK) lists[warp][tok] = part;
+        for (int o = 16; o >= TOK; o /= 2) {
+            part += __shfl_xor_sync(~0u, part, o);
+            wild |= __shfl_xor_sync(~0u, (int)wild, o) != 0;
+        }
+        if (threadIdx.x % 32 < TOK) {
+            lists[warp][tok] = part;
+            beyond[warp][tok] = wild;
+        }
         __syncthreads();
     }
     if (warp == 0) {
@@ -1090,8 +1103,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_head_join(const JoinArgs a) {
             if (state == kBad) {
                 loss = NAN;
             } else if (state == kCounts && a.row.k > 0) {
-                for (int w = 0; w < kWarps; ++w) loss += lists[w][tok];
-                loss *= a.row.temperature * a.row.temperature;
+                for (int w = 0; w < kWarps; ++w) {
+                    loss += lists[w][tok];
+                    if (beyond[w][tok]) lse = NAN;
+                }
+                loss = isnan(lse) ? NAN : loss * (a.row.temperature * a.row.temperature);
             } else if (state == kCounts) {
                 loss = loss1;
             }
