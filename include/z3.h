@@ -456,8 +456,8 @@ z3_status z3_head_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab, in
  *   lse[t] = log sum_j exp(z[t][j]);  loss[t] = lse[t] - z[t][targets[t]].
  * targets: int32 or int64 [tokens] (index_bytes 4 or 8).  A negative target
  * leaves the token out; one >= vocab reads nothing, and makes the token's loss
- * NaN and all gradients with it.  loss, lse (float [tokens]) and total (float
- * [2]) are written. */
+ * NaN and, unless its weight is 0, its row of d_hidden and d_weight with it.
+ * loss, lse (float [tokens]) and total (float [2]) are written. */
 z3_status z3_xent(const z3_head *head, const void *targets, int32_t index_bytes, float *loss,
                   float *lse, float *total, void *workspace, int64_t workspace_bytes,
                   z3_stream stream);
@@ -480,7 +480,8 @@ z3_status z3_xent_grad(const z3_head *head, const void *targets, int32_t index_b
  * dtype Z3_BF16 or Z3_F32, and the words that they belong to, int32 or int64
  * [tokens][k] (index_bytes 4 or 8).  1 <= k <= 1024.  An entry with a negative
  * index or a logit of -Inf is left out, and a token without any other; an
- * index >= vocab reads nothing and makes the token's loss and all gradients NaN.
+ * index >= vocab reads nothing and makes the token's loss NaN and, unless its
+ * weight is 0, its row of d_hidden and d_weight.
  * A word may stand in a list more than once: its shares add up. */
 typedef struct z3_teacher {
     const void *logits;

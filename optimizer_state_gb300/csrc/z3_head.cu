@@ -1186,10 +1186,12 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
     const Row state = state_of(a.row, t, &word);
     float f = a.scale;
     if (a.total) f = a.total[1] == 0.0f ? 0.0f : __fdiv_rn(f, a.total[1]);
-    if (a.row.weights && state != kLeftOut) f = __fmul_rn(f, a.row.weights[t]);
+    float w = state == kLeftOut ? 0.0f : 1.0f;
+    if (a.row.weights && state != kLeftOut) w = a.row.weights[t];
+    f = __fmul_rn(f, w);
     if (a.row.k > 0) f = __fmul_rn(f, a.row.temperature);
-    if (state == kLeftOut) f = 0.0f;
     if (state == kBad) f = NAN;
+    if (w == 0.0f) f = 0.0f;  // out of the gradients, whatever else there is
     const float lse = a.lse[t];
     const uint16_t *row = a.hidden + t * a.stride;
     float z = lse;
