@@ -173,10 +173,8 @@ struct Tile {
     int m, n, split;
 };
 
-template <int PAIRS>
-__device__ __forceinline__ Tile tile_of(const Job &jb, int item, int pair) {
-    const int m_tiles = (jb.cut.m_tiles + PAIRS - 1) / PAIRS;  // of a cluster
-    const int tiles = m_tiles * jb.cut.n_tiles;
+__device__ __forceinline__ Tile tile_of(const Job &jb, int item) {
+    const int tiles = jb.cut.m_tiles * jb.cut.n_tiles;
     Tile t;
     t.split = item / tiles;
     int i = item - t.split * tiles;
@@ -184,15 +182,14 @@ __device__ __forceinline__ Tile tile_of(const Job &jb, int item, int pair) {
         t.m = i / jb.cut.n_tiles;
         t.n = i - t.m * jb.cut.n_tiles;
     } else {
-        constexpr int kGroup = 32 / PAIRS;  // row tiles whose operand stays in L2
+        constexpr int kGroup = 32;  // row tiles whose operand stays in L2
         const int per = kGroup * jb.cut.n_tiles;
         const int g = i / per;
-        const int rows = min(kGroup, m_tiles - g * kGroup);
+        const int rows = min(kGroup, jb.cut.m_tiles - g * kGroup);
         i -= g * per;
         t.n = i / rows;
         t.m = g * kGroup + i - t.n * rows;
     }
-    t.m = t.m * PAIRS + pair;
     return t;
 }
 
@@ -298,10 +295,6 @@ __device__ __forceinline__ void put64(uint32_t stage, int lane, const uint32_t (
 // and N along tokens, so that the weight fills the tiles; a warp turns its 32
 // x 32 values over in shared memory, after which thread, row and columns mean
 // what they mean without SWAP.
-// PAIRS = 2: clusters of two CTA pairs, which take the same columns of two row
-// tiles.  Each pair loads half of b's tile for both, so that L2 hands out a
-// quarter less.  In exchange only 36 such clusters, 144 SMs, fit the GPU
-// (cut_logits says where it pays).
 // Bound by the tensor cores: 256 x 256 values of one k tile take 528 clocks, 512
 // at their nominal rate.  6 stages of 64 values of K hide L2's latency; the
 // epilogue takes 2,800 clocks a tile beside the next one's products (8,450 at
@@ -312,8 +305,7 @@ __device__ __forceinline__ void put64(uint32_t stage, int lane, const uint32_t (
 // AMN, BMN: an operand's rows run along M or N rather than K.
 // JOINT: d_hidden and d_weight in one launch, whose tiles fill each other's last
 // wave; a's rows run either way, by job.
-template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST,
-          bool JOINT>
+template <int CG, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST, bool JOINT>
 __global__ void __launch_bounds__(kMmaThreads, 1)
 k_head_mma(const __grid_constant__ MmaArgs p) {
     constexpr int S = stages<BN, CG>();
@@ -331,13 +323,9 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     auto tempty = [&](int i) { return bars + 8 * (2 * S + 2 + i); };
     const uint32_t tmem_at = bars + 8 * (2 * S + 4);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t place = CG == 1 ? 0 : cluster_rank();  // in the cluster
-    const uint32_t rank = place % CG;                      // in the pair
-    const int pair = place / CG;
-    const uint32_t leader = place - rank;
-    const int group = blockIdx.x / (CG * PAIRS), groups = gridDim.x / (CG * PAIRS);
-    const int items = (p.job[0].cut.m_tiles + PAIRS - 1) / PAIRS * p.job[0].cut.n_tiles *
-                      p.job[0].cut.splits;
+    const uint32_t rank = CG == 1 ? 0 : cluster_rank();  // in the pair
+    const int group = blockIdx.x / CG, groups = gridDim.x / CG;
+    const int items = p.job[0].cut.m_tiles * p.job[0].cut.n_tiles * p.job[0].cut.splits;
     [[maybe_unused]] const int second_items =
         JOINT ? p.job[1].cut.m_tiles * p.job[1].cut.n_tiles * p.job[1].cut.splits : 0;
     const int first_items = items > group ? (items - group + groups - 1) / groups : 0;
@@ -365,7 +353,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         tma_prefetch_map(&p.job[0].b);
         for (int i = 0; i < S; ++i) {
             mbar_init(full(i), 1);
-            mbar_init(empty(i), PAIRS);
+            mbar_init(empty(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull(i), 1);
@@ -376,7 +364,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     if (warp == 2) tmem_alloc<CG>(tmem_at, kCols);
     __syncwarp();
     tmem_fence_before();
-    group_sync<CG * PAIRS>();
+    group_sync<CG>();
     if constexpr (CG > 1) __syncthreads();
     tmem_fence_after();
     uint32_t tmem;
@@ -396,7 +384,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         const int b_boxes = BMN ? (bn / CG + 63) / 64 : 0;  // of 64 columns
         for (int n = 0; ok && take(n, &job, &item); ++n) {
             const Job &jb = p.job[JOINT ? job : 0];
-            const Tile t = tile_of<PAIRS>(jb, item, pair);
+            const Tile t = tile_of(jb, item);
             const bool a_mn = JOINT ? jb.a_mn != 0 : AMN;
             const uint32_t bytes =
                 KIND == kOut && !SWAP
@@ -413,7 +401,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 if (!ok) break;
                 const uint32_t a = base + stage * kStage, b = a + kA;
                 if (rank == 0) mbar_expect(full(stage), bytes);
-                const uint32_t bar = CG == 1 ? full(stage) : in_cta(full(stage), leader);
+                const uint32_t bar = CG == 1 ? full(stage) : in_cta(full(stage), 0);
                 const int ka = jb.a_k + kt * kBK, kb = jb.b_k + kt * kBK;
                 if (a_mn) {
                     for (int i = 0; i < 2; ++i)
@@ -421,11 +409,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 } else {
                     tma_load<CG>(a, &jb.a, bar, ka, m0);
                 }
-                if constexpr (PAIRS == 2) {  // half of it, for both pairs
-                    static_assert(PAIRS == 1 || !BMN);
-                    tma_load_many(b + pair * (bn / 4) * 128, &jb.b, bar, kb, n0 + pair * (bn / 4),
-                                  5 << rank);
-                } else if constexpr (BMN) {
+                if constexpr (BMN) {
                     for (int i = 0; i < b_boxes; ++i)
                         tma_load<CG>(b + i * (64 * kBK * 2), &jb.b, bar, n0 + 64 * i, kb);
                 } else {
@@ -453,7 +437,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         bool ok = true;
         for (int done = 0; ok && take(done, &job, &item); ++done) {
             const Job &jb = p.job[JOINT ? job : 0];
-            const Tile t = tile_of<PAIRS>(jb, item, pair);
+            const Tile t = tile_of(jb, item);
             const bool a_mn = JOINT ? jb.a_mn != 0 : AMN;
             const uint32_t idesc = mma_desc(128 * CG, bn, a_mn, BMN);
             const uint32_t step_a = a_mn ? 16 * 128 / 16 : 32 / 16;
@@ -476,7 +460,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
 #pragma unroll
                 for (int k = 0; k < decltype(steps)::value; ++k)
                     mma<CG>(d, da + k * step_a, db + k * kStepB, idesc, kt > k0 || k > 0);
-                mma_commit<CG>(empty(stage), PAIRS == 2 ? 15 : 3);
+                mma_commit<CG>(empty(stage));
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1;
@@ -490,7 +474,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 if (jb.steps == 2) product(whole, Steps<2>{});
                 if (jb.steps == 3) product(whole, Steps<3>{});
             }
-            if (ok) mma_commit<CG>(tfull(buf), 3 << leader);
+            if (ok) mma_commit<CG>(tfull(buf));
         }
     } else if (KIND == kStats && !LIST && (warp == 2 || warp == 3)) {
         // The targets' logits, summed with rounding: the tensor cores cut off, 1e-6
@@ -549,7 +533,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
         bool ok = true;
         for (int done = 0; take(done, &job, &item); ++done) {
             const Job &jb = p.job[JOINT ? job : 0];
-            const Tile t = tile_of<PAIRS>(jb, item, pair);
+            const Tile t = tile_of(jb, item);
             const int buf = done & 1;
             // this warp's first row and column; with SWAP its columns are those of the
             // quarter, and its rows go on with each 32
@@ -594,7 +578,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_cta(tempty(buf), leader));
+                    mbar_arrive_cluster(CG == 1 ? tempty(buf) : in_cta(tempty(buf), 0));
             };
             if (c0 >= BN || per == 0) release();
 #pragma unroll 1
@@ -787,7 +771,7 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
-    group_sync<CG * PAIRS>();
+    group_sync<CG>();
     tmem_fence_after();
     if (warp == 2) tmem_free<CG>(tmem, kCols);
 }
@@ -1312,17 +1296,14 @@ bool make_out(CUtensorMap *m, void *p, bool f32, int64_t cols, int64_t rows, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters that the GPU holds at a time.
-int64_t room(int cg, int pairs) { return pairs == 2 ? 36 : kHeadSMs / cg; }
+// CTAs or pairs that the GPU holds at a time.
+int64_t room(int cg) { return kHeadSMs / cg; }
 
-int64_t tiles(const Cut &c, int pairs = 1) {
-    return ceil_div(c.m_tiles, pairs) * c.n_tiles * c.splits;
-}
+int64_t tiles(const Cut &c) { return (int64_t)c.m_tiles * c.n_tiles * c.splits; }
 
-template <int CG, int PAIRS, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST,
-          bool JOINT = false>
+template <int CG, int BN, bool SWAP, bool AMN, bool BMN, Kind KIND, bool LIST, bool JOINT = false>
 cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
-    auto *kernel = k_head_mma<CG, PAIRS, BN, SWAP, AMN, BMN, KIND, LIST, JOINT>;
+    auto *kernel = k_head_mma<CG, BN, SWAP, AMN, BMN, KIND, LIST, JOINT>;
     // once for each device (1 us of host time)
     static std::atomic<uint64_t> allowed{0};
     int device;
@@ -1334,10 +1315,9 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         allowed.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int64_t items =
-        tiles(p.job[0].cut, PAIRS) + (JOINT ? tiles(p.job[1].cut) : 0);
+    const int64_t items = tiles(p.job[0].cut) + (JOINT ? tiles(p.job[1].cut) : 0);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(CG * PAIRS * std::min<int64_t>(items, room(CG, PAIRS))));
+    cfg.gridDim = dim3((unsigned)(CG * std::min<int64_t>(items, room(CG))));
     cfg.blockDim = dim3(kMmaThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
@@ -1345,7 +1325,7 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG * PAIRS;
+    attr[1].val.clusterDim.x = CG;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = CG > 1 ? 2 : 1;
@@ -1363,17 +1343,16 @@ cudaError_t launch_mma(const MmaArgs &p, cudaStream_t s) {
 template <Kind KIND, bool LIST>
 cudaError_t launch_logits(const MmaArgs &p, cudaStream_t s) {
     const Cut &c = p.job[0].cut;
-    if (c.pairs == 2) return launch_mma<2, 2, 256, false, false, false, KIND, LIST>(p, s);
-    if (!c.swap) return launch_mma<2, 1, 256, false, false, false, KIND, LIST>(p, s);
-    if (c.bn == 32) return launch_mma<1, 1, 32, true, false, false, KIND, LIST>(p, s);
-    return launch_mma<1, 1, 128, true, false, false, KIND, LIST>(p, s);
+    if (!c.swap) return launch_mma<2, 256, false, false, false, KIND, LIST>(p, s);
+    if (c.bn == 32) return launch_mma<1, 32, true, false, false, KIND, LIST>(p, s);
+    return launch_mma<1, 128, true, false, false, KIND, LIST>(p, s);
 }
 
 // One product of dz; or both, in any order.
 template <bool AMN>
 cudaError_t launch_out(const MmaArgs &p, cudaStream_t s) {
-    return p.job[0].cut.bn > 128 ? launch_mma<2, 1, 256, false, AMN, true, kOut, false>(p, s)
-                                 : launch_mma<2, 1, 128, false, AMN, true, kOut, false>(p, s);
+    return p.job[0].cut.bn > 128 ? launch_mma<2, 256, false, AMN, true, kOut, false>(p, s)
+                                 : launch_mma<2, 128, false, AMN, true, kOut, false>(p, s);
 }
 
 cudaError_t launch_both(MmaArgs &p, cudaStream_t s) {
@@ -1381,7 +1360,7 @@ cudaError_t launch_both(MmaArgs &p, cudaStream_t s) {
     auto cost = [](const Job &jb) { return (int64_t)jb.cut.k_chunk + 2; };
     if (cost(p.job[0]) < cost(p.job[1])) std::swap(p.job[0], p.job[1]);
     const int64_t first = tiles(p.job[0].cut), second = tiles(p.job[1].cut);
-    const int64_t groups = std::min(room(2, 1), first + second);
+    const int64_t groups = std::min(room(2), first + second);
     const int64_t more = first % groups, each = first / groups;
     const int64_t c0 = cost(p.job[0]), c1 = cost(p.job[1]);
     // tiles of the second that a group ends in this time after `firsts` of the first
@@ -1399,14 +1378,14 @@ cudaError_t launch_both(MmaArgs &p, cudaStream_t s) {
     p.more = (int32_t)more;
     p.ahead = more > 0 ? (int32_t)(fits(lo, each) - fits(lo, each + 1)) : 0;
     return p.job[0].cut.bn > 128
-               ? launch_mma<2, 1, 256, false, false, true, kOut, false, true>(p, s)
-               : launch_mma<2, 1, 128, false, false, true, kOut, false, true>(p, s);
+               ? launch_mma<2, 256, false, false, true, kOut, false, true>(p, s)
+               : launch_mma<2, 128, false, false, true, kOut, false, true>(p, s);
 }
 
 // d_hidden of few tokens
 cudaError_t launch_d_hidden_few(const MmaArgs &p, cudaStream_t s) {
-    return p.job[0].cut.bn == 32 ? launch_mma<1, 1, 32, true, true, false, kOut, false>(p, s)
-                                 : launch_mma<1, 1, 128, true, true, false, kOut, false>(p, s);
+    return p.job[0].cut.bn == 32 ? launch_mma<1, 32, true, true, false, kOut, false>(p, s)
+                                 : launch_mma<1, 128, true, true, false, kOut, false>(p, s);
 }
 
 constexpr int64_t kFew = 128;  // tokens that SWAP takes
@@ -1415,14 +1394,8 @@ constexpr int64_t kFew = 128;  // tokens that SWAP takes
 // rows are cut so that every SM has the same number of tiles, none more than
 // 128 rows (50257 rows by 128 leave the third wave of tiles 58% full, by 112
 // 95%).
-// Two pairs to a cluster where rows do not start on lines of 128 bytes: a box's
-// rows then touch two lines each, and what L2 gives bounds the product (3001 x
-// 32003 x 1032: 139 us with single pairs, 134 with two; 8192 x 50257 x 1032: 546
-// and 492).  Where they do, the 8 more SMs of single pairs tell (8192 x 50257
-// x 1024: 510 us and 521).
 Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
     Cut c{};
-    c.pairs = 1;
     c.k_tiles = c.k_chunk = (int32_t)ceil_div(dim, kBK);
     c.splits = 1;
     c.swap = tokens <= kFew;
@@ -1437,13 +1410,12 @@ Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
         c.cg = 2;
         c.tile_m = 128;
         c.m_tiles = (int32_t)ceil_div(tokens, 256);
-        c.pairs = c.m_tiles > 1 && dim % 64 != 0 ? 2 : 1;
         // columns of a tile: what leaves the last wave of tiles fullest, a tile
         // costing as much as 24 columns beside its own
         int64_t best = 0;
         for (int bn = 256; bn >= 128; bn -= 32) {
-            const int64_t tiles = ceil_div(c.m_tiles, c.pairs) * ceil_div(words, bn);
-            const int64_t x = ceil_div(tiles, room(2, c.pairs)) * (bn + 24);
+            const int64_t tiles = c.m_tiles * ceil_div(words, bn);
+            const int64_t x = ceil_div(tiles, room(2)) * (bn + 24);
             if (best == 0 || x < best) {
                 best = x;
                 c.bn = bn;
@@ -1460,7 +1432,6 @@ Cut cut_logits(int64_t tokens, int64_t words, int64_t dim) {
 Cut cut_out(int64_t m, int64_t n, int64_t k, bool swap, int64_t tokens) {
     Cut c{};
     c.swap = swap;
-    c.pairs = 1;
     c.cg = swap ? 1 : 2;
     // the columns in equal tiles of up to 256, in steps of 32
     c.bn = swap ? (tokens <= 32 ? 32 : 128)
@@ -1470,7 +1441,7 @@ Cut cut_out(int64_t m, int64_t n, int64_t k, bool swap, int64_t tokens) {
     c.n_tiles = (int32_t)ceil_div(n, c.bn);
     c.k_tiles = (int32_t)ceil_div(k, kBK);
     int64_t splits = 1;
-    const int64_t tiles = (int64_t)c.m_tiles * c.n_tiles, at_a_time = room(c.cg, 1);
+    const int64_t tiles = (int64_t)c.m_tiles * c.n_tiles, at_a_time = room(c.cg);
     if (tiles * 2 <= at_a_time)
         splits = std::max<int64_t>(1, std::min<int64_t>(at_a_time / tiles, c.k_tiles / 4));
     c.k_chunk = (int32_t)ceil_div(c.k_tiles, splits);
@@ -1567,7 +1538,7 @@ bool logits_job(MmaArgs *m, const HeadArgs &a, const Cut &cut, int64_t w0, int64
     (cut.swap ? jb.a_m : jb.b_n) = (int32_t)w0;
     return make_map(hidden, a.hidden, p.dim, p.tokens, a.hidden_stride, cut.swap ? cut.bn : 128) &&
            make_map(weight, a.weight, p.dim, p.vocab, a.weight_stride,
-                    cut.swap ? cut.tile_m : cut.bn / 2 / cut.pairs);
+                    cut.swap ? cut.tile_m : cut.bn / 2);
 }
 
 }  // namespace

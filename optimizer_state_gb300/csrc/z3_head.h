@@ -19,7 +19,6 @@ constexpr int kHeadMaxList = 1024; // a token's teacher logits
 // depth of a tile into splits.
 struct Cut {
     int32_t cg;        // CTAs to a tile
-    int32_t pairs;     // tiles to a cluster
     int32_t swap;      // rows and columns are exchanged (few tokens)
     int32_t tile_m;    // rows of a CTA's: 128, or with swap fewer
     int32_t bn;        // columns of a tile

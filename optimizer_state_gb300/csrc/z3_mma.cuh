@@ -140,18 +140,6 @@ __device__ __forceinline__ void st_shared(uint32_t at, uint32_t x, uint32_t y, u
                  : "memory");
 }
 
-// The same box into the CTAs of `mask`, for CTA pairs.  Each of them has its
-// bytes counted by the barrier at `bar`'s place in its pair's even CTA.
-__device__ __forceinline__ void tma_load_many(uint32_t dst, const CUtensorMap *map, uint32_t bar,
-                                              int x, int y, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(
-            dst),
-        "l"(map), "r"(bar), "r"(x), "r"(y), "h"(mask)
-        : "memory");
-}
-
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -248,10 +236,10 @@ __device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint3
     }
 }
 
-// The barrier (with CG = 2 that of the CTAs of `mask`) is arrived at once all
-// products issued by this thread so far are done.
+// The barrier (with CG = 2 that of both CTAs) is arrived at once all products
+// issued by this thread so far are done.
 template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t mask) {
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
     if constexpr (CG == 1) {
         asm volatile(
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -261,7 +249,7 @@ __device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t mask) {
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
             ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"(mask)
+            "h"((uint16_t)3)
             : "memory");
     }
 }
