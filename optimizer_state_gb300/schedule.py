@@ -92,6 +92,11 @@ class Head:
         self.vocab, self.dim = shape
         self.tokens, self.ranks = tokens, u.w.n_ranks
         first = u.L.full_off[param]
+        if first % 8 or self.dim % 8:
+            what = (f"starts at element {first}" if first % 8
+                    else f"has rows of {self.dim} elements")
+            raise ValueError(f"parameter {param} of unit {unit} {what}: a head's weight and "
+                             "its rows start on 16 bytes, a multiple of 8 elements")
         self._part = slice(first, first + self.vocab * self.dim)
         rows, dev = (self.ranks, tokens), model.dev
         self._made_on = torch.cuda.current_stream()
@@ -186,8 +191,9 @@ class Model:
 
     def head(self, tokens: int, unit: int = 0, param: int = 0, k: int = 0) -> Head:
         """The loss of `tokens` tokens of every rank over the vocabulary of one
-        parameter, [vocab, dim] (an embedding's where the head is tied to it);
-        k: the length of a teacher's lists, where there is one."""
+        parameter, [vocab, dim] (an embedding's where the head is tied to it),
+        whose dim and place in its unit are multiples of 8 elements; k: the
+        length of a teacher's lists, where there is one."""
         return Head(self, tokens, unit, param, k)
 
     def launches_per_step(self) -> int:
