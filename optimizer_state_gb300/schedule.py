@@ -254,6 +254,15 @@ class Model:
             z3.z3_model_step_clipped(self.unit_args(), clips, full, hp, t, max_norm, self.clip,
                                      self._workspace, stream=stream, gather_stream=gather_stream)
 
+    def _take_loss(self, loss, stream, counted: bool):
+        if loss is None:
+            return
+        try:
+            loss(stream)
+        except Exception:
+            self.t -= counted
+            raise
+
     def _backward(self, i: int, hp: dict, t: int, max_norm, stream):
         """What follows the backward compute of unit i: its update, or in a
         clipped step its reduced gradient and sums of squares."""
@@ -290,7 +299,8 @@ class Model:
         """One training step, scheduled by the library (z3_model_step).
         `loss(stream)` is called where the backward pass begins, such as for a
         Head's call: after the forward gathers of a step with hooks, and before
-        a step that the library schedules as a whole.
+        a step that the library schedules as a whole.  Where it raises, no state
+        has been touched and the step keeps no number.
         With `max_norm` the gradients of all units are clipped to that global
         norm first (z3_model_step_clipped); `clip` then holds [norm, coef] on
         the device, coef NaN where the norm was not finite and the step was
@@ -302,20 +312,19 @@ class Model:
         enqueued, with the transient buffer holding that unit's parameters
         once the stream reaches it -- the point where the forward or backward
         compute of the unit would run."""
-        if t is None:
+        counted = t is None
+        if counted:
             self.t += 1
             t = self.t
         if on_gather is None:
-            if loss is not None:
-                loss(stream)
+            self._take_loss(loss, stream, counted)
             self._library_step([self.full], hp, t, max_norm, stream)
             return
         for i, u in enumerate(self.units):            # forward
             if u.resident is None:
                 z3.z3_allgather(u.L, u.shards, self.full, stream=stream)
             on_gather("forward", i)
-        if loss is not None:
-            loss(stream)
+        self._take_loss(loss, stream, counted)
         for i in range(len(self.units) - 1, -1, -1):    # backward, reverse order
             u = self.units[i]
             if u.resident is None:
@@ -359,12 +368,12 @@ class PrefetchModel(Model):
 
     def step(self, hp: dict, stream=None, t: int | None = None, on_gather=None,
              max_norm: float | None = None, loss=None):
-        if t is None:
+        counted = t is None
+        if counted:
             self.t += 1
             t = self.t
         if on_gather is None:
-            if loss is not None:
-                loss(stream)
+            self._take_loss(loss, stream, counted)
             self._library_step(self.bufs, hp, t, max_norm, stream, self.gstream)
             return
         if self.depth != 1:
@@ -379,9 +388,8 @@ class PrefetchModel(Model):
                 z3.z3_allgather(u.L, u.shards, self.bufs[i % 2], stream=g.cuda_stream)
             with torch.cuda.stream(g):
                 on_gather("forward", i)
-        if loss is not None:
-            with torch.cuda.stream(g):
-                loss(g)
+        with torch.cuda.stream(g):
+            self._take_loss(loss, g, counted)
         order = list(range(n - 1, -1, -1))
         gathered = {}
 
