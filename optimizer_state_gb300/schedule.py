@@ -99,7 +99,8 @@ class Head:
                              "its rows start on 16 bytes, a multiple of 8 elements")
         self._part = slice(first, first + self.vocab * self.dim)
         rows, dev = (self.ranks, tokens), model.dev
-        self._made_on = torch.cuda.current_stream()
+        self._home = torch.cuda.current_stream()   # where the buffers are allocated
+        self._waited, self._seen = False, {self._home.cuda_stream}
         self.loss = torch.empty(rows, dtype=torch.float32, device=dev)
         self.lse = torch.empty(rows, dtype=torch.float32, device=dev)
         self.total = torch.empty(2, dtype=torch.float32, device=dev)
@@ -154,16 +155,24 @@ class Head:
     def _await(self, stream):
         """The first call on another stream than the one that the buffers were
         allocated on waits for that one; a captured call, which cannot wait for
-        what is outside its capture, leaves it to the next."""
-        if self._made_on is None:
-            return
+        what is outside its capture, leaves it to the next.  And the allocator
+        hears of each torch stream that uses them, so that a head may go while
+        its calls still run.  A raw handle's stream may be gone by then: who gives
+        one keeps the head until the calls have ended, as for a graph that holds
+        them."""
         s = _torch_stream(stream)
-        if s.cuda_stream != self._made_on.cuda_stream:
+        if s.cuda_stream not in self._seen and not isinstance(stream, int):
+            for x in (self.loss, self.lse, self.total, self.d_hidden, self._workspace):
+                x.record_stream(s)
+            self._seen.add(s.cuda_stream)
+        if self._waited:
+            return
+        if s.cuda_stream != self._home.cuda_stream:
             with torch.cuda.stream(s):
                 if torch.cuda.is_current_stream_capturing():
                     return
-            s.wait_stream(self._made_on)
-        self._made_on = None
+            s.wait_stream(self._home)
+        self._waited = True
 
 
 class Model:
