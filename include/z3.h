@@ -425,14 +425,15 @@ z3_status z3_model_step_clipped(const z3_unit *units, const z3_clip_unit *clips,
  * are NaN; so has one whose target, or a listed word with q > 0, has a logit of
  * -Inf.  Another word's logit of -Inf is a probability of 0.
  *
- * dim is a multiple of 8, at most 2^31 - 1024 as are tokens and vocab (a call
- * of 0 tokens writes total = {0, 0}, and zeros to d_weight); strides are in
+ * dim is a multiple of 8, at most 2^25, tokens and vocab at most 2^31 - 1024 (a
+ * call of 0 tokens writes total = {0, 0}, and zeros to d_weight); strides are in
  * elements, >= dim and multiples of 8.  hidden, weight, d_hidden, d_weight and
  * the workspace start on a 16-byte boundary, the other buffers on one of their
- * elements.  Errors: sizes out of these ranges, a NULL buffer, a workspace
- * that is too small, an output or the workspace overlapping another buffer of
- * the call, scale not finite (INVALID_ARG); strides, boundaries (ALIGNMENT);
- * sizes whose workspace no memory holds (OVERFLOW). */
+ * elements.  Errors: a size below its range or a dim that is no multiple of 8, a
+ * NULL buffer, a workspace that is too small, an output or the workspace
+ * overlapping another buffer of the call, scale not finite (INVALID_ARG); strides,
+ * boundaries (ALIGNMENT); sizes beyond these, or whose workspace no memory holds
+ * (OVERFLOW). */
 typedef struct z3_head {
     const uint16_t *hidden; /* bf16 [tokens][hidden_stride] */
     int64_t hidden_stride;

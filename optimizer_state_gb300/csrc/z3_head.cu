@@ -1551,7 +1551,7 @@ bool head_plan(int64_t tokens, int64_t dim, int64_t vocab, int64_t k, bool grads
     p->k = k;
     // tiles and rows are counted in 32 bits, bytes in 64
     constexpr int64_t kMost = (1ll << 31) - 1024;
-    if (tokens > kMost || vocab > kMost || dim > kMost) return false;
+    if (tokens > kMost || vocab > kMost || dim > kHeadMaxDim) return false;
     int64_t probe;
     if (__builtin_mul_overflow(tokens, vocab, &probe) ||
         __builtin_mul_overflow(std::max(tokens, vocab), dim, &probe) || probe > (1ll << 56) ||

@@ -14,6 +14,9 @@ namespace z3 {
 
 constexpr int kHeadSMs = 152;      // of a GB300
 constexpr int kHeadMaxList = 1024; // a token's teacher logits
+// Values of a row.  A tile of logits sums whole rows, 64 values in 1,400 clocks
+// where they come from memory: 7.4e8 clocks at most, of the 4e9 that a wait takes.
+constexpr int64_t kHeadMaxDim = 1ll << 25;
 
 // A grid of products: how a [M][N] result of depth K is cut into tiles, and the
 // depth of a tile into splits.
