@@ -129,26 +129,41 @@ __device__ __forceinline__ int64_t load_index(const void *p, int bytes, int64_t 
                       : (int64_t)static_cast<const int32_t *>(p)[i];
 }
 
-// The part of a row's dot product that one of `lanes` threads sums: products of
-// bf16 are exact, their sums rounded to nearest.
-__device__ __forceinline__ float dot_part(const uint16_t *x, const uint16_t *y, int64_t dim,
-                                          int lane, int lanes) {
-    float s[8] = {};
-#pragma unroll 8
-    for (int64_t i = lane * 8; i < dim; i += lanes * 8) {
-        float a[8], b[8];
-        unpack8(ld8b(x + i), a);
-        unpack8(ld8b(y + i), b);
+// The logit of a token's target, by LANES neighbours of a warp.  Products of bf16
+// are exact, their sums rounded to nearest, in the same order for every LANES: 256
+// chains, eight to each of 32 places, joined by a tree.  So the loss, the gradient
+// and lse between them are of one logit.
+template <int LANES>
+__device__ __forceinline__ float target_logit(const uint16_t *x, const uint16_t *y, int64_t dim,
+                                              int lane) {
+    constexpr int kPlaces = 32 / LANES;  // of a lane: every LANES-th
+    float s[kPlaces][8] = {};
+#pragma unroll LANES / 4
+    for (int64_t i = lane % LANES * 8; i < dim; i += 256) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = __fmaf_rn(a[j], b[j], s[j]);
+        for (int n = 0; n < kPlaces; ++n) {
+            const int64_t at = i + n * LANES * 8;
+            if (at >= dim) break;
+            float a[8], b[8];
+            unpack8(ld8b(x + at), a);
+            unpack8(ld8b(y + at), b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[n][j] = __fmaf_rn(a[j], b[j], s[n][j]);
+        }
     }
-    return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
+    float z[kPlaces];
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(~0u, x, o);
-    return x;
+    for (int n = 0; n < kPlaces; ++n)
+        z[n] = ((s[n][0] + s[n][1]) + (s[n][2] + s[n][3])) +
+               ((s[n][4] + s[n][5]) + (s[n][6] + s[n][7]));
+#pragma unroll
+    for (int o = kPlaces / 2; o > 0; o /= 2)  // places 16 lanes apart, then 8
+#pragma unroll
+        for (int n = 0; n < o; ++n) z[n] += z[n + o];
+    const unsigned lanes = LANES == 32 ? ~0u : (0xffu << (lane & 24));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o /= 2) z[0] += __shfl_xor_sync(lanes, z[0], o);
+    return z[0];
 }
 
 template <int BN, int CG>
@@ -486,14 +501,10 @@ k_head_mma(const __grid_constant__ MmaArgs p) {
             const int64_t t = t0 + lane / 8;
             int64_t w = -1;
             if (t < tokens) w = load_index(p.targets, p.target_bytes, t);
-            float z = 0.0f;
-            const bool counts = w >= 0 && w < p.vocab;
-            if (counts)
-                z = dot_part(p.hidden + t * p.hidden_stride, p.weight + w * p.weight_stride, p.dim,
-                             lane % 8, 8);
-#pragma unroll
-            for (int o = 4; o > 0; o /= 2) z += __shfl_xor_sync(~0u, z, o);
-            if (counts && lane % 8 == 0) p.z[t] = z;
+            if (w < 0 || w >= p.vocab) continue;
+            const float z = target_logit<8>(p.hidden + t * p.hidden_stride,
+                                            p.weight + w * p.weight_stride, p.dim, lane);
+            if (lane % 8 == 0) p.z[t] = z;
         }
     } else if (KIND == kOut && !SWAP && (warp == 2 || warp == 3)) {
         // few tokens' d_hidden, beside the tiles of d_weight
@@ -1155,8 +1166,9 @@ struct FactorArgs {
 };
 
 // Each token's factor a = scale w / total[1] (times the temperature), its lse in
-// powers of two and, with a target, dz there: a (exp(z - lse) - 1) of a logit
-// that is summed with rounding, as in the forward call.  And the hidden states
+// powers of two and, with a target, dz there: a (exp(z - lse) - 1) of the very
+// logit that lse was made with, which leaves lse's own rounding as the error of a
+// likely target's small dz.  And the hidden states
 // with zeros in the rows left out: what stands there may be anything, and 0 *
 // NaN would reach d_weight.  The copy costs 4 bytes a value, the targets' rows
 // of the weight 2 more: 10 us of the 2.1 ms at 8192 x 1024.
@@ -1180,7 +1192,7 @@ __global__ void __launch_bounds__(128) k_head_factors(const FactorArgs a) {
     const uint16_t *row = a.hidden + t * a.stride;
     float z = lse;
     if (a.row.k == 0 && state == kCounts)
-        z = warp_sum(dot_part(row, a.weight + word * a.weight_stride, a.row.dim, lane, 32));
+        z = target_logit<32>(row, a.weight + word * a.weight_stride, a.row.dim, lane);
     if (lane == 0) {
         a.factor[t] = make_float2(f, __fmul_rn(lse, kLog2e));
         if (a.row.k == 0) {
