@@ -313,7 +313,7 @@ __device__ __forceinline__ void put64(uint32_t stage, int lane, const uint32_t (
 // Bound by the tensor cores: 256 x 256 values of one k tile take 528 clocks, 512
 // at their nominal rate.  6 stages of 64 values of K hide L2's latency; the
 // epilogue takes 2,800 clocks a tile beside the next one's products (8,450 at
-// depth 1024), whose issue it slows by 5%.  4608 x 32768 x 1024: 168 us, 1.84
+// depth 1024), which it slows by 7%.  4608 x 32768 x 1024: 168 us, 1.84
 // PFLOP/s; in long calls the power limit sets the clocks.
 // Every wait ends (mbar_wait); an epilogue whose tile did not come takes NaN for
 // its values.

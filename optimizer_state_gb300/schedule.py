@@ -79,7 +79,8 @@ class Head:
     loss of every rank's tokens against the gathered copy in one forward pass,
     and each rank's gradients: that of the weight into the parameter's part of
     the rank's row of the unit's gradients, that of the hidden states into
-    `d_hidden`.  They are the gradients of the mean over all ranks' tokens that
+    `d_hidden`.  Both are written: what else adds to the weight's gradient, such
+    as a tied embedding's look-ups, is added after the call.  They are the gradients of the mean over all ranks' tokens that
     count, times the number of ranks: the step's reduction divides by it."""
 
     def __init__(self, model: Model, tokens: int, unit: int = 0, param: int = 0, k: int = 0):
